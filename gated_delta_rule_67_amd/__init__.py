@@ -38,13 +38,16 @@ __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_varlen", "kda_chunk_bwd",
            "kda_chunk_bwd_varlen", "kda_recurrent_step",
            "kda_recurrent_step_slots", "kda_gate_fwd", "kda_gate_bwd",
            "kda_chunk_fwd_gated", "kda_recurrent_step_gated", "kda_chunk_fwd_segmented",
-           "kda_chunk_fwd_noalloc", "NOALLOC_SCRATCH_BYTES", "library", "library_path", "status_string",
+           "kda_chunk_fwd_noalloc",
+           "kda_conv_fwd", "kda_conv_bwd", "kda_conv_step", "kda_slots_copy",
+           "kda_slots_compact", "NOALLOC_SCRATCH_BYTES", "library", "library_path", "status_string",
            "KDA_OK", "KDA_ERR_INVALID", "KDA_ERR_UNSUPPORTED", "KDA_ERR_HIP", "KDA_ERR_SCRATCH",
            "KDA_FLAG_QK_L2NORM", "KDA_FLAG_BETA_SIGMOID"]
 
 KDA_OK, KDA_ERR_INVALID, KDA_ERR_UNSUPPORTED, KDA_ERR_HIP, KDA_ERR_SCRATCH = 0, -1, -2, -3, -4
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES
 KDA_FLAG_QK_L2NORM, KDA_FLAG_BETA_SIGMOID = 1, 2
+KDA_CONV_SILU, KDA_ZERO_REST = 1, 2
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
@@ -112,6 +115,22 @@ def library():
     lib.kda_stream_copy.restype = i
     lib.kda_status_string.argtypes = [i]
     lib.kda_status_string.restype = ctypes.c_char_p
+    i64 = ctypes.c_int64
+    lib.kda_conv_fwd.argtypes = [vp, i64] + [vp] * 4 + [i] + [vp] * 2 + [i] * 5 + [vp]
+    lib.kda_conv_fwd.restype = i
+    lib.kda_conv_bwd_workspace_size.argtypes = [i] * 4
+    lib.kda_conv_bwd_workspace_size.restype = sz
+    lib.kda_conv_bwd.argtypes = ([vp, i64] + [vp] * 4 + [i, vp, i64] + [vp] * 5 + [i] * 5
+                                 + [vp, sz, vp])
+    lib.kda_conv_bwd.restype = i
+    lib.kda_conv_step.argtypes = [vp, i64] + [vp] * 4 + [i, vp] + [i] * 5 + [vp]
+    lib.kda_conv_step.restype = i
+    lib.kda_slots_copy.argtypes = [vp] * 2 + [i, i] + [vp] * 2 + [i, vp]
+    lib.kda_slots_copy.restype = i
+    lib.kda_slots_compact_workspace_size.argtypes = [i]
+    lib.kda_slots_compact_workspace_size.restype = sz
+    lib.kda_slots_compact.argtypes = [vp] * 2 + [i, i] + [vp] * 4 + [sz, vp]
+    lib.kda_slots_compact.restype = i
     lib.kda_version.argtypes = []
     lib.kda_version.restype = ctypes.c_char_p
     _lib = lib
@@ -591,6 +610,208 @@ def kda_chunk_fwd_noalloc(q, k, v, g, beta, o, final_state=None, scale=None, ini
                                        _flags(qk_l2norm, beta_sigmoid), ctypes.c_void_p(stream))
     _check(rc)
     return o
+
+
+def _call(dev, fn, *args):
+    """fn(*args, stream) on dev's current stream with dev current; raises unless KDA_OK."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, stream))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _token_stride(name, t, lead):
+    """Elements between the tokens of t, whose first `lead` dimensions are tokens in order (one, or
+    batch and token) and whose others are dense: t may be a slice of a wider activation."""
+    width = 1
+    for size, stride in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
+        _require(size == 1 or stride == width, f"{name} must be dense in its last dimensions")
+        width *= size
+    step = None
+    for size, stride in zip(reversed(t.shape[:lead]), reversed(t.stride()[:lead])):
+        if size > 1:
+            _require(step is None or stride == step * tokens,
+                     f"{name} must hold its tokens at one stride")
+            step, tokens = (stride, size) if step is None else (step, tokens * size)
+    _require(step is None or step >= width, f"{name} must not overlap itself")
+    return width if step is None else step
+
+
+def _check_params(named, dev):
+    for name, t, shape in named:
+        if t is not None:
+            _require(t.device == dev and t.dtype == torch.float32 and t.is_contiguous()
+                     and tuple(t.shape) == shape, f"{name} must be float32 {list(shape)} on {dev}")
+
+
+def _sequences(x, cu_seqlens):
+    """(token dimensions of x, sequences N, tokens T) of a dense batch [B, T, ...] or, with
+    cu_seqlens, of packed tokens [T, ...] or [1, T, ...]."""
+    if cu_seqlens is None:
+        return 2, x.shape[0], x.shape[0] * x.shape[1]
+    _require(cu_seqlens.device == x.device and cu_seqlens.dtype == torch.int32
+             and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous() and cu_seqlens.numel() >= 2,
+             "cu_seqlens must be a contiguous int32 vector of at least two offsets on the same GPU")
+    return None, cu_seqlens.numel() - 1, None
+
+
+def _conv_flags(silu):
+    return (KDA_CONV_SILU if silu else 0) | KDA_ZERO_REST
+
+
+def _conv_args(x, weight, bias, states, cu_seqlens, others):
+    _require(x.is_cuda, "inputs must be on a GPU")
+    _require(x.dtype in _DTYPE, f"unsupported dtype {x.dtype}")
+    dev, dt = x.device, x.dtype
+    _, N, T = _sequences(x, cu_seqlens)
+    if cu_seqlens is None:
+        _require(x.dim() == 3, "x must be [B, T, D] (packed sequences: give cu_seqlens)")
+    else:
+        _require(x.dim() == 2 or (x.dim() == 3 and x.shape[0] == 1), "packed x must be [T, D] or [1, T, D]")
+        T = x.shape[-2]
+    D, lead = x.shape[-1], x.dim() - 1
+    _require(weight.dim() == 2 and weight.shape[0] == D, "weight must be [D, W]")
+    W = weight.shape[1]
+    _require(D >= 1 and N >= 1, "x must have at least one sequence and one channel")
+    _check_params([("weight", weight, (D, W)), ("bias", bias, (D,))], dev)
+    for name, t in states:
+        if t is not None:
+            _require(tuple(t.shape) == (N, W - 1, D), f"{name} must be [N, W-1, D]")
+            _check_tensors([(name, t)], dt, dev)
+    strides = []
+    for name, t in [("x", x)] + others:
+        _require(t.shape == x.shape and t.dtype == dt and t.device == dev, f"{name} must match x")
+        strides.append(_token_stride(name, t, lead))
+    return dev, dt, N, T, D, W, strides
+
+
+def kda_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, silu=True,
+                 output_final_state=True):
+    """Short causal depthwise convolution of each sequence, then SiLU (unless silu=False):
+    y_t[d] = silu(bias[d] + sum_w weight[d, w] x_{t-(W-1)+w}[d]). x [B,T,D], or packed [T,D] /
+    [1,T,D] with cu_seqlens int32 [N+1] (float32 or bf16; its rows may lie in a wider
+    activation); weight [D,W] (W = 2..4) and bias [D] float32; initial_state [N,W-1,D] like x:
+    the rows before each sequence (None: zeros). Returns (y shaped like x, final_state
+    [N,W-1,D] or None); y rows in no packed sequence are zero."""
+    dev, dt, N, T, D, W, (ldx,) = _conv_args(x, weight, bias, [("initial_state", initial_state)],
+                                             cu_seqlens, [])
+    lib = library()
+    y = torch.empty(x.shape, dtype=dt, device=dev)
+    final = torch.empty((N, W - 1, D), dtype=dt, device=dev) if output_final_state else None
+    _call(dev, lib.kda_conv_fwd, x.data_ptr(), ldx, weight.data_ptr(), _addr(bias),
+          _addr(initial_state), _addr(cu_seqlens), N, _addr(final), y.data_ptr(), T, D, W,
+          _conv_flags(silu), _DTYPE[dt])
+    return y, final
+
+
+def kda_conv_bwd(x, weight, dy, bias=None, initial_state=None, dfinal_state=None, cu_seqlens=None,
+                 silu=True):
+    """Gradients of <y, dy> + <final_state, dfinal_state> for kda_conv_fwd's inputs. dy like y;
+    dfinal_state [N,W-1,D] like x or None. Returns (dx like x, dweight [D,W] and dbias [D]
+    float32, dinitial_state [N,W-1,D]); the last two are None where bias / initial_state is, and
+    dx rows in no packed sequence are zero."""
+    dev, dt, N, T, D, W, (ldx, lddy) = _conv_args(
+        x, weight, bias, [("initial_state", initial_state), ("dfinal_state", dfinal_state)],
+        cu_seqlens, [("dy", dy)])
+    lib = library()
+    dx = torch.empty(x.shape, dtype=dt, device=dev)
+    dweight = torch.empty((D, W), dtype=torch.float32, device=dev)
+    dbias = None if bias is None else torch.empty((D,), dtype=torch.float32, device=dev)
+    dinit = None if initial_state is None else torch.empty((N, W - 1, D), dtype=dt, device=dev)
+    ws_bytes = lib.kda_conv_bwd_workspace_size(T, D, W, _DTYPE[dt])
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    _call(dev, lib.kda_conv_bwd, x.data_ptr(), ldx, weight.data_ptr(), _addr(bias),
+          _addr(initial_state), _addr(cu_seqlens), N, dy.data_ptr(), lddy, _addr(dfinal_state),
+          dx.data_ptr(), dweight.data_ptr(), _addr(dbias), _addr(dinit), T, D, W, _conv_flags(silu),
+          _DTYPE[dt], _addr(ws), ws_bytes)
+    return dx, dweight, dbias, dinit
+
+
+def _check_slots(slots, B, num_slots, dev):
+    if slots is None:
+        _require(num_slots >= B, "without slots the pool needs a state per request")
+    else:
+        _require(slots.device == dev and slots.dtype == torch.int32 and tuple(slots.shape) == (B,)
+                 and slots.is_contiguous(), "slots must be int32 [B] on the GPU")
+
+
+def kda_conv_step(x, weight, state_pool, bias=None, slots=None, silu=True):
+    """One token of kda_conv_fwd per request. x [B,D]; state_pool [num_slots,W-1,D] like x, moved
+    on by one row in place; slots int32 [B] (a slot outside [0, num_slots) gives y = 0 and no
+    update), or None: request n uses slot n. Returns y [B,D]."""
+    _require(x.is_cuda, "inputs must be on a GPU")
+    dev, dt = x.device, x.dtype
+    _require(dt in _DTYPE, f"unsupported dtype {dt}")
+    _require(x.dim() == 2 and x.numel() > 0, "x must be [B, D]")
+    B, D = x.shape
+    _require(weight.dim() == 2 and weight.shape[0] == D, "weight must be [D, W]")
+    W = weight.shape[1]
+    _check_params([("weight", weight, (D, W)), ("bias", bias, (D,))], dev)
+    _require(state_pool.dim() == 3 and tuple(state_pool.shape[1:]) == (W - 1, D),
+             "state_pool must be [num_slots, W-1, D]")
+    _check_tensors([("state_pool", state_pool)], dt, dev)
+    _check_slots(slots, B, state_pool.shape[0], dev)
+    y = torch.empty((B, D), dtype=dt, device=dev)
+    _call(dev, library().kda_conv_step, x.data_ptr(), _token_stride("x", x, 1), weight.data_ptr(),
+          _addr(bias), state_pool.data_ptr(), _addr(slots), state_pool.shape[0], y.data_ptr(), B,
+          D, W, _conv_flags(silu), _DTYPE[dt])
+    return y
+
+
+def _pools(pools):
+    """(device, host arrays of addresses and slot sizes, count, num_slots) of one pool or several."""
+    pools = [pools] if isinstance(pools, torch.Tensor) else list(pools)
+    _require(len(pools) > 0, "at least one pool is needed")
+    dev, num_slots = pools[0].device, pools[0].shape[0] if pools[0].dim() else 0
+    spans = []
+    for p in pools:
+        _require(p.is_cuda and p.device == dev, "pools must be on one GPU")
+        _require(p.dim() >= 1 and p.shape[0] == num_slots and p.numel() > 0,
+                 "pools must be [num_slots, ...] with the same num_slots >= 1")
+        _require(p.is_contiguous(), "pools must be contiguous")
+        spans.append((p.data_ptr(), p.numel() * p.element_size()))
+    order = sorted(spans)
+    _require(all(a + n <= b for (a, n), (b, _) in zip(order, order[1:])), "pools must not overlap")
+    n = len(spans)
+    return (dev, (ctypes.c_void_p * n)(*[a for a, _ in spans]),
+            (ctypes.c_size_t * n)(*[size // num_slots for _, size in spans]), n, num_slots)
+
+
+def kda_slots_copy(pools, src, dst):
+    """Copies slots within every pool, in place: pair by pair, in order, slot dst[i] becomes slot
+    src[i] (a fork), or zeros where src[i] < 0 (a cleared slot). pools: a tensor [num_slots, ...]
+    or a list of them (a model's layers; any dtype); src, dst int32 [n] on the GPU; pairs with dst
+    outside [0, num_slots) or src >= num_slots do nothing."""
+    dev, base, size, n, num_slots = _pools(pools)
+    for name, t in (("src", src), ("dst", dst)):
+        _require(t.device == dev and t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous()
+                 and t.shape == src.shape, f"{name} must be int32 [n] on the pools' GPU")
+    _call(dev, library().kda_slots_copy, base, size, n, num_slots, src.data_ptr(), dst.data_ptr(),
+          src.numel())
+
+
+def kda_slots_compact(pools, live):
+    """Moves the live slots of every pool to its front, in place: with c live slots, those at or
+    behind slot c move, in order, into the free slots in front of it. pools: as kda_slots_copy;
+    live: bool (or uint8) [num_slots] on the GPU. Returns (new_slot int32 [num_slots]: where a
+    slot's state lives now, -1 for a free one; count int32 [1])."""
+    dev, base, size, n, num_slots = _pools(pools)
+    _require(live.device == dev and live.dtype in (torch.bool, torch.uint8) and live.is_contiguous()
+             and tuple(live.shape) == (num_slots,), "live must be bool [num_slots] on the pools' GPU")
+    lib = library()
+    new_slot = torch.empty((num_slots,), dtype=torch.int32, device=dev)
+    count = torch.empty((1,), dtype=torch.int32, device=dev)
+    ws_bytes = lib.kda_slots_compact_workspace_size(num_slots)
+    ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+    _call(dev, lib.kda_slots_compact, base, size, n, num_slots, live.data_ptr(),
+          new_slot.data_ptr(), count.data_ptr(), ws.data_ptr(), ws_bytes)
+    return new_slot, count
 
 
 def stream_copy(src, dst):

@@ -40,6 +40,17 @@ hipError_t launch_gate_bwd(const void* x, const float* A_log, const float* dt_bi
                            const void* dg, void* dx, float* dA_log, float* ddt_bias,
                            int64_t rows, int HV, int K, float lower_bound, bool bf,
                            void* workspace, hipStream_t stream);
+hipError_t launch_conv_fwd(const ConvArgs& p, hipStream_t stream);
+hipError_t launch_conv_bwd(const ConvArgs& p, const void* dy, int64_t lddy, const void* dfinal,
+                           float* dweight, float* dbias, void* workspace, hipStream_t stream);
+hipError_t launch_conv_step(const ConvArgs& p, const ConvStep& st, hipStream_t stream);
+size_t conv_bwd_workspace_bytes(int T, int D, int W, bool bf);
+hipError_t launch_slots_copy(void* const* pools, const size_t* slot_bytes, int npools, int nslots,
+                             const int* src, const int* dst, int n, hipStream_t stream);
+size_t slots_compact_workspace_bytes(int nslots);
+hipError_t launch_slots_compact(void* const* pools, const size_t* slot_bytes, int npools, int nslots,
+                                const uint8_t* live, int* new_slot, int* count, void* workspace,
+                                hipStream_t stream);
 }  // namespace kda
 
 namespace {
@@ -504,6 +515,112 @@ int kda_chunk_fwd_noalloc(const void* q, const void* k, const void* v, const voi
   return chunk_fwd(q, k, v, g, beta, initial_state, final_state, o, B, T, H, HV, K, V, scale,
                    chunk_size, dtype, ws, ws ? (size_t)KDA_NOALLOC_SCRATCH_BYTES : 0, flags,
                    nullptr, nullptr, 0.f, segments, stream);
+}
+
+// ---- Short causal convolution
+
+// Sequences and token strides the convolution and the scan accept: N >= 1 sequences over T >= 0
+// tokens, equal ones unless offsets are given.
+static bool valid_sequences(int N, int T, const int* cu_seqlens) {
+  return N >= 1 && T >= 0 && (cu_seqlens || T % N == 0);
+}
+
+static int check_conv(int N, int T, int D, int W, const int* cu_seqlens, unsigned flags, int dtype) {
+  if (flags & ~(unsigned)(KDA_CONV_SILU | KDA_ZERO_REST)) return KDA_ERR_INVALID;
+  if (!valid_sequences(N, T, cu_seqlens) || !positive(D)) return KDA_ERR_INVALID;
+  if (dtype != KDA_DTYPE_F32 && dtype != KDA_DTYPE_BF16) return KDA_ERR_INVALID;
+  if (W < 2 || W > 4 || D > (1 << 20) || N > (1 << 17)) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+int kda_conv_fwd(const void* x, int64_t x_stride, const float* weight, const float* bias,
+                 const void* initial_state, const int* cu_seqlens, int N, void* final_state,
+                 void* y, int T, int D, int W, unsigned flags, int dtype, void* stream) {
+  const int rc = check_conv(N, T, D, W, cu_seqlens, flags, dtype);
+  if (rc != KDA_OK) return rc;
+  if (!weight || (T > 0 && (!x || !y)) || (T > 1 && x_stride < D)) return KDA_ERR_INVALID;
+  const kda::ConvArgs a{x, x_stride, weight, bias, initial_state, cu_seqlens, N, T, D, W, (flags & KDA_CONV_SILU) != 0,
+                        (flags & KDA_ZERO_REST) != 0, dtype == KDA_DTYPE_BF16, y, final_state};
+  return kda::launch_conv_fwd(a, static_cast<hipStream_t>(stream)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+size_t kda_conv_bwd_workspace_size(int T, int D, int W, int dtype) {
+  if (check_conv(1, T, D, W, nullptr, 0u, dtype) != KDA_OK) return 0;
+  return kda::conv_bwd_workspace_bytes(T, D, W, dtype == KDA_DTYPE_BF16);
+}
+
+int kda_conv_bwd(const void* x, int64_t x_stride, const float* weight, const float* bias,
+                 const void* initial_state, const int* cu_seqlens, int N, const void* dy,
+                 int64_t dy_stride, const void* dfinal_state, void* dx, float* dweight,
+                 float* dbias, void* dinitial_state, int T, int D, int W, unsigned flags, int dtype,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_conv(N, T, D, W, cu_seqlens, flags, dtype);
+  if (rc != KDA_OK) return rc;
+  if (!weight || (T > 0 && (!x || !dy || !dx))) return KDA_ERR_INVALID;
+  if (T > 1 && (x_stride < D || dy_stride < D)) return KDA_ERR_INVALID;
+  const size_t need = kda_conv_bwd_workspace_size(T, D, W, dtype);
+  if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return KDA_ERR_INVALID;
+  const kda::ConvArgs a{x, x_stride, weight, bias, initial_state, cu_seqlens, N, T, D, W, (flags & KDA_CONV_SILU) != 0,
+                        (flags & KDA_ZERO_REST) != 0, dtype == KDA_DTYPE_BF16, dx, dinitial_state};
+  const hipError_t e = kda::launch_conv_bwd(a, dy, dy_stride, dfinal_state, dweight, dbias, workspace,
+                                            static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+int kda_conv_step(const void* x, int64_t x_stride, const float* weight, const float* bias,
+                  void* state_pool, const int* slots, int num_slots, void* y, int B, int D, int W,
+                  unsigned flags, int dtype, void* stream) {
+  const int rc = check_conv(1, 0, D, W, nullptr, flags, dtype);
+  if (rc != KDA_OK) return rc;
+  if (!positive(B) || num_slots < 1 || (!slots && num_slots < B)) return KDA_ERR_INVALID;
+  if (!x || !weight || !state_pool || !y || (B > 1 && x_stride < D)) return KDA_ERR_INVALID;
+  if (B > 65535) return KDA_ERR_UNSUPPORTED;
+  kda::ConvArgs a{};
+  a.x = x, a.ldx = x_stride, a.weight = weight, a.bias = bias, a.out = y;
+  a.D = D, a.W = W, a.silu = (flags & KDA_CONV_SILU) != 0, a.bf = dtype == KDA_DTYPE_BF16;
+  const kda::ConvStep st{state_pool, slots, num_slots, B};
+  return kda::launch_conv_step(a, st, static_cast<hipStream_t>(stream)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+// ---- Slots of state pools
+
+static int check_pools(void* const* pools, const size_t* slot_bytes, int num_pools, int num_slots) {
+  if (num_pools < 0 || num_slots < 1 || (num_pools > 0 && (!pools || !slot_bytes))) return KDA_ERR_INVALID;
+  for (int i = 0; i < num_pools; ++i)
+    if (!pools[i] || slot_bytes[i] < 1) return KDA_ERR_INVALID;
+  if (num_slots > (1 << 18)) return KDA_ERR_UNSUPPORTED;
+  for (int i = 0; i < num_pools; ++i)
+    if (slot_bytes[i] > ((size_t)1 << 40)) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+int kda_slots_copy(void* const* pools, const size_t* slot_bytes, int num_pools, int num_slots,
+                   const int* src, const int* dst, int n, void* stream) {
+  const int rc = check_pools(pools, slot_bytes, num_pools, num_slots);
+  if (rc != KDA_OK) return rc;
+  if (n < 0 || (n > 0 && (!src || !dst))) return KDA_ERR_INVALID;
+  if (n == 0 || num_pools == 0) return KDA_OK;
+  const hipError_t e = kda::launch_slots_copy(pools, slot_bytes, num_pools, num_slots, src, dst, n,
+                                              static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+size_t kda_slots_compact_workspace_size(int num_slots) {
+  return num_slots < 1 || num_slots > (1 << 18) ? 0 : kda::slots_compact_workspace_bytes(num_slots);
+}
+
+int kda_slots_compact(void* const* pools, const size_t* slot_bytes, int num_pools, int num_slots,
+                      const unsigned char* live, int* new_slot, int* count, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  const int rc = check_pools(pools, slot_bytes, num_pools, num_slots);
+  if (rc != KDA_OK) return rc;
+  if (!live || !new_slot || !count) return KDA_ERR_INVALID;
+  if (!workspace || workspace_bytes < kda_slots_compact_workspace_size(num_slots)) return KDA_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return KDA_ERR_INVALID;
+  const hipError_t e = kda::launch_slots_compact(pools, slot_bytes, num_pools, num_slots, live, new_slot,
+                                                 count, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
 }  // extern "C"

@@ -183,6 +183,26 @@ struct PrefillArgs {
   float gate_lb;
 };
 
+// Arguments of one convolution launch (validated by the C ABI): forward, backward or step.
+struct ConvArgs {
+  const void* x;
+  int64_t ldx;        // elements between the rows of x
+  const float* weight;
+  const float* bias;
+  const void* init;   // initial states, or null
+  const int* cu;      // offsets of packed sequences, or null
+  int N, T, D, W, silu;
+  int zero_rest;      // zeros in the rows of `out` that lie in no sequence
+  bool bf;
+  void* out;          // y, or dx
+  void* out_state;    // final states, or the initial states' gradient, or null
+};
+struct ConvStep {
+  void* pool;
+  const int* slots;  // null: request n's state is slot n
+  int nslots, B;
+};
+
 }  // namespace kda
 
 namespace kda {

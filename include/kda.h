@@ -43,6 +43,7 @@
 #define KDA_H
 
 #include <stddef.h>
+#include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
@@ -420,6 +421,114 @@ int kda_chunk_fwd_noalloc(const void* q, const void* k, const void* v, const voi
                           const void* beta, const float* initial_state, float* final_state,
                           void* o, int B, int T, int H, int HV, int K, int V, float scale,
                           int chunk_size, int dtype, unsigned flags, void* stream);
+
+/*
+ * Short causal depthwise convolution: the layer that q, k and v (or a selective scan's x, b and
+ * c) pass right before the recurrence (KDA CUDA Trainer README, model paragraph; the
+ * DM-KDAGQA-1.7B-SD model card's usage notes: generation keeps conv states beside the recurrent
+ * ones). Per channel d, in float32:
+ *
+ *     pre_t = bias[d] + sum_w weight[d, w] x_{t - (W-1) + w},   y_t = pre_t / (1 + exp(-pre_t))
+ *
+ * (without KDA_CONV_SILU: y_t = pre_t). The W - 1 rows in front of a sequence's first token are its initial
+ * state, or zeros; the final state is the last W - 1 rows of (initial state ; sequence), ready to
+ * be the next call's initial state or a slot of kda_conv_step's pool.
+ *
+ *   x              [T, D]       dtype   the tokens of all sequences; x_stride elements between
+ *                                       rows (>= D: x may be a slice of a wider activation)
+ *   weight, bias   [D, W], [D]  float32 (bias may be NULL: zeros)
+ *   initial_state  [N, W-1, D]  dtype   or NULL: zeros
+ *   cu_seqlens     [N+1] int32 DEVICE memory: sequence n holds tokens cu_seqlens[n] ..
+ *                  cu_seqlens[n+1] - 1 (non-decreasing, within [0, T]; empty sequences allowed;
+ *                  rows in no sequence are not read, and left as they were in y, or set to
+ *                  zero with KDA_ZERO_REST), or NULL: N sequences of
+ *                  T / N tokens each (T % N == 0)
+ *   final_state    [N, W-1, D]  dtype   out, or NULL
+ *   y              [T, D]       dtype   out
+ *
+ * Constraints: N >= 1, T >= 0, D >= 1 (else KDA_ERR_INVALID); 2 <= W <= 4, D <= 2^20, N <= 2^17
+ * (else KDA_ERR_UNSUPPORTED). No alignment is required; 16-byte aligned rows are fastest. Outputs
+ * must not overlap inputs (final_state not initial_state either). Nothing is allocated.
+ */
+typedef enum {
+  KDA_CONV_SILU = 1, /* y = silu(pre); otherwise y = pre */
+  KDA_ZERO_REST = 2  /* set the output rows that lie in no sequence to zero */
+} kda_conv_flags;
+
+int kda_conv_fwd(const void* x, int64_t x_stride, const float* weight, const float* bias,
+                 const void* initial_state, const int* cu_seqlens, int N, void* final_state,
+                 void* y, int T, int D, int W, unsigned flags, int dtype, void* stream);
+
+/*
+ * Backward of kda_conv_fwd for dy reaching y and dfinal_state reaching the final state (NULL:
+ * zeros): dx [T, D], dweight [D, W], dbias [D] (float32, either may be NULL) and
+ * dinitial_state [N, W-1, D] dtype (may be NULL). dx rows in no sequence are
+ * treated as y rows are there.
+ * The sums over tokens are taken in a fixed order (bitwise reproducible). dy_stride: as x_stride.
+ * workspace: device memory of kda_conv_bwd_workspace_size() bytes, 256-byte aligned,
+ * caller-owned, overwritten; NULL only where that size is 0 (T == 0). Constraints as kda_conv_fwd.
+ */
+size_t kda_conv_bwd_workspace_size(int T, int D, int W, int dtype);
+
+int kda_conv_bwd(const void* x, int64_t x_stride, const float* weight, const float* bias,
+                 const void* initial_state, const int* cu_seqlens, int N, const void* dy,
+                 int64_t dy_stride, const void* dfinal_state, void* dx, float* dweight,
+                 float* dbias, void* dinitial_state, int T, int D, int W, unsigned flags, int dtype,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token of kda_conv_fwd per request: request n takes the W - 1 rows of its state from slot
+ * slots[n] of state_pool [num_slots, W-1, D] (dtype) and its token x[n], writes y[n] [D] and
+ * moves the state on by one row in place. slots NULL: request n uses slot n (num_slots >= B). A
+ * request whose slot is outside [0, num_slots) gets y = 0 and changes no state; valid slots of
+ * one call must be distinct. B <= 65535, otherwise as kda_conv_fwd.
+ */
+int kda_conv_step(const void* x, int64_t x_stride, const float* weight, const float* bias,
+                  void* state_pool, const int* slots, int num_slots, void* y, int B, int D, int W,
+                  unsigned flags, int dtype, void* stream);
+
+/*
+ * Slots of state pools (the caches of kda_recurrent_step_slots, kda_conv_step and kda_ssm_step):
+ * copying, forking and clearing them. A pool is [num_slots] slots of slot_bytes[p] bytes each, in
+ * any type; one call treats the same slots of num_pools pools, such as every layer's states of a
+ * model. Pairs apply in order, i = 0 .. n-1, in every pool:
+ *   - dst[i] and src[i] in [0, num_slots): slot dst[i] becomes a copy of slot src[i] (a fork where
+ *     src[i] stays in use);
+ *   - src[i] < 0: slot dst[i] is cleared (all bytes zero), ready for a new request;
+ *   - dst[i] outside [0, num_slots), or src[i] >= num_slots: nothing (padding).
+ * Pairs that are independent of each other (no destination named twice or read by another pair)
+ * run side by side; other lists give the same result as one pair after the other, more slowly.
+ *
+ *   pools, slot_bytes  [num_pools] HOST memory, read during the call: device pointers and slot
+ *                      sizes (>= 1). Pools must not overlap. 16-byte aligned pools whose slot
+ *                      size is a multiple of 16 are fastest.
+ *   src, dst           [n] int32 DEVICE memory, not inside a pool
+ *
+ * num_slots >= 1, n >= 0, num_pools >= 0 (else KDA_ERR_INVALID); num_slots <= 2^18, slots up to
+ * 2^40 bytes (else KDA_ERR_UNSUPPORTED). Nothing is allocated.
+ */
+int kda_slots_copy(void* const* pools, const size_t* slot_bytes, int num_pools, int num_slots,
+                   const int* src, const int* dst, int n, void* stream);
+
+/*
+ * Compaction: brings the live slots of every pool to its front. With c live slots, the live slots
+ * at or behind slot c, in order, move into the free slots in front of it, in order; slots that
+ * are already in front stay where they are, so as little as possible moves. Slots from c on keep
+ * their bytes. The host needs no copy of the lists: nothing synchronises.
+ *
+ *   live       [num_slots] bytes, DEVICE memory: nonzero where the slot is in use
+ *   new_slot   [num_slots] int32 out: where the slot's state lives now, -1 for a free slot
+ *              (a request's slot s becomes new_slot[s])
+ *   count      [1] int32 out: c
+ *   workspace  device memory of kda_slots_compact_workspace_size() bytes, 256-byte aligned,
+ *              caller-owned, overwritten
+ *   the rest   as for kda_slots_copy
+ */
+size_t kda_slots_compact_workspace_size(int num_slots);
+
+int kda_slots_compact(void* const* pools, const size_t* slot_bytes, int num_pools, int num_slots,
+                      const unsigned char* live, int* new_slot, int* count, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /*
  * A plain streaming copy of `bytes` bytes from src to dst (device memory, 16-byte aligned,

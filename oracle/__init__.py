@@ -22,6 +22,8 @@ Three independent CPU formulations, all in float64 numpy:
 * ``gate`` / ``gate_bwd``: the decay gate that produces g from the gate input,
   A_log and dt_bias (standard and safe, K3 README roadmap row L5), and its
   gradients.
+* ``conv`` / ``conv_bwd``: the short causal convolution in front of the recurrence, and
+  its gradients.
 * ``transforms``: the optional in-operator input transforms (q/k L2
   normalisation, beta sigmoid) that ``recurrent`` / ``decode_step`` apply on
   request.
@@ -37,6 +39,7 @@ from .brute import brute
 from .transforms import l2_normalize, sigmoid
 from .backward import recurrent_bwd
 from .gate import gate, gate_bwd
+from .conv import conv, conv_bwd
 
 __all__ = [
     "decode_step",
@@ -49,4 +52,6 @@ __all__ = [
     "recurrent_bwd",
     "gate",
     "gate_bwd",
+    "conv",
+    "conv_bwd",
 ]

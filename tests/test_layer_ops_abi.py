@@ -1,0 +1,111 @@
+"""Refusals of the convolution, selective scan and slot entry points, without a GPU: validation
+returns before any HIP call, and the binding refuses tensors that are not on a GPU."""
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+import gated_delta_rule_67_amd as kda
+
+FAKE = ctypes.c_void_p(0x1000)  # never dereferenced: every call below fails validation
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(kda.library_path):
+        pytest.skip("libkda.so not built")
+    return kda.library()
+
+
+INV, UNS = kda.KDA_ERR_INVALID, kda.KDA_ERR_UNSUPPORTED
+CONV_BAD = [
+    (dict(x=None), INV), (dict(weight=None), INV), (dict(N=0), INV), (dict(T=-1), INV), (dict(D=0), INV),
+    (dict(T=65), INV),                       # T % N without offsets
+    (dict(x_stride=63), INV),                # rows overlap
+    (dict(dtype=2), INV), (dict(flags=8), INV),
+    (dict(W=1), UNS), (dict(W=5), UNS), (dict(D=1 << 21, x_stride=1 << 21), UNS),
+    (dict(N=1 << 18, T=1 << 18), UNS),
+]
+
+
+@pytest.mark.parametrize("bad,rc", CONV_BAD + [(dict(y=None), INV)])
+def test_conv_fwd_refuses(lib, bad, rc):
+    a = dict(x=FAKE, x_stride=64, weight=FAKE, N=2, y=FAKE, T=64, D=64, W=4, flags=1, dtype=1)
+    a.update(bad)
+    assert lib.kda_conv_fwd(a["x"], a["x_stride"], a["weight"], None, None, None, a["N"], None, a["y"], a["T"],
+                            a["D"], a["W"], a["flags"], a["dtype"], None) == rc
+
+
+@pytest.mark.parametrize("bad,rc", CONV_BAD + [
+    (dict(dy=None), INV), (dict(dx=None), INV), (dict(dy_stride=3), INV), (dict(ws=None), INV),
+    (dict(ws_bytes=4), INV), (dict(ws=ctypes.c_void_p(0x1010)), INV)])
+def test_conv_bwd_refuses(lib, bad, rc):
+    a = dict(x=FAKE, x_stride=64, weight=FAKE, N=2, dy=FAKE, dy_stride=64, dx=FAKE, T=64, D=64, W=4, flags=1,
+             dtype=1, ws=FAKE, ws_bytes=1 << 30)
+    a.update(bad)
+    assert lib.kda_conv_bwd(a["x"], a["x_stride"], a["weight"], None, None, None, a["N"], a["dy"], a["dy_stride"],
+                            None, a["dx"], None, None, None, a["T"], a["D"], a["W"], a["flags"], a["dtype"],
+                            a["ws"], a["ws_bytes"], None) == rc
+
+
+@pytest.mark.parametrize("bad,rc", [
+    (dict(x=None), INV), (dict(pool=None), INV), (dict(y=None), INV), (dict(B=0), INV), (dict(nslots=0), INV),
+    (dict(slots=None, nslots=3), INV), (dict(x_stride=8), INV), (dict(W=5), UNS), (dict(B=70000), UNS),
+    (dict(dtype=3), INV)])
+def test_conv_step_refuses(lib, bad, rc):
+    a = dict(x=FAKE, x_stride=64, weight=FAKE, pool=FAKE, slots=FAKE, nslots=8, y=FAKE, B=4, D=64, W=4, dtype=1)
+    a.update(bad)
+    assert lib.kda_conv_step(a["x"], a["x_stride"], a["weight"], None, a["pool"], a["slots"], a["nslots"], a["y"],
+                             a["B"], a["D"], a["W"], 1, a["dtype"], None) == rc
+
+
+def test_conv_workspace(lib):
+    ws = lib.kda_conv_bwd_workspace_size
+    assert ws(0, 64, 4, 1) == 0 and ws(64, 64, 9, 1) == 0
+    assert ws(4, 64, 4, 1) == 5 * 64 * 4  # one row block: (W + 1) D floats
+    assert ws(32768, 6144, 4, 1) <= 128 * 5 * 6144 * 4
+
+
+def _arrays(ptrs, sizes):
+    return (ctypes.c_void_p * len(ptrs))(*ptrs), (ctypes.c_size_t * len(sizes))(*sizes)
+
+
+@pytest.mark.parametrize("bad,rc", [
+    (dict(ptrs=[0x1000, None]), INV), (dict(sizes=[16, 0]), INV), (dict(nslots=0), INV), (dict(n=-1), INV),
+    (dict(src=None), INV), (dict(dst=None), INV), (dict(npools=-1), INV), (dict(nslots=1 << 19), UNS),
+    (dict(sizes=[16, (1 << 40) + 1]), UNS)])
+def test_slots_copy_refuses(lib, bad, rc):
+    a = dict(ptrs=[0x1000, 0x2000], sizes=[16, 16], npools=2, nslots=4, src=FAKE, dst=FAKE, n=2)
+    a.update(bad)
+    base, size = _arrays(a["ptrs"], a["sizes"])
+    assert lib.kda_slots_copy(base, size, a["npools"], a["nslots"], a["src"], a["dst"], a["n"], None) == rc
+
+
+@pytest.mark.parametrize("bad,rc", [
+    (dict(live=None), INV), (dict(new=None), INV), (dict(count=None), INV), (dict(ws=None), INV),
+    (dict(ws_bytes=8), INV), (dict(ws=ctypes.c_void_p(0x1010)), INV), (dict(nslots=1 << 19), UNS)])
+def test_slots_compact_refuses(lib, bad, rc):
+    a = dict(live=FAKE, new=FAKE, count=FAKE, ws=FAKE, ws_bytes=1 << 20, nslots=4)
+    a.update(bad)
+    base, size = _arrays([0x1000], [16])
+    assert lib.kda_slots_compact(base, size, 1, a["nslots"], a["live"], a["new"], a["count"], a["ws"],
+                                 a["ws_bytes"], None) == rc
+
+
+def test_nothing_to_do_returns_ok(lib):
+    base, size = _arrays([0x1000], [16])
+    assert lib.kda_slots_copy(base, size, 1, 4, None, None, 0, None) == kda.KDA_OK
+    assert lib.kda_slots_copy(None, None, 0, 4, FAKE, FAKE, 3, None) == kda.KDA_OK
+
+
+def test_binding_refuses_host_tensors():
+    x, w = torch.zeros(2, 8, 16), torch.zeros(16, 4)
+    for call in (lambda: kda.kda_conv_fwd(x, w), lambda: kda.kda_conv_bwd(x, w, x),
+                 lambda: kda.kda_conv_step(x[:, 0], w, torch.zeros(2, 3, 16)),
+                 lambda: kda.kda_slots_copy(x, torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)),
+                 lambda: kda.kda_slots_compact([x], torch.ones(2, dtype=torch.bool)),
+                 lambda: kda.kda_slots_copy([], torch.zeros(1), torch.zeros(1))):
+        with pytest.raises(ValueError):
+            call()
