@@ -40,7 +40,7 @@ __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_varlen", "kda_chunk_bwd",
            "kda_chunk_fwd_gated", "kda_recurrent_step_gated", "kda_chunk_fwd_segmented",
            "kda_chunk_fwd_noalloc",
            "kda_conv_fwd", "kda_conv_bwd", "kda_conv_step", "kda_slots_copy",
-           "kda_slots_compact", "NOALLOC_SCRATCH_BYTES", "library", "library_path", "status_string",
+           "kda_slots_compact", "kda_ssm_chunk_fwd", "kda_ssm_step", "NOALLOC_SCRATCH_BYTES", "library", "library_path", "status_string",
            "KDA_OK", "KDA_ERR_INVALID", "KDA_ERR_UNSUPPORTED", "KDA_ERR_HIP", "KDA_ERR_SCRATCH",
            "KDA_FLAG_QK_L2NORM", "KDA_FLAG_BETA_SIGMOID"]
 
@@ -125,6 +125,14 @@ def library():
     lib.kda_conv_bwd.restype = i
     lib.kda_conv_step.argtypes = [vp, i64] + [vp] * 4 + [i, vp] + [i] * 5 + [vp]
     lib.kda_conv_step.restype = i
+    ssm = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp]
+    lib.kda_ssm_chunk_fwd_workspace_size.argtypes = [i] * 8
+    lib.kda_ssm_chunk_fwd_workspace_size.restype = sz
+    lib.kda_ssm_chunk_fwd.argtypes = (ssm + [vp, vp, i, vp, vp] + [i] * 5
+                                      + [ctypes.c_uint, i, vp, sz, vp])
+    lib.kda_ssm_chunk_fwd.restype = i
+    lib.kda_ssm_step.argtypes = ssm + [vp, vp, i, vp] + [i] * 6 + [vp]
+    lib.kda_ssm_step.restype = i
     lib.kda_slots_copy.argtypes = [vp] * 2 + [i, i] + [vp] * 2 + [i, vp]
     lib.kda_slots_copy.restype = i
     lib.kda_slots_compact_workspace_size.argtypes = [i]
@@ -761,6 +769,75 @@ def kda_conv_step(x, weight, state_pool, bias=None, slots=None, silu=True):
     _call(dev, library().kda_conv_step, x.data_ptr(), _token_stride("x", x, 1), weight.data_ptr(),
           _addr(bias), state_pool.data_ptr(), _addr(slots), state_pool.shape[0], y.data_ptr(), B,
           D, W, _conv_flags(silu), _DTYPE[dt])
+    return y
+
+
+def _ssm_args(x, dt, A_log, b, c, D, dt_bias, lead):
+    """Checks what the scan's entry points share; tokens are the first `lead` dimensions.
+    Returns (device, dtype, H, HV, K, V, token strides of x, dt, b, c)."""
+    _require(x.is_cuda, "inputs must be on a GPU")
+    dev, dtype = x.device, x.dtype
+    _require(dtype in _DTYPE, f"unsupported dtype {dtype}")
+    tokens, (HV, V) = tuple(x.shape[:lead]), x.shape[lead:]
+    _require(b.dim() == lead + 2 and tuple(b.shape[:lead]) == tokens, "b must be [tokens, H, K]")
+    H, K = b.shape[lead:]
+    _require(c.shape == b.shape, "c must match b")
+    _require(tuple(dt.shape) == tokens + (HV,), "dt must be [tokens, HV]")
+    strides = []
+    for name, t in (("x", x), ("dt", dt), ("b", b), ("c", c)):
+        _require(t.dtype == dtype and t.device == dev, f"{name} must match x in dtype and device")
+        strides.append(_token_stride(name, t, lead))
+    _check_params([("A_log", A_log, (HV,)), ("D", D, (HV,)), ("dt_bias", dt_bias, (HV,))], dev)
+    return dev, dtype, H, HV, K, V, strides
+
+
+def kda_ssm_chunk_fwd(x, dt, A_log, b, c, D=None, dt_bias=None, initial_state=None, cu_seqlens=None,
+                      output_final_state=True):
+    """Selective state space scan with a scalar decay per head: with D_t = softplus(dt_t + dt_bias),
+    S_t = exp(-exp(A_log) D_t) S_{t-1} + b_t (D_t x_t)^T, y_t = S_t^T c_t + D x_t. x [B,T,HV,V], dt
+    [B,T,HV], b, c [B,T,H,K] (float32 or bf16; slices of a wider activation allowed; value head hv
+    reads pair hv // (HV // H)), or packed without B (or with B = 1) and cu_seqlens int32 [N+1];
+    A_log, D, dt_bias [HV] float32; initial_state [N,HV,K,V] float32. Returns (y shaped like x,
+    final_state [N,HV,K,V] or None); y rows in no packed sequence are zero."""
+    _, N, T = _sequences(x, cu_seqlens)
+    if cu_seqlens is None:
+        _require(x.dim() == 4, "x must be [B, T, HV, V] (packed sequences: give cu_seqlens)")
+    else:
+        _require(x.dim() == 3 or (x.dim() == 4 and x.shape[0] == 1), "packed x must be [T, HV, V] or [1, T, HV, V]")
+        T = x.shape[-3]
+    dev, dtype, H, HV, K, V, strides = _ssm_args(x, dt, A_log, b, c, D, dt_bias, x.dim() - 2)
+    _require(N >= 1, "x must have at least one sequence")
+    if initial_state is not None:
+        _require(tuple(initial_state.shape) == (N, HV, K, V), "initial_state must be [N, HV, K, V]")
+        _check_tensors([("initial_state", initial_state)], torch.float32, dev)
+    lib = library()
+    y = torch.empty(x.shape, dtype=dtype, device=dev)
+    final = torch.empty((N, HV, K, V), dtype=torch.float32, device=dev) if output_final_state else None
+    ws_bytes = lib.kda_ssm_chunk_fwd_workspace_size(N, T, int(cu_seqlens is not None), H, HV, K, V, _DTYPE[dtype])
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    ldx, lddt, ldb, ldc = strides
+    _call(dev, lib.kda_ssm_chunk_fwd, x.data_ptr(), ldx, dt.data_ptr(), lddt, A_log.data_ptr(),
+          b.data_ptr(), ldb, c.data_ptr(), ldc, _addr(D), _addr(dt_bias), _addr(initial_state),
+          _addr(cu_seqlens), N, _addr(final), y.data_ptr(), T, H, HV, K, V, KDA_ZERO_REST,
+          _DTYPE[dtype], _addr(ws), ws_bytes)
+    return y, final
+
+
+def kda_ssm_step(x, dt, A_log, b, c, state_pool, D=None, dt_bias=None, slots=None):
+    """One token of kda_ssm_chunk_fwd per request. x [B,HV,V], dt [B,HV], b, c [B,H,K]; state_pool
+    [num_slots,HV,K,V] float32, updated in place; slots int32 [B] (a slot outside [0, num_slots)
+    gives y = 0 and no update), or None: request n uses slot n. Returns y [B,HV,V]."""
+    _require(x.dim() == 3 and x.numel() > 0, "x must be [B, HV, V]")
+    dev, dtype, H, HV, K, V, (ldx, lddt, ldb, ldc) = _ssm_args(x, dt, A_log, b, c, D, dt_bias, 1)
+    B = x.shape[0]
+    _require(state_pool.dim() == 4 and tuple(state_pool.shape[1:]) == (HV, K, V),
+             "state_pool must be [num_slots, HV, K, V]")
+    _check_tensors([("state_pool", state_pool)], torch.float32, dev)
+    _check_slots(slots, B, state_pool.shape[0], dev)
+    y = torch.empty((B, HV, V), dtype=dtype, device=dev)
+    _call(dev, library().kda_ssm_step, x.data_ptr(), ldx, dt.data_ptr(), lddt, A_log.data_ptr(),
+          b.data_ptr(), ldb, c.data_ptr(), ldc, _addr(D), _addr(dt_bias), state_pool.data_ptr(),
+          _addr(slots), state_pool.shape[0], y.data_ptr(), B, H, HV, K, V, _DTYPE[dtype])
     return y
 
 

@@ -7,6 +7,7 @@
 
 #include "../../include/kda.h"
 #include "kda_device.h"
+#include "kda_ssm.h"
 
 namespace kda {
 template <typename Tin>
@@ -45,6 +46,9 @@ hipError_t launch_conv_bwd(const ConvArgs& p, const void* dy, int64_t lddy, cons
                            float* dweight, float* dbias, void* workspace, hipStream_t stream);
 hipError_t launch_conv_step(const ConvArgs& p, const ConvStep& st, hipStream_t stream);
 size_t conv_bwd_workspace_bytes(int T, int D, int W, bool bf);
+hipError_t launch_ssm_prefill(SsmArgs a, void* workspace, hipStream_t stream);
+size_t ssm_prefill_workspace_bytes(int T, int N, bool packed, int H, int HV, int K, int V, bool bf);
+hipError_t launch_ssm_step(const SsmArgs& a, hipStream_t stream);
 hipError_t launch_slots_copy(void* const* pools, const size_t* slot_bytes, int npools, int nslots,
                              const int* src, const int* dst, int n, hipStream_t stream);
 size_t slots_compact_workspace_bytes(int nslots);
@@ -581,6 +585,75 @@ int kda_conv_step(const void* x, int64_t x_stride, const float* weight, const fl
   a.D = D, a.W = W, a.silu = (flags & KDA_CONV_SILU) != 0, a.bf = dtype == KDA_DTYPE_BF16;
   const kda::ConvStep st{state_pool, slots, num_slots, B};
   return kda::launch_conv_step(a, st, static_cast<hipStream_t>(stream)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+// ---- Selective state space scan
+
+static int check_ssm(int H, int HV, int K, int V, int dtype) {
+  const int rc = check_common(1, H, HV, K, V, 1.f, dtype);
+  if (rc != KDA_OK) return rc;
+  return HV > (1 << 16) ? KDA_ERR_UNSUPPORTED : KDA_OK;
+}
+
+// Token strides (elements) of n > 1 tokens: no overlap, and a tile's offsets fit 31 bits.
+static int check_stride(int64_t stride, int64_t width, int n) {
+  if (n > 1 && stride < width) return KDA_ERR_INVALID;
+  return stride < 0 || stride > (1 << 24) ? KDA_ERR_UNSUPPORTED : KDA_OK;
+}
+
+size_t kda_ssm_chunk_fwd_workspace_size(int N, int T, int packed, int H, int HV, int K, int V, int dtype) {
+  if (N < 1 || T < 0 || (!packed && T % N != 0) || check_ssm(H, HV, K, V, dtype) != KDA_OK) return 0;
+  return kda::ssm_prefill_workspace_bytes(T, N, packed != 0, H, HV, K, V, dtype == KDA_DTYPE_BF16);
+}
+
+int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride,
+                      const float* A_log, const void* b, int64_t b_stride, const void* c,
+                      int64_t c_stride, const float* D, const float* dt_bias,
+                      const float* initial_state, const int* cu_seqlens, int N,
+                      float* final_state, void* y, int T, int H, int HV, int K, int V,
+                      unsigned flags, int dtype, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  if (!valid_sequences(N, T, cu_seqlens) || (flags & ~(unsigned)KDA_ZERO_REST)) return KDA_ERR_INVALID;
+  int rc = check_ssm(H, HV, K, V, dtype);
+  if (rc != KDA_OK) return rc;
+  if (!A_log || (T > 0 && (!x || !dt || !b || !c || !y))) return KDA_ERR_INVALID;
+  const int64_t strides[] = {x_stride, dt_stride, b_stride, c_stride};
+  const int64_t widths[] = {(int64_t)HV * V, HV, (int64_t)H * K, (int64_t)H * K};
+  for (int i = 0; i < 4; ++i)
+    if ((rc = check_stride(strides[i], widths[i], T)) != KDA_OK) return rc;
+  if (N > (1 << 20)) return KDA_ERR_UNSUPPORTED;
+  const size_t need = kda_ssm_chunk_fwd_workspace_size(N, T, cu_seqlens != nullptr, H, HV, K, V, dtype);
+  if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return KDA_ERR_INVALID;
+  kda::SsmArgs a{};
+  a.x = x, a.ldx = x_stride, a.dt = dt, a.lddt = dt_stride, a.A_log = A_log;
+  a.b = b, a.ldb = b_stride, a.c = c, a.ldc = c_stride, a.D = D, a.dt_bias = dt_bias;
+  a.s0 = initial_state, a.cu = cu_seqlens, a.N = N, a.T = T, a.H = H, a.HV = HV, a.K = K, a.V = V;
+  a.sT = final_state, a.y = y, a.bf = dtype == KDA_DTYPE_BF16, a.zero_rest = (flags & KDA_ZERO_REST) != 0;
+  const hipError_t e = kda::launch_ssm_prefill(a, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+int kda_ssm_step(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride,
+                 const float* A_log, const void* b, int64_t b_stride, const void* c,
+                 int64_t c_stride, const float* D, const float* dt_bias, float* state_pool,
+                 const int* slots, int num_slots, void* y, int B, int H, int HV, int K, int V,
+                 int dtype, void* stream) {
+  if (!positive(B) || num_slots < 1 || (!slots && num_slots < B)) return KDA_ERR_INVALID;
+  int rc = check_ssm(H, HV, K, V, dtype);
+  if (rc != KDA_OK) return rc;
+  if (!x || !dt || !A_log || !b || !c || !state_pool || !y) return KDA_ERR_INVALID;
+  const int64_t strides[] = {x_stride, dt_stride, b_stride, c_stride};
+  const int64_t widths[] = {(int64_t)HV * V, HV, (int64_t)H * K, (int64_t)H * K};
+  for (int i = 0; i < 4; ++i)
+    if (B > 1 && strides[i] < widths[i]) return KDA_ERR_INVALID;
+  if ((int64_t)B * HV * 4 > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  kda::SsmArgs a{};
+  a.x = x, a.ldx = x_stride, a.dt = dt, a.lddt = dt_stride, a.A_log = A_log;
+  a.b = b, a.ldb = b_stride, a.c = c, a.ldc = c_stride, a.D = D, a.dt_bias = dt_bias;
+  a.H = H, a.HV = HV, a.K = K, a.V = V, a.y = y, a.bf = dtype == KDA_DTYPE_BF16;
+  a.pool = state_pool, a.slots = slots, a.nslots = num_slots, a.B = B;
+  return kda::launch_ssm_step(a, static_cast<hipStream_t>(stream)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
 // ---- Slots of state pools

@@ -1,0 +1,42 @@
+// Arguments of the selective scan's launches (validated by the C ABI).
+#pragma once
+
+#include "kda_sequence.h"
+
+namespace kda {
+
+struct SsmArgs {
+  const void* x;   // [T, HV, V], ldx elements between tokens
+  int64_t ldx;
+  const void* dt;  // [T, HV]
+  int64_t lddt;
+  const float* A_log;  // [HV]
+  const void* b;       // [T, H, K]
+  int64_t ldb;
+  const void* c;
+  int64_t ldc;
+  const float* D;        // [HV] or null
+  const float* dt_bias;  // [HV] or null
+  const float* s0;       // [N, HV, K, V] or null
+  const int* cu;         // [N+1] or null: N sequences of T / N tokens
+  int N, T, H, HV, K, V;
+  float* sT;             // [N, HV, K, V] or null
+  void* y;               // [T, HV, V]
+  bool bf, zero_rest;
+  // the step
+  float* pool;
+  const int* slots;
+  int nslots, B;
+  // the prefill's segments of the token axis: seg tokens each, nseg of them; the state entering
+  // segment k in seg_state[k - 1], the log2 of its decay since the segment before in seg_g
+  int seg, nseg;
+  bool crossed;      // whether a sequence may go on over a segment's end
+  float* seg_state;  // [nseg - 1][HV][K][V]
+  float* seg_g;      // [nseg - 1][HV]
+  bool vec;          // rows of x, b, c and y are whole 16-byte pieces, aligned
+};
+
+// seg_g of a segment boundary at which no sequence goes on (decays have g <= 0).
+constexpr float kNoCarry = 2.f;
+
+}  // namespace kda

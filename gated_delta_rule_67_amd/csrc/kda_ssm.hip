@@ -1,0 +1,627 @@
+// Selective state space scan over whole sequences: the recurrence with one scalar decay per
+// head that hybrid stacks put beside the gated delta rule. Per value head, K x V float32 state S:
+//   D_t = softplus(dt_t + dt_bias),  a_t = exp(-exp(A_log) D_t)      (the KDA decay gate's form)
+//   S_t = a_t S_{t-1} + b_t (D_t x_t)^T,     y_t = S_t^T c_t + D x_t
+// HV value heads share H pairs of b and c (value head hv reads pair hv / (HV / H)).
+//
+// Tiles of 64 tokens, with G the in-tile inclusive sum of log2 a (so every exponent below is of a
+// difference <= 0):
+//   M[i, j] = (c_i . b_j) 2^(G_i - G_j) D_j  for j <= i, else 0
+//   y_i     = sum_j M[i, j] x_j + 2^(G_i) S^T c_i + D x_i
+//   S      <- 2^(G_63) S + sum_j b_j (2^(G_63 - G_j) D_j x_j)^T
+// The products run on the matrix cores (16x16x32 bf16, float32 accumulators). M and the S that y
+// reads are rounded to bf16, as y is; the state itself keeps float32 accuracy: b is bf16 as given,
+// and the weighted x of its update is split into three bf16 terms (8 bits each), three products.
+//
+// A workgroup of four waves owns 64 PT columns: one or more value heads of one b / c pair, whose
+// b, c and c . b products they share, and carries the state in accumulators (16 PT columns a
+// wave) over the tiles of one segment of the token axis. Segments have equal lengths whatever the
+// sequences: a tile ends at the sequence's end. float32 inputs take the same steps with tiles of
+// 32 tokens, 16x16x4 float32 products and nothing rounded. With more than one segment, a pass over the tiles
+// of each boundary's sequence without outputs (OUT = false) gives the state that leaves the
+// segment, a scan composes them, and the pass with outputs starts from the composed states.
+#include "kda_ssm.h"
+
+namespace kda {
+namespace ssm {
+
+// Tokens of a tile. float32 takes half as many: its products are 16 times as expensive, and those
+// inside a tile grow with it.
+template <typename T> constexpr int kTokens = sizeof(T) == 2 ? 64 : 32;
+constexpr int kThreads = 256;
+constexpr unsigned kOutOfRange = 0x80000000u;  // buffer loads there read zeros
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) unsigned char lds_u8;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, unsigned bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
+}
+
+// Four bf16 by the LDS transpose load: in each 16-lane group, lane l receives element l % 4 of
+// the 8-byte pieces addressed by lanes 4e + l / 4, e = 0 .. 3.
+__device__ __forceinline__ bf16x4 load_tr4(const bf16* p) {
+#if __HIP_DEVICE_COMPILE__
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                        (__attribute__((address_space(3))) s16x4*)(lds_u8*)p));
+#else
+  (void)p;
+  return bf16x4{};
+#endif
+}
+
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x4 mfma(float a, float b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+// A tile: tokens t0 .. t0 + rows - 1 of sequence seq; first / last: holds its first / last token.
+struct Tile {
+  int t0, rows, seq;
+  bool first, last;
+};
+
+// A ROWS x COLS matrix on its way from memory to LDS: each thread holds pieces of 16 bytes.
+// Columns are blocks of PAD, of which `width` are real. VEC: every real row of a block is whole
+// 16-byte pieces, aligned in memory.
+template <typename T, int ROWS, int COLS, int PAD, bool VEC>
+struct Stage {
+  static constexpr int kElem = 16 / sizeof(T), kRow = COLS / kElem, kPieces = ROWS * kRow / kThreads;
+  static_assert(kPieces * kThreads == ROWS * kRow, "every thread holds the same number of pieces");
+  u32x4 v[kPieces];
+
+  // src: row 0, column 0; ld: elements between rows; rows behind `rows` and columns behind
+  // `width` of a block read zeros.
+  __device__ __forceinline__ void load(const T* src, int64_t ld, int rows, int width) {
+    constexpr int kBlocks = COLS / PAD;
+    const __amdgpu_buffer_rsrc_t r =
+        make_rsrc(src, (unsigned)((((int64_t)rows - 1) * ld + (int64_t)kBlocks * width) * sizeof(T)));
+    const unsigned rowb = (unsigned)(ld * sizeof(T));
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e) {
+      const int piece = threadIdx.x + kThreads * e, row = piece / kRow, c = piece % kRow * kElem;
+      const int blk = c / PAD, p = c - blk * PAD;
+      const unsigned off = (unsigned)row * rowb + (unsigned)(blk * width + p) * sizeof(T);
+      auto in = [&](int k) { return p + k < width ? off + k * (unsigned)sizeof(T) : kOutOfRange; };
+      if constexpr (VEC) {
+        v[e] = __builtin_amdgcn_raw_buffer_load_b128(r, in(0), 0, 0);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (sizeof(T) == 4) {
+            v[e][k] = __builtin_amdgcn_raw_buffer_load_b32(r, in(k), 0, 0);
+          } else {
+            const unsigned lo = __builtin_amdgcn_raw_buffer_load_b16(r, in(2 * k), 0, 0);
+            const unsigned hi = __builtin_amdgcn_raw_buffer_load_b16(r, in(2 * k + 1), 0, 0);
+            v[e][k] = lo | hi << 16;
+          }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* dst, int ldd) const {
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e) {
+      const int piece = threadIdx.x + kThreads * e, row = piece / kRow, c = piece % kRow * kElem;
+      *reinterpret_cast<u32x4*>(dst + row * ldd + c) = v[e];
+    }
+  }
+};
+
+// Per token and head of a tile.
+struct Decay {
+  float dt[64], hi[64], lo[64];  // D, and G as a sum of two floats (log2 units)
+  float eg[64], w[64];           // 2^G, and D 2^(G_63 - G)
+  float ghi, glo;                // G_63, the whole tile's
+};
+
+// One wave: lane = token (those behind the tile's rows have D = 0). G is summed in float64, so
+// that differences of two of its values keep float32 accuracy however large both are.
+__device__ __forceinline__ void make_decay(Decay& d, float raw, bool in, float bias, float neg_rate) {
+  const int lane = __lane_id();
+  float e, r;
+  const float dt = in ? softplus_f32(raw + bias, e, r) : 0.f;
+  double g = (double)(neg_rate * dt) * 1.4426950408889634;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const double up = __shfl_up(g, off);
+    g += lane >= off ? up : 0.0;
+  }
+  const double end = __shfl(g, 63);
+  const float hi = (float)g;
+  d.dt[lane] = dt;
+  d.hi[lane] = hi;
+  d.lo[lane] = (float)(g - (double)hi);
+  d.eg[lane] = fast_exp2(hi);
+  d.w[lane] = dt * fast_exp2((float)(end - g));
+  if (lane == 63) {
+    d.ghi = hi;
+    d.glo = d.lo[63];
+  }
+}
+
+// NT: K in tiles of 16; HB heads of PP columns; PT tiles of 16 columns a wave.
+template <typename T, int NT, int PP, int HB, int PT, bool OUT, bool VEC>
+__global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hblocks) {
+  constexpr bool BF = sizeof(T) == 2;
+  constexpr int kTok = kTokens<T>, kPad = 16 / sizeof(T);
+  constexpr int XC = HB * PP, NP = 16 * NT, LDN = NP + kPad, LDX = XC + kPad, LDM = kTok + kPad, KS = NT / 2;
+  static_assert(XC <= 64 * PT && NT % 2 == 0 && PP % (16 * PT) == 0, "tile shape");
+  __shared__ __attribute__((aligned(16))) T Xs[kTok * LDX];
+  __shared__ __attribute__((aligned(16))) T Bs[kTok * LDN];
+  __shared__ __attribute__((aligned(16))) T Cs[OUT ? kTok * LDN : 8];
+  __shared__ __attribute__((aligned(16))) T Ms[OUT ? HB * kTok * LDM : 8];
+  __shared__ __attribute__((aligned(16))) Decay s_dec[2][HB];
+
+  const int K = a.K, V = a.V, vblocks = (V + PP - 1) / PP;
+  const int main_blocks = hblocks * (OUT ? a.nseg : a.nseg - 1);
+  int bid = blockIdx.x;
+  if (OUT && bid >= main_blocks) {  // empty sequences: the state passes through
+    const int n = bid - main_blocks;
+    const Span s = sequence_span(a.cu, a.N, a.T, n);
+    if (s.eos > s.bos) return;
+    const int64_t sz = (int64_t)a.HV * K * V;
+    for (int64_t i = threadIdx.x; i < sz; i += kThreads) a.sT[n * sz + i] = a.s0 ? a.s0[n * sz + i] : 0.f;
+    return;
+  }
+  // neighbouring head blocks (which share b and c) on one XCD: workgroups are dealt out
+  // round-robin over the 8 of them
+  if (main_blocks % 8 == 0) bid = (bid & 7) * (main_blocks / 8) + (bid >> 3);
+  const int segk = bid / hblocks, hb = bid - segk * hblocks;
+  const int h0 = hb / vblocks * HB, v0 = hb % vblocks * PP;  // first head, first column in it
+  const int width = min(PP, V - v0);                          // real columns of each head
+  const int grp = h0 / (a.HV / a.H);
+
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lr = lane & 15, lq = lane >> 4;
+  const int col0 = wv * 16 * PT, hh = col0 / PP, p0 = v0 + col0 - hh * PP;
+  const bool active = hh < HB;  // waves behind the last head only help with the products c . b
+  const int hv = h0 + (active ? hh : 0);
+
+  const int seg0 = segk * a.seg;
+  const int end = (int)min((int64_t)seg0 + a.seg, (int64_t)a.T);
+  int pos = seg0, seq;
+  bool carry = true;  // OUT = false: the state entering the segment reaches its end
+  if constexpr (OUT) {
+    seq = find_sequence(a.cu, a.N, a.T, seg0);
+  } else {
+    // only the part of the sequence that goes on behind the segment's end
+    seq = find_sequence(a.cu, a.N, a.T, end - 1);
+    const Span s = sequence_span(a.cu, a.N, a.T, seq);
+    if (s.eos <= end || s.bos >= end) {
+      if (wv == 0 && lane < HB && v0 == 0) a.seg_g[(int64_t)segk * a.HV + h0 + lane] = kNoCarry;
+      return;
+    }
+    carry = s.bos < seg0;
+    pos = max(seg0, s.bos);
+  }
+
+  T* y = static_cast<T*>(a.y);
+  const int64_t ldy = (int64_t)a.HV * V;
+  // the tile at or behind token t: rows == 0 if the segment holds none
+  auto tile_at = [&](int t, int s) {
+    while (t < end && s < a.N) {
+      const Span sp = sequence_span(a.cu, a.N, a.T, s);
+      if (sp.eos <= t) { ++s; continue; }
+      if (sp.bos > t) { t = sp.bos; continue; }
+      const int rows = min(kTok, min(sp.eos, end) - t);
+      return Tile{t, rows, s, t == sp.bos, t + rows == sp.eos};
+    }
+    return Tile{end, 0, s, false, false};
+  };
+  // rows [t, to) lie in no sequence
+  auto outside = [&](int t, int to) {
+    if (!OUT || !a.zero_rest || t >= to) return;
+    for (; t < to; ++t)
+      for (int i = threadIdx.x; i < HB * width; i += kThreads)
+        y[t * ldy + (int64_t)(h0 + i / width) * V + v0 + i % width] = from_f32<T>(0.f);
+  };
+
+  Stage<T, kTok, XC, PP, VEC> xr;
+  Stage<T, kTok, NP, NP, VEC> br, cr;
+  T dtr = from_f32<T>(0.f);
+  auto load = [&](const Tile& t) {
+    xr.load(static_cast<const T*>(a.x) + (int64_t)t.t0 * a.ldx + (int64_t)h0 * V + v0, a.ldx, t.rows, width);
+    br.load(static_cast<const T*>(a.b) + (int64_t)t.t0 * a.ldb + (int64_t)grp * K, a.ldb, t.rows, K);
+    if constexpr (OUT)
+      cr.load(static_cast<const T*>(a.c) + (int64_t)t.t0 * a.ldc + (int64_t)grp * K, a.ldc, t.rows, K);
+    if (wv < HB && lane < t.rows)
+      dtr = static_cast<const T*>(a.dt)[(int64_t)(t.t0 + lane) * a.lddt + h0 + wv];
+  };
+  float bias = 0.f, neg_rate = 0.f;
+  if (wv < HB) {  // wave w prepares the decays of head w
+    bias = a.dt_bias ? a.dt_bias[h0 + wv] : 0.f;
+    neg_rate = -expf(a.A_log[h0 + wv]);
+  }
+  const float skip = a.D ? a.D[hv] : 0.f;
+
+  f32x4 S[PT][NT];  // rows 16 nt + 4 lq .. + 3, column 16 pt + lr of the wave's
+  auto each_state = [&](auto f) {
+    if (!active) return;
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) {
+      int p = p0 + 16 * pt + lr;
+      asm volatile("" : "+v"(p));  // the addresses are made here, not kept over the tile loop
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int n = 16 * nt + 4 * lq + r;
+          if (n < K && p < V) S[pt][nt][r] = f(S[pt][nt][r], (int64_t)n * V + p);
+        }
+    }
+  };
+  auto zero_state = [&] {
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) S[pt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  const int64_t sz = (int64_t)K * V;
+  zero_state();
+  if constexpr (OUT) {
+    if (segk > 0 && sequence_span(a.cu, a.N, a.T, seq).bos < seg0) {
+      const float* src = a.seg_state + ((int64_t)(segk - 1) * a.HV + hv) * sz;
+      each_state([&](float, int64_t i) { return src[i]; });
+    }
+  }
+
+  Tile cur = tile_at(pos, seq);
+  outside(pos, cur.t0);
+  if (cur.rows == 0) return;
+  load(cur);
+  if (wv < HB)
+    make_decay(s_dec[0][wv], to_f32(dtr), lane < cur.rows, bias, neg_rate);
+  double gsum = 0.0;
+
+  for (int buf = 0;; buf ^= 1) {
+    xr.store(Xs, LDX);
+    br.store(Bs, LDN);
+    if constexpr (OUT) cr.store(Cs, LDN);
+    lds_barrier();
+    const Tile nxt = cur.t0 + cur.rows < end ? tile_at(cur.t0 + cur.rows, cur.seq) : Tile{end, 0, cur.seq, false, false};
+    outside(cur.t0 + cur.rows, nxt.t0);
+    if (nxt.rows) load(nxt);
+
+    if (cur.first) {  // the sequence's initial state
+      zero_state();
+      if (a.s0) {
+        const float* src = a.s0 + ((int64_t)cur.seq * a.HV + hv) * sz;
+        each_state([&](float, int64_t i) { return src[i]; });
+      }
+    }
+    const Decay* dec = s_dec[buf];
+
+    if constexpr (OUT) {
+      // c . b transposed (rows j, columns i), then M of each head. bf16: a wave takes the 16
+      // tokens i of its number and all j up to theirs; float32: wave 0, 1 and 2 one tile each.
+      const int it = BF ? wv : (wv + 1) / 2, i = 16 * it + lr;
+      bf16x8 cf[BF ? KS : 1];
+      if constexpr (BF) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) cf[ks] = *reinterpret_cast<const bf16x8*>(Cs + i * LDN + 32 * ks + 8 * lq);
+      }
+      const int jt0 = BF ? 0 : wv / 2, jt1 = BF ? (wv | 1) : (wv < 3 ? jt0 : jt0 - 1);
+      for (int jt = jt0; jt <= jt1; ++jt) {
+        f32x4 sc = {0.f, 0.f, 0.f, 0.f};
+        if (jt <= it) {  // tiles above the diagonal that a product of 32 tokens reads are zeros
+          if constexpr (BF) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+              sc = mfma(*reinterpret_cast<const bf16x8*>(Bs + (16 * jt + lr) * LDN + 32 * ks + 8 * lq), cf[ks], sc);
+          } else {
+#pragma unroll 4
+            for (int k = lq; k < NP; k += 4) sc = mfma(Bs[(16 * jt + lr) * LDN + k], Cs[i * LDN + k], sc);
+          }
+        }
+        const int j = 16 * jt + 4 * lq;
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+          const f32x4 hj = *reinterpret_cast<const f32x4*>(dec[h].hi + j), lj = *reinterpret_cast<const f32x4*>(dec[h].lo + j);
+          const f32x4 dj = *reinterpret_cast<const f32x4*>(dec[h].dt + j);
+          const float hi = dec[h].hi[i], lo = dec[h].lo[i];
+          T m[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float w = sc[r] * dj[r] * fast_exp2((hi - hj[r]) + (lo - lj[r]));
+            m[r] = from_f32<T>(j + r <= i ? w : 0.f);
+          }
+          typedef T vec4 __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<vec4*>(Ms + (h * kTok + i) * LDM + j) = vec4{m[0], m[1], m[2], m[3]};
+        }
+      }
+      lds_barrier();
+    }
+
+    if (active) {
+      // y of 16 tokens and this wave's columns (rows p), from accumulators that hold it transposed
+      auto store_y = [&](int i, const f32x4 (&acc)[PT]) {
+        if (i >= cur.rows) return;
+        T* yr = y + (int64_t)(cur.t0 + i) * ldy + (int64_t)hv * V;
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) {
+          const int p = p0 + 16 * pt + 4 * lq;
+          typedef T vec4 __attribute__((ext_vector_type(4)));
+          vec4 o;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[r] = from_f32<T>(acc[pt][r]);
+          if constexpr (VEC) {
+            if (p < V) *reinterpret_cast<vec4*>(yr + p) = o;
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (p + r < V) yr[p + r] = o[r];
+          }
+        }
+      };
+      // 2^(G_i) (S^T c_i) + D x_i, ahead of the products inside the tile
+      auto decay_y = [&](int i, f32x4 (&acc)[PT]) {
+        const float eg = dec[hh].eg[i];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[pt][r] = acc[pt][r] * eg + skip * to_f32(Xs[i * LDX + col0 + 16 * pt + 4 * lq + r]);
+      };
+      const float ga = fast_exp2(dec[hh].ghi);
+      if constexpr (BF) {
+        // x of this wave's columns, transposed: rows p, 8 tokens a lane
+        bf16x8 xf[PT][2];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            const bf16* src = Xs + (32 * ks + 8 * lq + (lr >> 2)) * LDX + col0 + 16 * pt + 4 * (lr & 3);
+            xf[pt][ks] = join(load_tr4(src), load_tr4(src + 4 * LDX));
+          }
+        if constexpr (OUT) {
+          // S^T as an operand: k slots 8 lq + e hold state rows 32 ks + 4 lq + e (e < 4) and
+          // 32 ks + 16 + 4 lq + e - 4
+          bf16x8 sf[PT][KS];
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                sf[pt][ks][e] = from_f32<bf16>(S[pt][2 * ks][e]);
+                sf[pt][ks][e + 4] = from_f32<bf16>(S[pt][2 * ks + 1][e]);
+              }
+#pragma unroll
+          for (int it = 0; it < kTok / 16; ++it) {
+            const int i = 16 * it + lr;
+            f32x4 acc[PT];
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) acc[pt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              const bf16* src = Cs + i * LDN + 32 * ks + 4 * lq;
+              const bf16x8 cv = join(*reinterpret_cast<const bf16x4*>(src), *reinterpret_cast<const bf16x4*>(src + 16));
+#pragma unroll
+              for (int pt = 0; pt < PT; ++pt) acc[pt] = mfma(sf[pt][ks], cv, acc[pt]);
+            }
+            decay_y(i, acc);
+#pragma unroll
+            for (int ks = 0; ks <= it / 2; ++ks) {
+              const bf16x8 mv = *reinterpret_cast<const bf16x8*>(Ms + (hh * kTok + i) * LDM + 32 * ks + 8 * lq);
+#pragma unroll
+              for (int pt = 0; pt < PT; ++pt) acc[pt] = mfma(xf[pt][ks], mv, acc[pt]);
+            }
+            store_y(i, acc);
+          }
+        }
+        // the state's update
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) S[pt][nt] *= ga;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          bf16x8 w0[PT], w1[PT], w2[PT];
+          const f32x4 wa = *reinterpret_cast<const f32x4*>(dec[hh].w + 32 * ks + 8 * lq);
+          const f32x4 wb = *reinterpret_cast<const f32x4*>(dec[hh].w + 32 * ks + 8 * lq + 4);
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float v = to_f32(xf[pt][ks][e]) * (e < 4 ? wa[e & 3] : wb[e & 3]);
+              w0[pt][e] = from_f32<bf16>(v);
+              const float v1 = v - to_f32(w0[pt][e]);
+              w1[pt][e] = from_f32<bf16>(v1);
+              w2[pt][e] = from_f32<bf16>(v1 - to_f32(w1[pt][e]));
+            }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const bf16* src = Bs + (32 * ks + 8 * lq + (lr >> 2)) * LDN + 16 * nt + 4 * (lr & 3);
+            const bf16x8 bt = join(load_tr4(src), load_tr4(src + 4 * LDN));
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) {
+              S[pt][nt] = mfma(bt, w0[pt], S[pt][nt]);
+              S[pt][nt] = mfma(bt, w1[pt], S[pt][nt]);
+              S[pt][nt] = mfma(bt, w2[pt], S[pt][nt]);
+            }
+          }
+        }
+      } else {
+        // float32: 16x16x4 products, one operand value a lane; slot lq of step r of a state tile
+        // holds its row 4 lq + r
+        if constexpr (OUT) {
+#pragma unroll
+          for (int it = 0; it < kTok / 16; ++it) {
+            const int i = 16 * it + lr;
+            f32x4 acc[PT];
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) acc[pt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const f32x4 cv = *reinterpret_cast<const f32x4*>(Cs + i * LDN + 16 * nt + 4 * lq);
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int pt = 0; pt < PT; ++pt) acc[pt] = mfma(S[pt][nt][r], cv[r], acc[pt]);
+            }
+            decay_y(i, acc);
+#pragma unroll
+            for (int j = 0; j < 16 * (it + 1); j += 4)
+#pragma unroll
+              for (int pt = 0; pt < PT; ++pt)
+                acc[pt] = mfma(Xs[(j + lq) * LDX + col0 + 16 * pt + lr], Ms[i * LDM + j + lq], acc[pt]);
+            store_y(i, acc);
+          }
+        }
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) S[pt][nt] *= ga;
+#pragma unroll 2
+        for (int j = lq; j < kTok; j += 4) {
+          const float w = dec[hh].w[j];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float bt = Bs[j * LDN + 16 * nt + lr];
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) S[pt][nt] = mfma(bt, w * Xs[j * LDX + col0 + 16 * pt + lr], S[pt][nt]);
+          }
+        }
+      }
+      if (OUT && cur.last && a.sT) {
+        float* dst = a.sT + ((int64_t)cur.seq * a.HV + hv) * sz;
+        each_state([&](float s, int64_t i) { return dst[i] = s; });
+      }
+      gsum += (double)dec[hh].ghi + (double)dec[hh].glo;
+    }
+    if (nxt.rows == 0) break;
+    if (wv < HB)
+      make_decay(s_dec[buf ^ 1][wv], to_f32(dtr), lane < nxt.rows, bias, neg_rate);
+    lds_barrier();
+    cur = nxt;
+  }
+  if constexpr (!OUT) {
+    float* dst = a.seg_state + ((int64_t)segk * a.HV + hv) * sz;
+    each_state([&](float s, int64_t i) { return dst[i] = s; });
+    // a sequence that starts in the segment takes nothing from the segment before
+    if (active && p0 == 0 && lane == 0) a.seg_g[(int64_t)segk * a.HV + hv] = carry ? (float)gsum : -INFINITY;
+  }
+}
+
+// Composes the segments' states in order, in place: seg_state[k] becomes the state that enters
+// segment k + 1. One thread an element of [HV, K, V].
+__global__ __launch_bounds__(kThreads) void compose_kernel(float* __restrict__ seg_state,
+                                                           const float* __restrict__ seg_g, int nb, int HV,
+                                                           int64_t sz) {
+  const int64_t n = (int64_t)HV * sz, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n) return;
+  const int hv = (int)(i / sz);
+  float s = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < nb; ++k) {
+    const float g = seg_g[(int64_t)k * HV + hv];
+    float v = 0.f;
+    if (g != kNoCarry) {
+      // where nothing is carried the product is left out: s may be infinite
+      v = seg_state[(int64_t)k * n + i];
+      if (g > -INFINITY) v += fast_exp2(g) * s;
+      seg_state[(int64_t)k * n + i] = v;
+    }
+    s = v;
+  }
+}
+
+// ---- launchers
+
+template <typename T, int NT, int PP, int HB, int PT, bool VEC>
+hipError_t run(const SsmArgs& a, hipStream_t stream) {
+  const int hblocks = a.HV / HB * ((a.V + PP - 1) / PP);
+  if (a.crossed) {
+    hipLaunchKernelGGL((prefill_kernel<T, NT, PP, HB, PT, false, VEC>), dim3(hblocks * (a.nseg - 1)),
+                       dim3(kThreads), 0, stream, a, hblocks);
+    const int64_t n = (int64_t)a.HV * a.K * a.V;
+    hipLaunchKernelGGL(compose_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream,
+                       a.seg_state, a.seg_g, a.nseg - 1, a.HV, (int64_t)a.K * a.V);
+  }
+  const int empties = (a.cu || a.T == 0) && a.sT ? a.N : 0;
+  if (hblocks * a.nseg + empties == 0) return hipSuccess;
+  hipLaunchKernelGGL((prefill_kernel<T, NT, PP, HB, PT, true, VEC>), dim3(hblocks * a.nseg + empties),
+                     dim3(kThreads), 0, stream, a, hblocks);
+  return hipGetLastError();
+}
+
+// Heads and columns of a workgroup.
+struct Shape {
+  int heads, cols;
+};
+inline Shape shape_of(bool bf, int H, int HV, int V) {
+  if (!bf) return {1, 64};
+  const int pair = (HV / H) % 2 == 0 ? 2 : 1;  // two heads that share b and c, where V leaves room
+  return V > 64 ? Shape{1, 128} : V > 32 ? Shape{pair, 64} : Shape{pair, 32};
+}
+
+template <typename T, int NT, bool VEC>
+hipError_t by_heads(const SsmArgs& a, hipStream_t stream) {
+  if constexpr (sizeof(T) == 4) return run<T, NT, 64, 1, 1, VEC>(a, stream);
+  else {
+    const Shape s = shape_of(true, a.H, a.HV, a.V);
+    if (s.cols == 128) return run<T, NT, 128, 1, 2, VEC>(a, stream);
+    if (s.cols == 64) return s.heads == 2 ? run<T, NT, 64, 2, 2, VEC>(a, stream) : run<T, NT, 64, 1, 1, VEC>(a, stream);
+    return s.heads == 2 ? run<T, NT, 32, 2, 1, VEC>(a, stream) : run<T, NT, 32, 1, 1, VEC>(a, stream);
+  }
+}
+
+template <typename T>
+hipError_t by_state(const SsmArgs& a, hipStream_t stream) {
+  if (a.K > 64) return a.vec ? by_heads<T, 8, true>(a, stream) : by_heads<T, 8, false>(a, stream);
+  return a.vec ? by_heads<T, 4, true>(a, stream) : by_heads<T, 4, false>(a, stream);
+}
+
+}  // namespace ssm
+
+// Segments of the token axis for these arguments.
+struct Segments {
+  int len, n;
+  bool crossed;  // a sequence may go on over a boundary
+};
+static Segments ssm_segments(int T, int N, bool packed, int H, int HV, int V, bool bf) {
+  if (T == 0) return {1, 0, false};
+  const ssm::Shape s = ssm::shape_of(bf, H, HV, V);
+  const int64_t hblocks = (int64_t)HV / s.heads * ((V + s.cols - 1) / s.cols);
+  const int64_t want = (512 + hblocks - 1) / hblocks;  // two workgroups a CU
+  int64_t len = (((int64_t)T + want - 1) / want + 63) / 64 * 64;
+  if (len < 256) len = 256;
+  if (!packed && len >= T / N) len = T / N;  // whole sequences
+  const int n = (int)((T + len - 1) / len);
+  return {(int)len, n, n > 1 && (packed || len % (T / N) != 0)};
+}
+
+size_t ssm_prefill_workspace_bytes(int T, int N, bool packed, int H, int HV, int K, int V, bool bf) {
+  const Segments g = ssm_segments(T, N, packed, H, HV, V, bf);
+  if (!g.crossed) return 0;
+  const size_t n = (size_t)(g.n - 1) * HV * ((size_t)K * V + 1) * 4;
+  return (n + 255) / 256 * 256;
+}
+
+hipError_t launch_ssm_prefill(SsmArgs a, void* workspace, hipStream_t stream) {
+  const Segments g = ssm_segments(a.T, a.N, a.cu != nullptr, a.H, a.HV, a.V, a.bf);
+  a.seg = g.len;
+  a.nseg = g.n;
+  a.crossed = g.crossed;
+  if (g.crossed) {
+    a.seg_state = static_cast<float*>(workspace);
+    a.seg_g = a.seg_state + (size_t)(g.n - 1) * a.HV * a.K * a.V;
+  }
+  // 16-byte pieces: whole ones in every row, at aligned addresses (y rows are whole ones too then)
+  const int per = a.bf ? 8 : 4;
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.b) |
+                         reinterpret_cast<uintptr_t>(a.c) | reinterpret_cast<uintptr_t>(a.y);
+  a.vec = (a.K | a.V | a.ldx | a.ldb | a.ldc) % per == 0 && bits % 16 == 0;
+  return a.bf ? ssm::by_state<bf16>(a, stream) : ssm::by_state<float>(a, stream);
+}
+
+}  // namespace kda

@@ -451,9 +451,9 @@ int kda_chunk_fwd_noalloc(const void* q, const void* k, const void* v, const voi
  * must not overlap inputs (final_state not initial_state either). Nothing is allocated.
  */
 typedef enum {
-  KDA_CONV_SILU = 1, /* y = silu(pre); otherwise y = pre */
-  KDA_ZERO_REST = 2  /* set the output rows that lie in no sequence to zero */
-} kda_conv_flags;
+  KDA_CONV_SILU = 1, /* convolution: y = silu(pre); otherwise y = pre */
+  KDA_ZERO_REST = 2  /* convolution and scan: set the output rows that lie in no sequence to zero */
+} kda_layer_flags;
 
 int kda_conv_fwd(const void* x, int64_t x_stride, const float* weight, const float* bias,
                  const void* initial_state, const int* cu_seqlens, int N, void* final_state,
@@ -486,6 +486,62 @@ int kda_conv_bwd(const void* x, int64_t x_stride, const float* weight, const flo
 int kda_conv_step(const void* x, int64_t x_stride, const float* weight, const float* bias,
                   void* state_pool, const int* slots, int num_slots, void* y, int B, int D, int W,
                   unsigned flags, int dtype, void* stream);
+
+/*
+ * Selective state space scan with one scalar decay per value head, over whole sequences: the
+ * recurrence that hybrid stacks put beside the gated delta rule, on the same K x V float32 state.
+ * Its decay is the standard gate's form (K3 README, roadmap row L5), per head instead of per
+ * channel. Per value head hv, with D_t = softplus(dt_t + dt_bias):
+ *
+ *     S_t = exp(-exp(A_log) D_t) S_{t-1} + b_t (D_t x_t)^T
+ *     y_t = S_t^T c_t + D x_t
+ *
+ *   x              [T, HV, V]   dtype   the tokens of all sequences, x_stride elements apart
+ *   dt             [T, HV]      dtype   step sizes before the softplus
+ *   b, c           [T, H, K]    dtype   value head hv reads pair hv / (HV / H)
+ *   A_log          [HV]         float32
+ *   D, dt_bias     [HV]         float32, or NULL: zeros
+ *   initial_state  [N, HV, K, V] float32, or NULL: zeros
+ *   cu_seqlens     [N+1] int32 DEVICE memory (non-decreasing, within [0, T], empty sequences
+ *                  allowed), or NULL: N sequences of T / N tokens each (T % N == 0)
+ *   final_state    [N, HV, K, V] float32 out, or NULL; must not overlap initial_state
+ *   y              [T, HV, V]   dtype   out; rows in no sequence are left as they were, or set to
+ *                  zero with KDA_ZERO_REST in flags
+ *   *_stride       elements between tokens (>= one token's width, <= 2^24): x, b and c may be
+ *                  slices of one activation. Rows of whole 16-byte pieces, 16-byte aligned, are
+ *                  fastest; no alignment is required.
+ *   workspace      device memory of kda_ssm_chunk_fwd_workspace_size() bytes, 256-byte aligned,
+ *                  caller-owned, overwritten (packed: whether cu_seqlens is given); NULL where
+ *                  that size is 0
+ *
+ * The token axis is cut into equal segments that run side by side; a scan of the states at their
+ * boundaries joins them (as in kda_chunk_fwd_segmented). Results are bitwise reproducible.
+ * Constraints: N >= 1, T >= 0, HV % H == 0 (else KDA_ERR_INVALID); K, V <= 128, HV <= 2^16,
+ * N <= 2^20 (else KDA_ERR_UNSUPPORTED). Nothing is allocated.
+ */
+size_t kda_ssm_chunk_fwd_workspace_size(int N, int T, int packed, int H, int HV, int K, int V,
+                                        int dtype);
+
+int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride,
+                      const float* A_log, const void* b, int64_t b_stride, const void* c,
+                      int64_t c_stride, const float* D, const float* dt_bias,
+                      const float* initial_state, const int* cu_seqlens, int N,
+                      float* final_state, void* y, int T, int H, int HV, int K, int V,
+                      unsigned flags, int dtype, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/*
+ * One token of kda_ssm_chunk_fwd per request, on slot slots[n] of state_pool [num_slots, HV, K, V]
+ * (float32, updated in place): x [B, HV, V], dt [B, HV], b, c [B, H, K], y [B, HV, V] out. slots
+ * NULL: request n uses slot n (num_slots >= B). A request whose slot is outside [0, num_slots)
+ * gets y = 0 and changes no state; valid slots of one call must be distinct. Otherwise as
+ * kda_ssm_chunk_fwd, without the limit on strides.
+ */
+int kda_ssm_step(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride,
+                 const float* A_log, const void* b, int64_t b_stride, const void* c,
+                 int64_t c_stride, const float* D, const float* dt_bias, float* state_pool,
+                 const int* slots, int num_slots, void* y, int B, int H, int HV, int K, int V,
+                 int dtype, void* stream);
 
 /*
  * Slots of state pools (the caches of kda_recurrent_step_slots, kda_conv_step and kda_ssm_step):

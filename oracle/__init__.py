@@ -24,6 +24,7 @@ Three independent CPU formulations, all in float64 numpy:
   gradients.
 * ``conv`` / ``conv_bwd``: the short causal convolution in front of the recurrence, and
   its gradients.
+* ``selective_scan``: the selective state space scan with a scalar decay per head.
 * ``transforms``: the optional in-operator input transforms (q/k L2
   normalisation, beta sigmoid) that ``recurrent`` / ``decode_step`` apply on
   request.
@@ -40,6 +41,7 @@ from .transforms import l2_normalize, sigmoid
 from .backward import recurrent_bwd
 from .gate import gate, gate_bwd
 from .conv import conv, conv_bwd
+from .ssm import selective_scan
 
 __all__ = [
     "decode_step",
@@ -54,4 +56,5 @@ __all__ = [
     "gate_bwd",
     "conv",
     "conv_bwd",
+    "selective_scan",
 ]
