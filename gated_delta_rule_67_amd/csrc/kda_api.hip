@@ -628,7 +628,7 @@ int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* dt, int64_t d
   kda::SsmArgs a{};
   a.x = x, a.ldx = x_stride, a.dt = dt, a.lddt = dt_stride, a.A_log = A_log;
   a.b = b, a.ldb = b_stride, a.c = c, a.ldc = c_stride, a.D = D, a.dt_bias = dt_bias;
-  a.s0 = initial_state, a.cu = cu_seqlens, a.N = N, a.T = T, a.H = H, a.HV = HV, a.K = K, a.V = V;
+  a.s0 = initial_state, a.seqs = kda::make_sequences(cu_seqlens, N, T), a.N = N, a.T = T, a.H = H, a.HV = HV, a.K = K, a.V = V;
   a.sT = final_state, a.y = y, a.bf = dtype == KDA_DTYPE_BF16, a.zero_rest = (flags & KDA_ZERO_REST) != 0;
   const hipError_t e = kda::launch_ssm_prefill(a, workspace, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;

@@ -52,7 +52,7 @@ struct Args {
   const float* weight; // [D, W]
   const float* bias;   // [D] or null
   const void* init;    // [N, W-1, D] or null
-  const int* cu;       // [N+1] or null: N sequences of T / N tokens
+  Sequences seqs;
   int N, T, D;
   int silu, zero_rest;
   int64_t rpb;         // rows per row block
@@ -109,7 +109,7 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a) {
   if ((int)blockIdx.y >= a.nrb) {  // final states: the last W - 1 rows of (state ; sequence)
     const int n = ((int)blockIdx.y - a.nrb) * kSlices + slice;
     if (n >= a.N || !active) return;
-    const Span s = sequence_span(a.cu, a.N, a.T, n);
+    const Span s = a.seqs.span(n);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
       *reinterpret_cast<vec_t*>(static_cast<T*>(a.out_state) + ((int64_t)n * (W - 1) + j) * a.D + col) =
@@ -122,14 +122,14 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a) {
   int r = rb0 + slice * q;
   const int r1 = min(r + q, rb1);
   if (r >= r1) return;
-  int seq = find_sequence(a.cu, a.N, a.T, r);  // uses every lane of the wave
+  int seq = a.seqs.find(r);  // uses every lane of the wave
   if (!active) return;
   float w[W][VEC], b[VEC];
   load_taps<VEC, W>(a, col, w, b);
   const T* x = static_cast<const T*>(a.x) + col;
   T* y = static_cast<T*>(a.out) + col;
   while (r < r1 && seq < a.N) {
-    const Span s = sequence_span(a.cu, a.N, a.T, seq);
+    const Span s = a.seqs.span(seq);
     if (s.eos <= r) { ++seq; continue; }
     if (s.bos > r) {  // rows in front of the first sequence
       outside<T, VEC>(a, r, min(s.bos, r1), col);
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a) {
   if ((int)blockIdx.y >= a.nrb) {  // empty sequences: the state's gradient passes through
     const int n = ((int)blockIdx.y - a.nrb) * kSlices + slice;
     if (n >= a.N || !active) return;
-    const Span s = sequence_span(a.cu, a.N, a.T, n);
+    const Span s = a.seqs.span(n);
     if (s.eos > s.bos) return;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
@@ -217,14 +217,14 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a) {
   const int q = (rb1 - rb0 + kSlices - 1) / kSlices;
   int r = min(rb0 + slice * q, rb1);
   const int r1 = min(r + q, rb1);
-  int seq = r < r1 ? find_sequence(a.cu, a.N, a.T, r) : a.N;
+  int seq = r < r1 ? a.seqs.find(r) : a.N;
   if (active && r < r1) {
     float w[W][VEC], b[VEC];
     load_taps<VEC, W>(a, col, w, b);
     const T* x = static_cast<const T*>(a.x) + col;
     const T* dy = static_cast<const T*>(a.dy) + col;
     while (r < r1 && seq < a.N) {
-      const Span s = sequence_span(a.cu, a.N, a.T, seq);
+      const Span s = a.seqs.span(seq);
       if (s.eos <= r) { ++seq; continue; }
       if (s.bos > r) {
         outside<T, VEC>(a, r, min(s.bos, r1), col);
@@ -523,7 +523,7 @@ size_t conv_bwd_workspace_bytes(int T, int D, int W, bool bf) {
 
 hipError_t launch_conv_fwd(const ConvArgs& p, hipStream_t stream) {
   conv::Args a{};
-  a.x = p.x, a.ldx = p.ldx, a.weight = p.weight, a.bias = p.bias, a.init = p.init, a.cu = p.cu;
+  a.x = p.x, a.ldx = p.ldx, a.weight = p.weight, a.bias = p.bias, a.init = p.init, a.seqs = make_sequences(p.cu, p.N, p.T);
   a.N = p.N, a.T = p.T, a.D = p.D, a.silu = p.silu, a.zero_rest = p.zero_rest, a.out_state = p.out_state, a.out = p.out;
   const void* ptrs[] = {p.x, p.init, p.out_state, p.out};
   const int vec = conv::vec_of(p.bf ? 2 : 4, p.D, p.ldx, ptrs, 4);
@@ -533,7 +533,7 @@ hipError_t launch_conv_fwd(const ConvArgs& p, hipStream_t stream) {
 hipError_t launch_conv_bwd(const ConvArgs& p, const void* dy, int64_t lddy, const void* dfinal,
                            float* dweight, float* dbias, void* workspace, hipStream_t stream) {
   conv::Args a{};
-  a.x = p.x, a.ldx = p.ldx, a.weight = p.weight, a.bias = p.bias, a.init = p.init, a.cu = p.cu;
+  a.x = p.x, a.ldx = p.ldx, a.weight = p.weight, a.bias = p.bias, a.init = p.init, a.seqs = make_sequences(p.cu, p.N, p.T);
   a.N = p.N, a.T = p.T, a.D = p.D, a.silu = p.silu, a.zero_rest = p.zero_rest, a.out_state = p.out_state, a.out = p.out;
   a.dy = dy, a.lddy = lddy, a.dfinal = dfinal, a.part = static_cast<float*>(workspace);
   const void* ptrs[] = {p.x, p.init, p.out_state, p.out, dy, dfinal};

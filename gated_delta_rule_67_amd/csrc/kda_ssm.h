@@ -18,7 +18,7 @@ struct SsmArgs {
   const float* D;        // [HV] or null
   const float* dt_bias;  // [HV] or null
   const float* s0;       // [N, HV, K, V] or null
-  const int* cu;         // [N+1] or null: N sequences of T / N tokens
+  Sequences seqs;
   int N, T, H, HV, K, V;
   float* sT;             // [N, HV, K, V] or null
   void* y;               // [T, HV, V]

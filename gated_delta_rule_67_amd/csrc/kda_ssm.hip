@@ -28,7 +28,7 @@ namespace ssm {
 // Tokens of a tile. float32 takes half as many: its products are 16 times as expensive, and those
 // inside a tile grow with it.
 template <typename T> constexpr int kTokens = sizeof(T) == 2 ? 64 : 32;
-constexpr int kThreads = 256;
+constexpr int kCompose = 256;  // threads of a composing workgroup
 constexpr unsigned kOutOfRange = 0x80000000u;  // buffer loads there read zeros
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -65,17 +65,17 @@ __device__ __forceinline__ f32x4 mfma(float a, float b, f32x4 c) {
 
 // A tile: tokens t0 .. t0 + rows - 1 of sequence seq; first / last: holds its first / last token.
 struct Tile {
-  int t0, rows, seq;
+  int t0, rows, seq, eos;  // eos: the sequence's end
   bool first, last;
 };
 
 // A ROWS x COLS matrix on its way from memory to LDS: each thread holds pieces of 16 bytes.
 // Columns are blocks of PAD, of which `width` are real. VEC: every real row of a block is whole
 // 16-byte pieces, aligned in memory.
-template <typename T, int ROWS, int COLS, int PAD, bool VEC>
+template <typename T, int THREADS, int ROWS, int COLS, int PAD, bool VEC>
 struct Stage {
-  static constexpr int kElem = 16 / sizeof(T), kRow = COLS / kElem, kPieces = ROWS * kRow / kThreads;
-  static_assert(kPieces * kThreads == ROWS * kRow, "every thread holds the same number of pieces");
+  static constexpr int kElem = 16 / sizeof(T), kRow = COLS / kElem, kPieces = ROWS * kRow / THREADS;
+  static_assert(kPieces * THREADS == ROWS * kRow, "every thread holds the same number of pieces");
   u32x4 v[kPieces];
 
   // src: row 0, column 0; ld: elements between rows; rows behind `rows` and columns behind
@@ -83,11 +83,11 @@ struct Stage {
   __device__ __forceinline__ void load(const T* src, int64_t ld, int rows, int width) {
     constexpr int kBlocks = COLS / PAD;
     const __amdgpu_buffer_rsrc_t r =
-        make_rsrc(src, (unsigned)((((int64_t)rows - 1) * ld + (int64_t)kBlocks * width) * sizeof(T)));
+        make_rsrc(src, rows ? (unsigned)((((int64_t)rows - 1) * ld + (int64_t)kBlocks * width) * sizeof(T)) : 0u);
     const unsigned rowb = (unsigned)(ld * sizeof(T));
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
-      const int piece = threadIdx.x + kThreads * e, row = piece / kRow, c = piece % kRow * kElem;
+      const int piece = threadIdx.x + THREADS * e, row = piece / kRow, c = piece % kRow * kElem;
       const int blk = c / PAD, p = c - blk * PAD;
       const unsigned off = (unsigned)row * rowb + (unsigned)(blk * width + p) * sizeof(T);
       auto in = [&](int k) { return p + k < width ? off + k * (unsigned)sizeof(T) : kOutOfRange; };
@@ -110,63 +110,113 @@ struct Stage {
   __device__ __forceinline__ void store(T* dst, int ldd) const {
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
-      const int piece = threadIdx.x + kThreads * e, row = piece / kRow, c = piece % kRow * kElem;
+      const int piece = threadIdx.x + THREADS * e, row = piece / kRow, c = piece % kRow * kElem;
       *reinterpret_cast<u32x4*>(dst + row * ldd + c) = v[e];
     }
   }
 };
 
-// Per token and head of a tile.
+// Per token and head of a tile: what the state's products take, and what M takes. Exponents are of
+// differences of G in float64.
 struct Decay {
-  float dt[64], hi[64], lo[64];  // D, and G as a sum of two floats (log2 units)
-  float eg[64], w[64];           // 2^G, and D 2^(G_63 - G)
-  float ghi, glo;                // G_63, the whole tile's
+  float eg[64], w[64];  // 2^G, and D 2^(G_63 - G)
+  float end, pad[3];    // G_63, the whole tile's
 };
+struct Inner {
+  float dt[64], hi[64], lo[64];  // D, and G as a sum of two floats (log2 units)
+  // between blocks of 16 tokens, over the last token q = 16 it - 1 in front of block it:
+  // row[i] = 2^(G_i - G_q) for i in it, col[8 it (it - 1) + j] = D_j 2^(G_q - G_j) for j <= q
+  float row[64], col[96];
+};
+
+// v of the lane `OP` names (a DPP control); lanes without one, or masked out, get 0.
+template <int OP, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)u, OP, ROWS, 0xf, false);
+  const unsigned hi = __builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), OP, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ double read_lane(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)u, lane);
+  const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 
 // One wave: lane = token (those behind the tile's rows have D = 0). G is summed in float64, so
 // that differences of two of its values keep float32 accuracy however large both are.
-__device__ __forceinline__ void make_decay(Decay& d, float raw, bool in, float bias, float neg_rate) {
+// BLOCKS: also what joins blocks of 16 tokens.
+template <bool OUT, bool BLOCKS>
+__device__ __forceinline__ void make_decay(Decay& d, Inner& m, float raw, bool in, float bias, float neg_rate) {
   const int lane = __lane_id();
   float e, r;
   const float dt = in ? softplus_f32(raw + bias, e, r) : 0.f;
   double g = (double)(neg_rate * dt) * 1.4426950408889634;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const double up = __shfl_up(g, off);
-    g += lane >= off ? up : 0.0;
-  }
-  const double end = __shfl(g, 63);
-  const float hi = (float)g;
-  d.dt[lane] = dt;
-  d.hi[lane] = hi;
-  d.lo[lane] = (float)(g - (double)hi);
-  d.eg[lane] = fast_exp2(hi);
+  g += dpp_or_zero<0x111, 0xf>(g);  // inclusive sums within rows of 16 lanes: shifts by 1, 2, 4, 8
+  g += dpp_or_zero<0x112, 0xf>(g);
+  g += dpp_or_zero<0x114, 0xf>(g);
+  g += dpp_or_zero<0x118, 0xf>(g);
+  g += dpp_or_zero<0x142, 0xa>(g);  // lane 15 of rows 0 and 2 to rows 1 and 3
+  g += dpp_or_zero<0x143, 0xc>(g);  // lane 31 to rows 2 and 3
+  const double end = read_lane(g, 63);
   d.w[lane] = dt * fast_exp2((float)(end - g));
-  if (lane == 63) {
-    d.ghi = hi;
-    d.glo = d.lo[63];
+  if (lane == 0) d.end = (float)end;
+  if constexpr (OUT) {
+    const float hi = (float)g;
+    d.eg[lane] = fast_exp2(hi);
+    m.dt[lane] = dt;
+    m.hi[lane] = hi;
+    m.lo[lane] = (float)(g - (double)hi);
+  }
+  if constexpr (BLOCKS) {
+    double before = 0.0;  // G of the token in front of this lane's block
+#pragma unroll
+    for (int it = 1; it < 4; ++it) {
+      const double q = read_lane(g, 16 * it - 1);
+      if (lane < 16 * it) m.col[8 * it * (it - 1) + lane] = dt * fast_exp2((float)(q - g));
+      else before = q;
+    }
+    m.row[lane] = fast_exp2((float)(g - before));
   }
 }
 
+// Two floats rounded to bf16 in one register, and back.
+__device__ __forceinline__ unsigned pack2(float a, float b) {
+  return __builtin_bit_cast(unsigned, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+__device__ __forceinline__ float low(unsigned u) { return __builtin_bit_cast(float, u << 16); }
+__device__ __forceinline__ float high(unsigned u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
+
+// Waves of a workgroup: 16 PT columns each, four at least.
+template <int PP, int HB, int PT> constexpr int kWaves = PP * HB > 64 * PT ? PP * HB / (16 * PT) : 4;
+
 // NT: K in tiles of 16; HB heads of PP columns; PT tiles of 16 columns a wave.
 template <typename T, int NT, int PP, int HB, int PT, bool OUT, bool VEC>
-__global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hblocks) {
+__global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8 ? 4 : 2)) void prefill_kernel(SsmArgs a, int hblocks) {
+  constexpr int NW = kWaves<PP, HB, PT>, kThreads = 64 * NW;
   constexpr bool BF = sizeof(T) == 2;
   constexpr int kTok = kTokens<T>, kPad = 16 / sizeof(T);
-  constexpr int XC = HB * PP, NP = 16 * NT, LDN = NP + kPad, LDX = XC + kPad, LDM = kTok + kPad, KS = NT / 2;
-  static_assert(XC <= 64 * PT && NT % 2 == 0 && PP % (16 * PT) == 0, "tile shape");
+  constexpr int XC = HB * PP, NP = 16 * NT, LDX = XC + kPad, LDM = kTok + kPad, KS = NT / 2;
+  // rows of b and c in LDS: c is read 16 bytes a lane along rows, b also four rows at a time; the
+  // row lengths with the fewest bank conflicts for these (cycles of a 1 KB read: c 4 instead of 6
+  // at 272 bytes a row, b 6 and, transposed, 3.4 instead of 6)
+  constexpr int LDC = BF ? NP + 16 : NP + 4, LDB = BF ? (NT == 8 ? 160 : 104) : NP + 4;
+  static_assert(XC <= 16 * PT * NW && NT % 2 == 0 && PP % (16 * PT) == 0, "tile shape");
   __shared__ __attribute__((aligned(16))) T Xs[kTok * LDX];
-  __shared__ __attribute__((aligned(16))) T Bs[kTok * LDN];
-  __shared__ __attribute__((aligned(16))) T Cs[OUT ? kTok * LDN : 8];
+  __shared__ __attribute__((aligned(16))) T Bs[kTok * LDB];
+  __shared__ __attribute__((aligned(16))) T Cs[OUT ? kTok * LDC : 8];
   __shared__ __attribute__((aligned(16))) T Ms[OUT ? HB * kTok * LDM : 8];
   __shared__ __attribute__((aligned(16))) Decay s_dec[2][HB];
+  __shared__ __attribute__((aligned(16))) Inner s_in[OUT ? HB : 1];  // read in front of a tile's second barrier only
 
   const int K = a.K, V = a.V, vblocks = (V + PP - 1) / PP;
   const int main_blocks = hblocks * (OUT ? a.nseg : a.nseg - 1);
   int bid = blockIdx.x;
   if (OUT && bid >= main_blocks) {  // empty sequences: the state passes through
     const int n = bid - main_blocks;
-    const Span s = sequence_span(a.cu, a.N, a.T, n);
+    const Span s = a.seqs.span(n);
     if (s.eos > s.bos) return;
     const int64_t sz = (int64_t)a.HV * K * V;
     for (int64_t i = threadIdx.x; i < sz; i += kThreads) a.sT[n * sz + i] = a.s0 ? a.s0[n * sz + i] : 0.f;
@@ -181,21 +231,22 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
   const int grp = h0 / (a.HV / a.H);
 
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lr = lane & 15, lq = lane >> 4;
+  int lr = lane & 15, lq = lane >> 4;
   const int col0 = wv * 16 * PT, hh = col0 / PP, p0 = v0 + col0 - hh * PP;
-  const bool active = hh < HB;  // waves behind the last head only help with the products c . b
+  const bool active = XC == 16 * PT * NW || hh < HB;  // waves behind the last head only help with c . b
   const int hv = h0 + (active ? hh : 0);
+  const int dw = wv - (NW - HB);  // the last HB waves prepare the decays of head dw
 
   const int seg0 = segk * a.seg;
   const int end = (int)min((int64_t)seg0 + a.seg, (int64_t)a.T);
   int pos = seg0, seq;
   bool carry = true;  // OUT = false: the state entering the segment reaches its end
   if constexpr (OUT) {
-    seq = find_sequence(a.cu, a.N, a.T, seg0);
+    seq = a.seqs.find(seg0);
   } else {
     // only the part of the sequence that goes on behind the segment's end
-    seq = find_sequence(a.cu, a.N, a.T, end - 1);
-    const Span s = sequence_span(a.cu, a.N, a.T, seq);
+    seq = a.seqs.find(end - 1);
+    const Span s = a.seqs.span(seq);
     if (s.eos <= end || s.bos >= end) {
       if (wv == 0 && lane < HB && v0 == 0) a.seg_g[(int64_t)segk * a.HV + h0 + lane] = kNoCarry;
       return;
@@ -209,13 +260,13 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
   // the tile at or behind token t: rows == 0 if the segment holds none
   auto tile_at = [&](int t, int s) {
     while (t < end && s < a.N) {
-      const Span sp = sequence_span(a.cu, a.N, a.T, s);
+      const Span sp = a.seqs.span(s);
       if (sp.eos <= t) { ++s; continue; }
       if (sp.bos > t) { t = sp.bos; continue; }
       const int rows = min(kTok, min(sp.eos, end) - t);
-      return Tile{t, rows, s, t == sp.bos, t + rows == sp.eos};
+      return Tile{t, rows, s, sp.eos, t == sp.bos, t + rows == sp.eos};
     }
-    return Tile{end, 0, s, false, false};
+    return Tile{end, 0, s, end, false, false};
   };
   // rows [t, to) lie in no sequence
   auto outside = [&](int t, int to) {
@@ -225,39 +276,58 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
         y[t * ldy + (int64_t)(h0 + i / width) * V + v0 + i % width] = from_f32<T>(0.f);
   };
 
-  Stage<T, kTok, XC, PP, VEC> xr;
-  Stage<T, kTok, NP, NP, VEC> br, cr;
+  Stage<T, kThreads, kTok, XC, PP, VEC> xr;
+  Stage<T, kThreads, kTok, NP, NP, VEC> br, cr;
   T dtr = from_f32<T>(0.f);
   auto load = [&](const Tile& t) {
     xr.load(static_cast<const T*>(a.x) + (int64_t)t.t0 * a.ldx + (int64_t)h0 * V + v0, a.ldx, t.rows, width);
     br.load(static_cast<const T*>(a.b) + (int64_t)t.t0 * a.ldb + (int64_t)grp * K, a.ldb, t.rows, K);
     if constexpr (OUT)
       cr.load(static_cast<const T*>(a.c) + (int64_t)t.t0 * a.ldc + (int64_t)grp * K, a.ldc, t.rows, K);
-    if (wv < HB && lane < t.rows)
-      dtr = static_cast<const T*>(a.dt)[(int64_t)(t.t0 + lane) * a.lddt + h0 + wv];
+    const __amdgpu_buffer_rsrc_t rd = make_rsrc(static_cast<const T*>(a.dt) + (int64_t)t.t0 * a.lddt + h0, 0x7fffffffu);
+    const unsigned off = dw >= 0 && lane < t.rows ? (unsigned)(lane * a.lddt + dw) * (unsigned)sizeof(T) : kOutOfRange;
+    if constexpr (BF) dtr = __builtin_bit_cast(T, (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(rd, off, 0, 0));
+    else dtr = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(rd, off, 0, 0));
   };
   float bias = 0.f, neg_rate = 0.f;
-  if (wv < HB) {  // wave w prepares the decays of head w
-    bias = a.dt_bias ? a.dt_bias[h0 + wv] : 0.f;
-    neg_rate = -expf(a.A_log[h0 + wv]);
+  if (dw >= 0) {
+    bias = a.dt_bias ? a.dt_bias[h0 + dw] : 0.f;
+    neg_rate = -expf(a.A_log[h0 + dw]);
   }
   const float skip = a.D ? a.D[hv] : 0.f;
 
-  f32x4 S[PT][NT];  // rows 16 nt + 4 lq .. + 3, column 16 pt + lr of the wave's
+  // column 16 pt + lr of the wave's; rows 16 nt + 4 lq .. + 3, or, for bf16, in the order in which
+  // two tiles make an operand of the next product: 32 (nt / 2) + 8 lq + 4 (nt % 2) .. + 3
+  f32x4 S[PT][NT];
+  // this wave's part of a [K, V] float32 state in memory; elements outside of it read zeros and
+  // are not written
   auto each_state = [&](auto f) {
     if (!active) return;
+    int n = (BF ? 8 : 4) * lq;
+    asm volatile("" : "+v"(n));  // the offsets are made here, not kept over the tile loop
 #pragma unroll
     for (int pt = 0; pt < PT; ++pt) {
-      int p = p0 + 16 * pt + lr;
-      asm volatile("" : "+v"(p));  // the addresses are made here, not kept over the tile loop
+      const int p = p0 + 16 * pt + lr;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int n = 16 * nt + 4 * lq + r;
-          if (n < K && p < V) S[pt][nt][r] = f(S[pt][nt][r], (int64_t)n * V + p);
-        }
+        for (int r = 0; r < 4; ++r)
+          f(pt, nt, r, p < V ? (unsigned)(((BF ? nt / 2 * 32 + nt % 2 * 4 : 16 * nt) + n + r) * V + p) * 4u : kOutOfRange);
     }
+  };
+  const unsigned state_bytes = (unsigned)(K * V * 4);
+  auto load_state = [&](const float* src) {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(src, state_bytes);
+    each_state([&](int pt, int nt, int r, unsigned off) {
+      S[pt][nt][r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
+    });
+  };
+  auto store_state = [&](float* dst) {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(dst, state_bytes);
+    each_state([&](int pt, int nt, int r, unsigned off) {
+      const float v = S[pt][nt][r];
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), rs, off, 0, 0);
+    });
   };
   auto zero_state = [&] {
 #pragma unroll
@@ -268,9 +338,16 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
   const int64_t sz = (int64_t)K * V;
   zero_state();
   if constexpr (OUT) {
-    if (segk > 0 && sequence_span(a.cu, a.N, a.T, seq).bos < seg0) {
-      const float* src = a.seg_state + ((int64_t)(segk - 1) * a.HV + hv) * sz;
-      each_state([&](float, int64_t i) { return src[i]; });
+    if (segk > 0 && a.seqs.span(seq).bos < seg0) {
+      load_state(a.seg_state + ((int64_t)(segk - 1) * a.HV + hv) * sz);
+    }
+  }
+
+  if constexpr (OUT && BF) {  // the blocks above the diagonal: (i, j) = (0, 1) and (2, 3)
+    const int i = threadIdx.x / 16 % 16, j = threadIdx.x % 16;
+    for (int h = 0; h < HB; ++h) {
+      Ms[(h * kTok + i) * LDM + 16 + j] = from_f32<T>(0.f);
+      Ms[(h * kTok + 32 + i) * LDM + 48 + j] = from_f32<T>(0.f);
     }
   }
 
@@ -278,64 +355,95 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
   outside(pos, cur.t0);
   if (cur.rows == 0) return;
   load(cur);
-  if (wv < HB)
-    make_decay(s_dec[0][wv], to_f32(dtr), lane < cur.rows, bias, neg_rate);
-  double gsum = 0.0;
+  if (dw >= 0)
+    make_decay<OUT, OUT && BF>(s_dec[0][dw], s_in[OUT ? dw : 0], to_f32(dtr), lane < cur.rows, bias, neg_rate);
+  float gsum = 0.f;
 
+  __builtin_amdgcn_s_waitcnt(0);  // the first tile's loads, so that the wait in the loop is that of later ones
   for (int buf = 0;; buf ^= 1) {
     xr.store(Xs, LDX);
-    br.store(Bs, LDN);
-    if constexpr (OUT) cr.store(Cs, LDN);
+    br.store(Bs, LDB);
+    if constexpr (OUT) cr.store(Cs, LDC);
     lds_barrier();
-    const Tile nxt = cur.t0 + cur.rows < end ? tile_at(cur.t0 + cur.rows, cur.seq) : Tile{end, 0, cur.seq, false, false};
-    outside(cur.t0 + cur.rows, nxt.t0);
-    if (nxt.rows) load(nxt);
-
+    const int done = cur.t0 + cur.rows;
+    Tile nxt = {done, min(kTok, min(cur.eos, end) - done), cur.seq, cur.eos, false, false};
+    if (nxt.rows > 0) {
+      nxt.last = done + nxt.rows == cur.eos;
+    } else {
+      nxt = tile_at(done, cur.seq);
+      outside(done, nxt.t0);
+    }
     if (cur.first) {  // the sequence's initial state
       zero_state();
       if (a.s0) {
-        const float* src = a.s0 + ((int64_t)cur.seq * a.HV + hv) * sz;
-        each_state([&](float, int64_t i) { return src[i]; });
+        load_state(a.s0 + ((int64_t)cur.seq * a.HV + hv) * sz);
+        // waited for here: a wait behind the branch would cover the loads of every next tile too
+        __builtin_amdgcn_s_waitcnt(0);
       }
     }
+    if constexpr (!OUT) load(nxt);
+
     const Decay* dec = s_dec[buf];
+    // lane addresses are made anew in every tile: kept over the loop they would not fit the registers
+    asm volatile("" : "+v"(lr), "+v"(lq));
 
     if constexpr (OUT) {
-      // c . b transposed (rows j, columns i), then M of each head. bf16: a wave takes the 16
-      // tokens i of its number and all j up to theirs; float32: wave 0, 1 and 2 one tile each.
-      const int it = BF ? wv : (wv + 1) / 2, i = 16 * it + lr;
-      bf16x8 cf[BF ? KS : 1];
-      if constexpr (BF) {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) cf[ks] = *reinterpret_cast<const bf16x8*>(Cs + i * LDN + 32 * ks + 8 * lq);
+      // c . b transposed (rows j, columns i) in blocks of 16, then M of each head. The blocks at
+      // and below the diagonal, dealt out evenly; those above are read as part of a product of 32
+      // tokens only where they are zeros from the start.
+      constexpr int kBlocks = !BF ? 1 : NW == 8 ? 2 : 3;  // a wave's blocks: i and j, four bits each, lowest first
+      int fresh = 0;
+      asm volatile("" : "+v"(fresh));  // as above: made in every tile
+      const int wv = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) + fresh);
+      unsigned its, jts;
+      if constexpr (!BF) {
+        its = wv == 0 ? 0x0 : wv < 3 ? 0x1 : 0xf;
+        jts = wv == 2 ? 0x1 : 0x0;
+      } else if constexpr (NW == 8) {
+        its = wv == 0 ? 0x33 : wv == 1 ? 0x22 : wv < 6 ? 0xf0 | (wv - 2) : wv == 6 ? 0xf3 : 0xf1;
+        jts = wv < 2 ? 0x10 : wv < 6 ? 0xf0 | (wv - 2) : wv == 6 ? 0xf2 : 0xf0;
+      } else {
+        its = wv == 0 ? 0x033 : wv == 1 ? 0x122 : wv == 2 ? 0xf33 : 0xf21;
+        jts = wv == 0 ? 0x010 : wv == 1 ? 0x110 : wv == 2 ? 0xf32 : 0xf20;
       }
-      const int jt0 = BF ? 0 : wv / 2, jt1 = BF ? (wv | 1) : (wv < 3 ? jt0 : jt0 - 1);
-      for (int jt = jt0; jt <= jt1; ++jt) {
-        f32x4 sc = {0.f, 0.f, 0.f, 0.f};
-        if (jt <= it) {  // tiles above the diagonal that a product of 32 tokens reads are zeros
-          if constexpr (BF) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-              sc = mfma(*reinterpret_cast<const bf16x8*>(Bs + (16 * jt + lr) * LDN + 32 * ks + 8 * lq), cf[ks], sc);
-          } else {
+      for (int k = 0; k < kBlocks; ++k) {
+        const int it = its >> 4 * k & 15, jt = jts >> 4 * k & 15;
+        if (it == 15) continue;
+        const int i = 16 * it + lr, j = 16 * jt + 4 * lq;
+        f32x4 sc = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (BF) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+            sc = mfma(*reinterpret_cast<const bf16x8*>(Bs + (16 * jt + lr) * LDB + 32 * ks + 8 * lq),
+                      *reinterpret_cast<const bf16x8*>(Cs + i * LDC + 32 * ks + 8 * lq), sc);
+        } else {
 #pragma unroll 4
-            for (int k = lq; k < NP; k += 4) sc = mfma(Bs[(16 * jt + lr) * LDN + k], Cs[i * LDN + k], sc);
-          }
+          for (int n = lq; n < NP; n += 4) sc = mfma(Bs[(16 * jt + lr) * LDB + n], Cs[i * LDC + n], sc);
         }
-        const int j = 16 * jt + 4 * lq;
 #pragma unroll
         for (int h = 0; h < HB; ++h) {
-          const f32x4 hj = *reinterpret_cast<const f32x4*>(dec[h].hi + j), lj = *reinterpret_cast<const f32x4*>(dec[h].lo + j);
-          const f32x4 dj = *reinterpret_cast<const f32x4*>(dec[h].dt + j);
-          const float hi = dec[h].hi[i], lo = dec[h].lo[i];
-          T m[4];
+          f32x4 m;
+          if (BF && jt < it) {
+            m = sc * *reinterpret_cast<const f32x4*>(&s_in[h].col[8 * it * (it - 1) + j]) * s_in[h].row[i];
+          } else {
+            const f32x4 hj = *reinterpret_cast<const f32x4*>(s_in[h].hi + j), lj = *reinterpret_cast<const f32x4*>(s_in[h].lo + j);
+            const f32x4 dj = *reinterpret_cast<const f32x4*>(s_in[h].dt + j);
+            const float hi = s_in[h].hi[i], lo = s_in[h].lo[i];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float w = sc[r] * dj[r] * fast_exp2((hi - hj[r]) + (lo - lj[r]));
-            m[r] = from_f32<T>(j + r <= i ? w : 0.f);
+            for (int r = 0; r < 4; ++r) {
+              // j > i gives a positive exponent, possibly inf: not taken
+              const float v = sc[r] * dj[r] * fast_exp2((hi - hj[r]) + (lo - lj[r]));
+              m[r] = j + r <= i ? v : 0.f;
+            }
           }
-          typedef T vec4 __attribute__((ext_vector_type(4)));
-          *reinterpret_cast<vec4*>(Ms + (h * kTok + i) * LDM + j) = vec4{m[0], m[1], m[2], m[3]};
+          T* dst = Ms + (h * kTok + i) * LDM + j;
+          if constexpr (BF) {
+            typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+            *reinterpret_cast<u32x2*>(dst) = u32x2{pack2(m[0], m[1]), pack2(m[2], m[3])};
+          } else {
+            *reinterpret_cast<f32x4*>(dst) = m;
+          }
         }
       }
       lds_barrier();
@@ -343,22 +451,31 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
 
     if (active) {
       // y of 16 tokens and this wave's columns (rows p), from accumulators that hold it transposed
+      const unsigned yrow = (unsigned)(ldy * sizeof(T));
+      const __amdgpu_buffer_rsrc_t yb = make_rsrc(y + (int64_t)cur.t0 * ldy + (int64_t)hv * V, 0x7fffffffu);
       auto store_y = [&](int i, const f32x4 (&acc)[PT]) {
-        if (i >= cur.rows) return;
-        T* yr = y + (int64_t)(cur.t0 + i) * ldy + (int64_t)hv * V;
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) {
           const int p = p0 + 16 * pt + 4 * lq;
-          typedef T vec4 __attribute__((ext_vector_type(4)));
-          vec4 o;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) o[r] = from_f32<T>(acc[pt][r]);
+          const unsigned off = (unsigned)i * yrow + (unsigned)p * sizeof(T);
           if constexpr (VEC) {
-            if (p < V) *reinterpret_cast<vec4*>(yr + p) = o;
+            unsigned at = i < cur.rows && p < V ? off : kOutOfRange;
+            asm volatile("" : "+v"(at));  // stays a select: a branch would leave the number of stores open
+            if constexpr (BF) {
+              typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+              const u32x2 o = {pack2(acc[pt][0], acc[pt][1]), pack2(acc[pt][2], acc[pt][3])};
+              __builtin_amdgcn_raw_buffer_store_b64(o, yb, at, 0, 0);
+            } else {
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[pt]), yb, at, 0, 0);
+            }
           } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (p + r < V) yr[p + r] = o[r];
+            for (int r = 0; r < 4; ++r) {
+              const unsigned at = i < cur.rows && p + r < V ? off + r * (unsigned)sizeof(T) : kOutOfRange;
+              const T o = from_f32<T>(acc[pt][r]);
+              if constexpr (BF) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, o), yb, at, 0, 0);
+              else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, o), yb, at, 0, 0);
+            }
           }
         }
       };
@@ -371,7 +488,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
           for (int r = 0; r < 4; ++r)
             acc[pt][r] = acc[pt][r] * eg + skip * to_f32(Xs[i * LDX + col0 + 16 * pt + 4 * lq + r]);
       };
-      const float ga = fast_exp2(dec[hh].ghi);
+      const float ga = fast_exp2(dec[hh].end);
       if constexpr (BF) {
         // x of this wave's columns, transposed: rows p, 8 tokens a lane
         bf16x8 xf[PT][2];
@@ -383,18 +500,15 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
             xf[pt][ks] = join(load_tr4(src), load_tr4(src + 4 * LDX));
           }
         if constexpr (OUT) {
-          // S^T as an operand: k slots 8 lq + e hold state rows 32 ks + 4 lq + e (e < 4) and
-          // 32 ks + 16 + 4 lq + e - 4
-          bf16x8 sf[PT][KS];
+          bf16x8 sf[PT][KS];  // S^T as an operand
 #pragma unroll
           for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                sf[pt][ks][e] = from_f32<bf16>(S[pt][2 * ks][e]);
-                sf[pt][ks][e + 4] = from_f32<bf16>(S[pt][2 * ks + 1][e]);
-              }
+            for (int ks = 0; ks < KS; ++ks) {
+              const f32x4 a0 = S[pt][2 * ks], a1 = S[pt][2 * ks + 1];
+              sf[pt][ks] = __builtin_bit_cast(bf16x8, u32x4{pack2(a0[0], a0[1]), pack2(a0[2], a0[3]),
+                                                            pack2(a1[0], a1[1]), pack2(a1[2], a1[3])});
+            }
 #pragma unroll
           for (int it = 0; it < kTok / 16; ++it) {
             const int i = 16 * it + lr;
@@ -403,8 +517,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
             for (int pt = 0; pt < PT; ++pt) acc[pt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-              const bf16* src = Cs + i * LDN + 32 * ks + 4 * lq;
-              const bf16x8 cv = join(*reinterpret_cast<const bf16x4*>(src), *reinterpret_cast<const bf16x4*>(src + 16));
+              const bf16x8 cv = *reinterpret_cast<const bf16x8*>(Cs + i * LDC + 32 * ks + 8 * lq);
 #pragma unroll
               for (int pt = 0; pt < PT; ++pt) acc[pt] = mfma(sf[pt][ks], cv, acc[pt]);
             }
@@ -418,6 +531,8 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
             store_y(i, acc);
           }
         }
+        // the next tile's loads go out here: their registers are free only now
+        if constexpr (OUT) load(nxt);
         // the state's update
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt)
@@ -425,28 +540,33 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
           for (int nt = 0; nt < NT; ++nt) S[pt][nt] *= ga;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          bf16x8 w0[PT], w1[PT], w2[PT];
+          u32x4 w0[PT], w1[PT], w2[PT];
           const f32x4 wa = *reinterpret_cast<const f32x4*>(dec[hh].w + 32 * ks + 8 * lq);
           const f32x4 wb = *reinterpret_cast<const f32x4*>(dec[hh].w + 32 * ks + 8 * lq + 4);
 #pragma unroll
-          for (int pt = 0; pt < PT; ++pt)
+          for (int pt = 0; pt < PT; ++pt) {
+            const u32x4 xu = __builtin_bit_cast(u32x4, xf[pt][ks]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float v = to_f32(xf[pt][ks][e]) * (e < 4 ? wa[e & 3] : wb[e & 3]);
-              w0[pt][e] = from_f32<bf16>(v);
-              const float v1 = v - to_f32(w0[pt][e]);
-              w1[pt][e] = from_f32<bf16>(v1);
-              w2[pt][e] = from_f32<bf16>(v1 - to_f32(w1[pt][e]));
+            for (int e = 0; e < 4; ++e) {
+              float a0 = low(xu[e]) * (e < 2 ? wa[2 * e] : wb[2 * e - 4]);
+              float a1 = high(xu[e]) * (e < 2 ? wa[2 * e + 1] : wb[2 * e - 3]);
+              const unsigned u0 = pack2(a0, a1);
+              a0 -= low(u0), a1 -= high(u0);
+              const unsigned u1 = pack2(a0, a1);
+              w0[pt][e] = u0;
+              w1[pt][e] = u1;
+              w2[pt][e] = pack2(a0 - low(u1), a1 - high(u1));
             }
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const bf16* src = Bs + (32 * ks + 8 * lq + (lr >> 2)) * LDN + 16 * nt + 4 * (lr & 3);
-            const bf16x8 bt = join(load_tr4(src), load_tr4(src + 4 * LDN));
+            const bf16* src = Bs + (32 * ks + 8 * lq + (lr >> 2)) * LDB + nt / 2 * 32 + nt % 2 * 4 + 8 * (lr & 3);
+            const bf16x8 bt = join(load_tr4(src), load_tr4(src + 4 * LDB));
 #pragma unroll
             for (int pt = 0; pt < PT; ++pt) {
-              S[pt][nt] = mfma(bt, w0[pt], S[pt][nt]);
-              S[pt][nt] = mfma(bt, w1[pt], S[pt][nt]);
-              S[pt][nt] = mfma(bt, w2[pt], S[pt][nt]);
+              S[pt][nt] = mfma(bt, __builtin_bit_cast(bf16x8, w0[pt]), S[pt][nt]);
+              S[pt][nt] = mfma(bt, __builtin_bit_cast(bf16x8, w1[pt]), S[pt][nt]);
+              S[pt][nt] = mfma(bt, __builtin_bit_cast(bf16x8, w2[pt]), S[pt][nt]);
             }
           }
         }
@@ -462,7 +582,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
             for (int pt = 0; pt < PT; ++pt) acc[pt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const f32x4 cv = *reinterpret_cast<const f32x4*>(Cs + i * LDN + 16 * nt + 4 * lq);
+              const f32x4 cv = *reinterpret_cast<const f32x4*>(Cs + i * LDC + 16 * nt + 4 * lq);
 #pragma unroll
               for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -476,6 +596,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
                 acc[pt] = mfma(Xs[(j + lq) * LDX + col0 + 16 * pt + lr], Ms[i * LDM + j + lq], acc[pt]);
             store_y(i, acc);
           }
+          load(nxt);
         }
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt)
@@ -486,52 +607,57 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
           const float w = dec[hh].w[j];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float bt = Bs[j * LDN + 16 * nt + lr];
+            const float bt = Bs[j * LDB + 16 * nt + lr];
 #pragma unroll
             for (int pt = 0; pt < PT; ++pt) S[pt][nt] = mfma(bt, w * Xs[j * LDX + col0 + 16 * pt + lr], S[pt][nt]);
           }
         }
       }
-      if (OUT && cur.last && a.sT) {
-        float* dst = a.sT + ((int64_t)cur.seq * a.HV + hv) * sz;
-        each_state([&](float s, int64_t i) { return dst[i] = s; });
-      }
-      gsum += (double)dec[hh].ghi + (double)dec[hh].glo;
+      if (OUT && cur.last && a.sT) store_state(a.sT + ((int64_t)cur.seq * a.HV + hv) * sz);
+      gsum += dec[hh].end;
+    } else if constexpr (OUT) {
+      load(nxt);
     }
     if (nxt.rows == 0) break;
-    if (wv < HB)
-      make_decay(s_dec[buf ^ 1][wv], to_f32(dtr), lane < nxt.rows, bias, neg_rate);
+    if (dw >= 0)
+      make_decay<OUT, OUT && BF>(s_dec[buf ^ 1][dw], s_in[OUT ? dw : 0], to_f32(dtr), lane < nxt.rows, bias, neg_rate);
     lds_barrier();
     cur = nxt;
   }
   if constexpr (!OUT) {
-    float* dst = a.seg_state + ((int64_t)segk * a.HV + hv) * sz;
-    each_state([&](float s, int64_t i) { return dst[i] = s; });
+    store_state(a.seg_state + ((int64_t)segk * a.HV + hv) * sz);
     // a sequence that starts in the segment takes nothing from the segment before
-    if (active && p0 == 0 && lane == 0) a.seg_g[(int64_t)segk * a.HV + hv] = carry ? (float)gsum : -INFINITY;
+    if (active && p0 == 0 && lane == 0) a.seg_g[(int64_t)segk * a.HV + hv] = carry ? gsum : -INFINITY;
   }
 }
 
+constexpr int kAhead = 8;  // boundaries whose loads are issued before any is used
+
 // Composes the segments' states in order, in place: seg_state[k] becomes the state that enters
 // segment k + 1. One thread an element of [HV, K, V].
-__global__ __launch_bounds__(kThreads) void compose_kernel(float* __restrict__ seg_state,
+__global__ __launch_bounds__(kCompose) void compose_kernel(float* __restrict__ seg_state,
                                                            const float* __restrict__ seg_g, int nb, int HV,
                                                            int64_t sz) {
-  const int64_t n = (int64_t)HV * sz, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t n = (int64_t)HV * sz, i = (int64_t)blockIdx.x * kCompose + threadIdx.x;
   if (i >= n) return;
   const int hv = (int)(i / sz);
   float s = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < nb; ++k) {
-    const float g = seg_g[(int64_t)k * HV + hv];
-    float v = 0.f;
-    if (g != kNoCarry) {
-      // where nothing is carried the product is left out: s may be infinite
-      v = seg_state[(int64_t)k * n + i];
-      if (g > -INFINITY) v += fast_exp2(g) * s;
-      seg_state[(int64_t)k * n + i] = v;
+  for (int k0 = 0; k0 < nb; k0 += kAhead) {
+    float g[kAhead], v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {  // loads behind the last boundary read it again
+      const int k = min(k0 + u, nb - 1);
+      g[u] = seg_g[(int64_t)k * HV + hv];
+      v[u] = seg_state[(int64_t)k * n + i];
     }
-    s = v;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (k0 + u >= nb) break;
+      // where nothing is carried the product is left out: s may be infinite
+      const bool none = g[u] == kNoCarry;
+      s = none ? 0.f : g[u] > -INFINITY ? v[u] + fast_exp2(g[u]) * s : v[u];
+      if (!none) seg_state[(int64_t)(k0 + u) * n + i] = s;
+    }
   }
 }
 
@@ -542,15 +668,15 @@ hipError_t run(const SsmArgs& a, hipStream_t stream) {
   const int hblocks = a.HV / HB * ((a.V + PP - 1) / PP);
   if (a.crossed) {
     hipLaunchKernelGGL((prefill_kernel<T, NT, PP, HB, PT, false, VEC>), dim3(hblocks * (a.nseg - 1)),
-                       dim3(kThreads), 0, stream, a, hblocks);
+                       dim3(64 * kWaves<PP, HB, PT>), 0, stream, a, hblocks);
     const int64_t n = (int64_t)a.HV * a.K * a.V;
-    hipLaunchKernelGGL(compose_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream,
+    hipLaunchKernelGGL(compose_kernel, dim3((unsigned)((n + kCompose - 1) / kCompose)), dim3(kCompose), 0, stream,
                        a.seg_state, a.seg_g, a.nseg - 1, a.HV, (int64_t)a.K * a.V);
   }
-  const int empties = (a.cu || a.T == 0) && a.sT ? a.N : 0;
+  const int empties = (a.seqs.cu || a.T == 0) && a.sT ? a.N : 0;
   if (hblocks * a.nseg + empties == 0) return hipSuccess;
   hipLaunchKernelGGL((prefill_kernel<T, NT, PP, HB, PT, true, VEC>), dim3(hblocks * a.nseg + empties),
-                     dim3(kThreads), 0, stream, a, hblocks);
+                     dim3(64 * kWaves<PP, HB, PT>), 0, stream, a, hblocks);
   return hipGetLastError();
 }
 
@@ -608,7 +734,7 @@ size_t ssm_prefill_workspace_bytes(int T, int N, bool packed, int H, int HV, int
 }
 
 hipError_t launch_ssm_prefill(SsmArgs a, void* workspace, hipStream_t stream) {
-  const Segments g = ssm_segments(a.T, a.N, a.cu != nullptr, a.H, a.HV, a.V, a.bf);
+  const Segments g = ssm_segments(a.T, a.N, a.seqs.cu != nullptr, a.H, a.HV, a.V, a.bf);
   a.seg = g.len;
   a.nseg = g.n;
   a.crossed = g.crossed;
