@@ -74,8 +74,9 @@ struct Tile {
 // 16-byte pieces, aligned in memory.
 template <typename T, int THREADS, int ROWS, int COLS, int PAD, bool VEC>
 struct Stage {
-  static constexpr int kElem = 16 / sizeof(T), kRow = COLS / kElem, kPieces = ROWS * kRow / THREADS;
-  static_assert(kPieces * THREADS == ROWS * kRow, "every thread holds the same number of pieces");
+  static constexpr int kElem = 16 / sizeof(T), kRow = COLS / kElem;
+  static constexpr int kPieces = (ROWS * kRow + THREADS - 1) / THREADS;
+  static constexpr bool kEven = kPieces * THREADS == ROWS * kRow;  // every thread holds as many
   u32x4 v[kPieces];
 
   // src: row 0, column 0; ld: elements between rows; rows behind `rows` and columns behind
@@ -90,7 +91,7 @@ struct Stage {
       const int piece = threadIdx.x + THREADS * e, row = piece / kRow, c = piece % kRow * kElem;
       const int blk = c / PAD, p = c - blk * PAD;
       const unsigned off = (unsigned)row * rowb + (unsigned)(blk * width + p) * sizeof(T);
-      auto in = [&](int k) { return p + k < width ? off + k * (unsigned)sizeof(T) : kOutOfRange; };
+      auto in = [&](int k) { return p + k < width && (kEven || row < ROWS) ? off + k * (unsigned)sizeof(T) : kOutOfRange; };
       if constexpr (VEC) {
         v[e] = __builtin_amdgcn_raw_buffer_load_b128(r, in(0), 0, 0);
       } else {
@@ -111,7 +112,7 @@ struct Stage {
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
       const int piece = threadIdx.x + THREADS * e, row = piece / kRow, c = piece % kRow * kElem;
-      *reinterpret_cast<u32x4*>(dst + row * ldd + c) = v[e];
+      if (kEven || row < ROWS) *reinterpret_cast<u32x4*>(dst + row * ldd + c) = v[e];
     }
   }
 };
