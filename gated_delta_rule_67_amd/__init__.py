@@ -620,83 +620,99 @@ def kda_chunk_fwd_noalloc(q, k, v, g, beta, o, final_state=None, scale=None, ini
     return o
 
 
-def _call(dev, fn, *args):
-    """fn(*args, stream) on dev's current stream with dev current; raises unless KDA_OK."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, stream))
+# The entry points below are called once per layer and token, so their checks are written for few
+# Python operations; messages are made only where a check fails.
+
+def _call(index, fn, *args):
+    """fn(*args, stream) on the current stream of GPU `index`, with that GPU current."""
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, stream)
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, stream))
+        with torch.cuda.device(index):
+            rc = fn(*args, stream)
+    if rc != KDA_OK:
+        _check(rc)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _token_stride(name, t, lead):
+def _fresh(t):
+    """An uninitialised contiguous tensor shaped and typed like t."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _dense(name, t, shape, dtype, index):
+    """t (or None) must be a contiguous tensor of this shape and dtype on GPU `index`."""
+    if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != index
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on the GPU of x")
+
+
+def _token_stride(name, t, lead, width):
     """Elements between the tokens of t, whose first `lead` dimensions are tokens in order (one, or
-    batch and token) and whose others are dense: t may be a slice of a wider activation."""
-    width = 1
+    batch and token) and whose others, `width` elements, are dense: t may be a slice of a wider
+    activation."""
+    if t.is_contiguous():
+        return width
+    expect = 1
     for size, stride in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
-        _require(size == 1 or stride == width, f"{name} must be dense in its last dimensions")
-        width *= size
+        _require(size == 1 or stride == expect, f"{name} must be dense in its last dimensions")
+        expect *= size
     step = None
     for size, stride in zip(reversed(t.shape[:lead]), reversed(t.stride()[:lead])):
         if size > 1:
-            _require(step is None or stride == step * tokens,
-                     f"{name} must hold its tokens at one stride")
+            _require(step is None or stride == step * tokens, f"{name} must hold its tokens at one stride")
             step, tokens = (stride, size) if step is None else (step, tokens * size)
     _require(step is None or step >= width, f"{name} must not overlap itself")
     return width if step is None else step
 
 
-def _check_params(named, dev):
-    for name, t, shape in named:
-        if t is not None:
-            _require(t.device == dev and t.dtype == torch.float32 and t.is_contiguous()
-                     and tuple(t.shape) == shape, f"{name} must be float32 {list(shape)} on {dev}")
+def _tokens(name, t, shape, like, index, lead, width):
+    """The token stride of t, a tensor of this shape, typed like x and on its GPU."""
+    if t.dtype is not like.dtype or t.shape != shape or t.get_device() != index:
+        raise ValueError(f"{name} must be {list(shape)}, of the dtype and on the GPU of x")
+    return _token_stride(name, t, lead, width)
 
 
-def _sequences(x, cu_seqlens):
-    """(token dimensions of x, sequences N, tokens T) of a dense batch [B, T, ...] or, with
-    cu_seqlens, of packed tokens [T, ...] or [1, T, ...]."""
+def _sequences(x, cu_seqlens, dims, index):
+    """(token dimensions, sequences, tokens) of x: a dense batch [B, T, ...] of `dims` dimensions
+    or, with cu_seqlens, packed tokens [T, ...] or [1, T, ...]."""
     if cu_seqlens is None:
-        return 2, x.shape[0], x.shape[0] * x.shape[1]
-    _require(cu_seqlens.device == x.device and cu_seqlens.dtype == torch.int32
+        _require(x.dim() == dims, "x must be a batch [B, T, ...] (packed sequences: give cu_seqlens)")
+        N, T = x.shape[0], x.shape[0] * x.shape[1]
+        _require(N >= 1, "x must have at least one sequence")
+        return 2, N, T
+    _require(cu_seqlens.get_device() == index and cu_seqlens.dtype is torch.int32
              and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous() and cu_seqlens.numel() >= 2,
-             "cu_seqlens must be a contiguous int32 vector of at least two offsets on the same GPU")
-    return None, cu_seqlens.numel() - 1, None
+             "cu_seqlens must be a contiguous int32 vector of at least two offsets on the GPU of x")
+    lead = x.dim() - dims + 2
+    _require(lead == 1 or (lead == 2 and x.shape[0] == 1), "packed x must be [T, ...] or [1, T, ...]")
+    return lead, cu_seqlens.numel() - 1, x.shape[lead - 1]
+
+
+def _gpu(x):
+    """(GPU index, the library's dtype) of x."""
+    index, code = x.get_device(), _DTYPE.get(x.dtype)
+    _require(index >= 0, "inputs must be on a GPU")
+    if code is None:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    return index, code
 
 
 def _conv_flags(silu):
     return (KDA_CONV_SILU if silu else 0) | KDA_ZERO_REST
 
 
-def _conv_args(x, weight, bias, states, cu_seqlens, others):
-    _require(x.is_cuda, "inputs must be on a GPU")
-    _require(x.dtype in _DTYPE, f"unsupported dtype {x.dtype}")
-    dev, dt = x.device, x.dtype
-    _, N, T = _sequences(x, cu_seqlens)
-    if cu_seqlens is None:
-        _require(x.dim() == 3, "x must be [B, T, D] (packed sequences: give cu_seqlens)")
-    else:
-        _require(x.dim() == 2 or (x.dim() == 3 and x.shape[0] == 1), "packed x must be [T, D] or [1, T, D]")
-        T = x.shape[-2]
-    D, lead = x.shape[-1], x.dim() - 1
-    _require(weight.dim() == 2 and weight.shape[0] == D, "weight must be [D, W]")
-    W = weight.shape[1]
-    _require(D >= 1 and N >= 1, "x must have at least one sequence and one channel")
-    _check_params([("weight", weight, (D, W)), ("bias", bias, (D,))], dev)
-    for name, t in states:
-        if t is not None:
-            _require(tuple(t.shape) == (N, W - 1, D), f"{name} must be [N, W-1, D]")
-            _check_tensors([(name, t)], dt, dev)
-    strides = []
-    for name, t in [("x", x)] + others:
-        _require(t.shape == x.shape and t.dtype == dt and t.device == dev, f"{name} must match x")
-        strides.append(_token_stride(name, t, lead))
-    return dev, dt, N, T, D, W, strides
+def _conv_params(x, weight, bias, index):
+    _require(weight.dim() == 2, "weight must be [D, W]")
+    W, D = weight.shape[1], x.shape[-1]
+    _require(D >= 1, "x must have at least one channel")
+    _dense("weight", weight, (D, W), torch.float32, index)
+    _dense("bias", bias, (D,), torch.float32, index)
+    return D, W
 
 
 def kda_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, silu=True,
@@ -707,14 +723,16 @@ def kda_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, silu
     activation); weight [D,W] (W = 2..4) and bias [D] float32; initial_state [N,W-1,D] like x:
     the rows before each sequence (None: zeros). Returns (y shaped like x, final_state
     [N,W-1,D] or None); y rows in no packed sequence are zero."""
-    dev, dt, N, T, D, W, (ldx,) = _conv_args(x, weight, bias, [("initial_state", initial_state)],
-                                             cu_seqlens, [])
-    lib = library()
-    y = torch.empty(x.shape, dtype=dt, device=dev)
-    final = torch.empty((N, W - 1, D), dtype=dt, device=dev) if output_final_state else None
-    _call(dev, lib.kda_conv_fwd, x.data_ptr(), ldx, weight.data_ptr(), _addr(bias),
+    index, code = _gpu(x)
+    lead, N, T = _sequences(x, cu_seqlens, 3, index)
+    D, W = _conv_params(x, weight, bias, index)
+    _dense("initial_state", initial_state, (N, W - 1, D), x.dtype, index)
+    ldx = _token_stride("x", x, lead, D)
+    y = _fresh(x)
+    final = x.new_empty((N, W - 1, D)) if output_final_state else None
+    _call(index, library().kda_conv_fwd, x.data_ptr(), ldx, weight.data_ptr(), _addr(bias),
           _addr(initial_state), _addr(cu_seqlens), N, _addr(final), y.data_ptr(), T, D, W,
-          _conv_flags(silu), _DTYPE[dt])
+          _conv_flags(silu), code)
     return y, final
 
 
@@ -724,71 +742,68 @@ def kda_conv_bwd(x, weight, dy, bias=None, initial_state=None, dfinal_state=None
     dfinal_state [N,W-1,D] like x or None. Returns (dx like x, dweight [D,W] and dbias [D]
     float32, dinitial_state [N,W-1,D]); the last two are None where bias / initial_state is, and
     dx rows in no packed sequence are zero."""
-    dev, dt, N, T, D, W, (ldx, lddy) = _conv_args(
-        x, weight, bias, [("initial_state", initial_state), ("dfinal_state", dfinal_state)],
-        cu_seqlens, [("dy", dy)])
+    index, code = _gpu(x)
+    lead, N, T = _sequences(x, cu_seqlens, 3, index)
+    D, W = _conv_params(x, weight, bias, index)
+    _dense("initial_state", initial_state, (N, W - 1, D), x.dtype, index)
+    _dense("dfinal_state", dfinal_state, (N, W - 1, D), x.dtype, index)
+    ldx = _token_stride("x", x, lead, D)
+    lddy = _tokens("dy", dy, x.shape, x, index, lead, D)
     lib = library()
-    dx = torch.empty(x.shape, dtype=dt, device=dev)
-    dweight = torch.empty((D, W), dtype=torch.float32, device=dev)
-    dbias = None if bias is None else torch.empty((D,), dtype=torch.float32, device=dev)
-    dinit = None if initial_state is None else torch.empty((N, W - 1, D), dtype=dt, device=dev)
-    ws_bytes = lib.kda_conv_bwd_workspace_size(T, D, W, _DTYPE[dt])
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-    _call(dev, lib.kda_conv_bwd, x.data_ptr(), ldx, weight.data_ptr(), _addr(bias),
+    dx = _fresh(x)
+    dweight = torch.empty_like(weight)
+    dbias = None if bias is None else torch.empty_like(bias)
+    dinit = None if initial_state is None else torch.empty_like(initial_state)
+    ws_bytes = lib.kda_conv_bwd_workspace_size(T, D, W, code)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device) if ws_bytes else None
+    _call(index, lib.kda_conv_bwd, x.data_ptr(), ldx, weight.data_ptr(), _addr(bias),
           _addr(initial_state), _addr(cu_seqlens), N, dy.data_ptr(), lddy, _addr(dfinal_state),
           dx.data_ptr(), dweight.data_ptr(), _addr(dbias), _addr(dinit), T, D, W, _conv_flags(silu),
-          _DTYPE[dt], _addr(ws), ws_bytes)
+          code, _addr(ws), ws_bytes)
     return dx, dweight, dbias, dinit
 
 
-def _check_slots(slots, B, num_slots, dev):
+def _slots(slots, B, num_slots, index):
     if slots is None:
         _require(num_slots >= B, "without slots the pool needs a state per request")
-    else:
-        _require(slots.device == dev and slots.dtype == torch.int32 and tuple(slots.shape) == (B,)
-                 and slots.is_contiguous(), "slots must be int32 [B] on the GPU")
+        return None
+    if (slots.dtype is not torch.int32 or slots.shape != (B,) or slots.get_device() != index
+            or not slots.is_contiguous()):
+        raise ValueError("slots must be int32 [B] on the GPU of x")
+    return slots.data_ptr()
 
 
 def kda_conv_step(x, weight, state_pool, bias=None, slots=None, silu=True):
     """One token of kda_conv_fwd per request. x [B,D]; state_pool [num_slots,W-1,D] like x, moved
     on by one row in place; slots int32 [B] (a slot outside [0, num_slots) gives y = 0 and no
     update), or None: request n uses slot n. Returns y [B,D]."""
-    _require(x.is_cuda, "inputs must be on a GPU")
-    dev, dt = x.device, x.dtype
-    _require(dt in _DTYPE, f"unsupported dtype {dt}")
-    _require(x.dim() == 2 and x.numel() > 0, "x must be [B, D]")
-    B, D = x.shape
-    _require(weight.dim() == 2 and weight.shape[0] == D, "weight must be [D, W]")
-    W = weight.shape[1]
-    _check_params([("weight", weight, (D, W)), ("bias", bias, (D,))], dev)
-    _require(state_pool.dim() == 3 and tuple(state_pool.shape[1:]) == (W - 1, D),
-             "state_pool must be [num_slots, W-1, D]")
-    _check_tensors([("state_pool", state_pool)], dt, dev)
-    _check_slots(slots, B, state_pool.shape[0], dev)
-    y = torch.empty((B, D), dtype=dt, device=dev)
-    _call(dev, library().kda_conv_step, x.data_ptr(), _token_stride("x", x, 1), weight.data_ptr(),
-          _addr(bias), state_pool.data_ptr(), _addr(slots), state_pool.shape[0], y.data_ptr(), B,
-          D, W, _conv_flags(silu), _DTYPE[dt])
+    index, code = _gpu(x)
+    _require(x.dim() == 2 and x.numel() > 0 and state_pool.dim() == 3,
+             "x must be [B, D], state_pool [num_slots, W-1, D]")
+    D, W = _conv_params(x, weight, bias, index)
+    B, num_slots = x.shape[0], state_pool.shape[0]
+    _dense("state_pool", state_pool, (num_slots, W - 1, D), x.dtype, index)
+    at = _slots(slots, B, num_slots, index)
+    ldx = _token_stride("x", x, 1, D)
+    y = _fresh(x)
+    _call(index, library().kda_conv_step, x.data_ptr(), ldx, weight.data_ptr(), _addr(bias),
+          state_pool.data_ptr(), at, num_slots, y.data_ptr(), B, D, W, _conv_flags(silu), code)
     return y
 
 
-def _ssm_args(x, dt, A_log, b, c, D, dt_bias, lead):
-    """Checks what the scan's entry points share; tokens are the first `lead` dimensions.
-    Returns (device, dtype, H, HV, K, V, token strides of x, dt, b, c)."""
-    _require(x.is_cuda, "inputs must be on a GPU")
-    dev, dtype = x.device, x.dtype
-    _require(dtype in _DTYPE, f"unsupported dtype {dtype}")
-    tokens, (HV, V) = tuple(x.shape[:lead]), x.shape[lead:]
-    _require(b.dim() == lead + 2 and tuple(b.shape[:lead]) == tokens, "b must be [tokens, H, K]")
+def _ssm_args(x, dt, A_log, b, c, D, dt_bias, lead, index):
+    """Checks what the scan's entry points share. Returns (H, HV, K, V, token strides of x, dt, b, c)."""
+    tokens, (HV, V) = x.shape[:lead], x.shape[lead:]
+    _require(b.dim() == lead + 2, "b must be [tokens, H, K]")
     H, K = b.shape[lead:]
-    _require(c.shape == b.shape, "c must match b")
-    _require(tuple(dt.shape) == tokens + (HV,), "dt must be [tokens, HV]")
-    strides = []
-    for name, t in (("x", x), ("dt", dt), ("b", b), ("c", c)):
-        _require(t.dtype == dtype and t.device == dev, f"{name} must match x in dtype and device")
-        strides.append(_token_stride(name, t, lead))
-    _check_params([("A_log", A_log, (HV,)), ("D", D, (HV,)), ("dt_bias", dt_bias, (HV,))], dev)
-    return dev, dtype, H, HV, K, V, strides
+    ldx = _token_stride("x", x, lead, HV * V)
+    lddt = _tokens("dt", dt, tokens + (HV,), x, index, lead, HV)
+    ldb = _tokens("b", b, tokens + (H, K), x, index, lead, H * K)
+    ldc = _tokens("c", c, tokens + (H, K), x, index, lead, H * K)
+    _dense("A_log", A_log, (HV,), torch.float32, index)
+    _dense("D", D, (HV,), torch.float32, index)
+    _dense("dt_bias", dt_bias, (HV,), torch.float32, index)
+    return H, HV, K, V, ldx, lddt, ldb, ldc
 
 
 def kda_ssm_chunk_fwd(x, dt, A_log, b, c, D=None, dt_bias=None, initial_state=None, cu_seqlens=None,
@@ -799,27 +814,19 @@ def kda_ssm_chunk_fwd(x, dt, A_log, b, c, D=None, dt_bias=None, initial_state=No
     reads pair hv // (HV // H)), or packed without B (or with B = 1) and cu_seqlens int32 [N+1];
     A_log, D, dt_bias [HV] float32; initial_state [N,HV,K,V] float32. Returns (y shaped like x,
     final_state [N,HV,K,V] or None); y rows in no packed sequence are zero."""
-    _, N, T = _sequences(x, cu_seqlens)
-    if cu_seqlens is None:
-        _require(x.dim() == 4, "x must be [B, T, HV, V] (packed sequences: give cu_seqlens)")
-    else:
-        _require(x.dim() == 3 or (x.dim() == 4 and x.shape[0] == 1), "packed x must be [T, HV, V] or [1, T, HV, V]")
-        T = x.shape[-3]
-    dev, dtype, H, HV, K, V, strides = _ssm_args(x, dt, A_log, b, c, D, dt_bias, x.dim() - 2)
-    _require(N >= 1, "x must have at least one sequence")
-    if initial_state is not None:
-        _require(tuple(initial_state.shape) == (N, HV, K, V), "initial_state must be [N, HV, K, V]")
-        _check_tensors([("initial_state", initial_state)], torch.float32, dev)
+    index, code = _gpu(x)
+    lead, N, T = _sequences(x, cu_seqlens, 4, index)
+    H, HV, K, V, ldx, lddt, ldb, ldc = _ssm_args(x, dt, A_log, b, c, D, dt_bias, lead, index)
+    _dense("initial_state", initial_state, (N, HV, K, V), torch.float32, index)
     lib = library()
-    y = torch.empty(x.shape, dtype=dtype, device=dev)
-    final = torch.empty((N, HV, K, V), dtype=torch.float32, device=dev) if output_final_state else None
-    ws_bytes = lib.kda_ssm_chunk_fwd_workspace_size(N, T, int(cu_seqlens is not None), H, HV, K, V, _DTYPE[dtype])
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-    ldx, lddt, ldb, ldc = strides
-    _call(dev, lib.kda_ssm_chunk_fwd, x.data_ptr(), ldx, dt.data_ptr(), lddt, A_log.data_ptr(),
+    y = _fresh(x)
+    final = torch.empty((N, HV, K, V), dtype=torch.float32, device=x.device) if output_final_state else None
+    ws_bytes = lib.kda_ssm_chunk_fwd_workspace_size(N, T, 0 if cu_seqlens is None else 1, H, HV, K, V, code)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device) if ws_bytes else None
+    _call(index, lib.kda_ssm_chunk_fwd, x.data_ptr(), ldx, dt.data_ptr(), lddt, A_log.data_ptr(),
           b.data_ptr(), ldb, c.data_ptr(), ldc, _addr(D), _addr(dt_bias), _addr(initial_state),
-          _addr(cu_seqlens), N, _addr(final), y.data_ptr(), T, H, HV, K, V, KDA_ZERO_REST,
-          _DTYPE[dtype], _addr(ws), ws_bytes)
+          _addr(cu_seqlens), N, _addr(final), y.data_ptr(), T, H, HV, K, V, KDA_ZERO_REST, code,
+          _addr(ws), ws_bytes)
     return y, final
 
 
@@ -827,37 +834,38 @@ def kda_ssm_step(x, dt, A_log, b, c, state_pool, D=None, dt_bias=None, slots=Non
     """One token of kda_ssm_chunk_fwd per request. x [B,HV,V], dt [B,HV], b, c [B,H,K]; state_pool
     [num_slots,HV,K,V] float32, updated in place; slots int32 [B] (a slot outside [0, num_slots)
     gives y = 0 and no update), or None: request n uses slot n. Returns y [B,HV,V]."""
+    index, code = _gpu(x)
     _require(x.dim() == 3 and x.numel() > 0, "x must be [B, HV, V]")
-    dev, dtype, H, HV, K, V, (ldx, lddt, ldb, ldc) = _ssm_args(x, dt, A_log, b, c, D, dt_bias, 1)
-    B = x.shape[0]
-    _require(state_pool.dim() == 4 and tuple(state_pool.shape[1:]) == (HV, K, V),
-             "state_pool must be [num_slots, HV, K, V]")
-    _check_tensors([("state_pool", state_pool)], torch.float32, dev)
-    _check_slots(slots, B, state_pool.shape[0], dev)
-    y = torch.empty((B, HV, V), dtype=dtype, device=dev)
-    _call(dev, library().kda_ssm_step, x.data_ptr(), ldx, dt.data_ptr(), lddt, A_log.data_ptr(),
-          b.data_ptr(), ldb, c.data_ptr(), ldc, _addr(D), _addr(dt_bias), state_pool.data_ptr(),
-          _addr(slots), state_pool.shape[0], y.data_ptr(), B, H, HV, K, V, _DTYPE[dtype])
+    H, HV, K, V, ldx, lddt, ldb, ldc = _ssm_args(x, dt, A_log, b, c, D, dt_bias, 1, index)
+    B, num_slots = x.shape[0], state_pool.shape[0] if state_pool.dim() == 4 else 0
+    _dense("state_pool", state_pool, (num_slots, HV, K, V), torch.float32, index)
+    at = _slots(slots, B, num_slots, index)
+    y = _fresh(x)
+    _call(index, library().kda_ssm_step, x.data_ptr(), ldx, dt.data_ptr(), lddt, A_log.data_ptr(),
+          b.data_ptr(), ldb, c.data_ptr(), ldc, _addr(D), _addr(dt_bias), state_pool.data_ptr(), at,
+          num_slots, y.data_ptr(), B, H, HV, K, V, code)
     return y
 
 
 def _pools(pools):
-    """(device, host arrays of addresses and slot sizes, count, num_slots) of one pool or several."""
-    pools = [pools] if isinstance(pools, torch.Tensor) else list(pools)
-    _require(len(pools) > 0, "at least one pool is needed")
-    dev, num_slots = pools[0].device, pools[0].shape[0] if pools[0].dim() else 0
-    spans = []
+    """(GPU index, host arrays of addresses and slot sizes, count, num_slots) of one pool or several."""
+    pools = [pools] if isinstance(pools, torch.Tensor) else pools
+    n = len(pools)
+    _require(n > 0, "at least one pool is needed")
+    index, num_slots = pools[0].get_device(), pools[0].shape[0] if pools[0].dim() else 0
+    _require(index >= 0, "pools must be on a GPU")
+    base, size = [], []
     for p in pools:
-        _require(p.is_cuda and p.device == dev, "pools must be on one GPU")
-        _require(p.dim() >= 1 and p.shape[0] == num_slots and p.numel() > 0,
-                 "pools must be [num_slots, ...] with the same num_slots >= 1")
-        _require(p.is_contiguous(), "pools must be contiguous")
-        spans.append((p.data_ptr(), p.numel() * p.element_size()))
-    order = sorted(spans)
-    _require(all(a + n <= b for (a, n), (b, _) in zip(order, order[1:])), "pools must not overlap")
-    n = len(spans)
-    return (dev, (ctypes.c_void_p * n)(*[a for a, _ in spans]),
-            (ctypes.c_size_t * n)(*[size // num_slots for _, size in spans]), n, num_slots)
+        if p.dim() < 1 or p.shape[0] != num_slots or p.get_device() != index or not p.is_contiguous():
+            raise ValueError("pools must be contiguous [num_slots, ...], with one num_slots, on one GPU")
+        base.append(p.data_ptr())
+        size.append(p.nbytes)
+    _require(min(size) > 0, "pools must hold at least one byte a slot")
+    if n > 1:
+        order = sorted(zip(base, size))
+        _require(all(a[0] + a[1] <= b[0] for a, b in zip(order, order[1:])), "pools must not overlap")
+    return (index, (ctypes.c_void_p * n)(*base), (ctypes.c_size_t * n)(*[v // num_slots for v in size]), n,
+            num_slots)
 
 
 def kda_slots_copy(pools, src, dst):
@@ -865,12 +873,14 @@ def kda_slots_copy(pools, src, dst):
     src[i] (a fork), or zeros where src[i] < 0 (a cleared slot). pools: a tensor [num_slots, ...]
     or a list of them (a model's layers; any dtype); src, dst int32 [n] on the GPU; pairs with dst
     outside [0, num_slots) or src >= num_slots do nothing."""
-    dev, base, size, n, num_slots = _pools(pools)
+    index, base, size, n, num_slots = _pools(pools)
+    _require(src.dim() == 1, "src must be int32 [n] on the pools' GPU")
     for name, t in (("src", src), ("dst", dst)):
-        _require(t.device == dev and t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous()
-                 and t.shape == src.shape, f"{name} must be int32 [n] on the pools' GPU")
-    _call(dev, library().kda_slots_copy, base, size, n, num_slots, src.data_ptr(), dst.data_ptr(),
-          src.numel())
+        if (t.dtype is not torch.int32 or t.shape != src.shape or t.get_device() != index
+                or not t.is_contiguous()):
+            raise ValueError(f"{name} must be int32 [n] on the pools' GPU")
+    _call(index, library().kda_slots_copy, base, size, n, num_slots, src.data_ptr(), dst.data_ptr(),
+          src.shape[0])
 
 
 def kda_slots_compact(pools, live):
@@ -878,16 +888,17 @@ def kda_slots_compact(pools, live):
     behind slot c move, in order, into the free slots in front of it. pools: as kda_slots_copy;
     live: bool (or uint8) [num_slots] on the GPU. Returns (new_slot int32 [num_slots]: where a
     slot's state lives now, -1 for a free one; count int32 [1])."""
-    dev, base, size, n, num_slots = _pools(pools)
-    _require(live.device == dev and live.dtype in (torch.bool, torch.uint8) and live.is_contiguous()
-             and tuple(live.shape) == (num_slots,), "live must be bool [num_slots] on the pools' GPU")
+    index, base, size, n, num_slots = _pools(pools)
+    if (live.dtype not in (torch.bool, torch.uint8) or live.shape != (num_slots,)
+            or live.get_device() != index or not live.is_contiguous()):
+        raise ValueError("live must be bool [num_slots] on the pools' GPU")
     lib = library()
-    new_slot = torch.empty((num_slots,), dtype=torch.int32, device=dev)
-    count = torch.empty((1,), dtype=torch.int32, device=dev)
     ws_bytes = lib.kda_slots_compact_workspace_size(num_slots)
-    ws = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
-    _call(dev, lib.kda_slots_compact, base, size, n, num_slots, live.data_ptr(),
-          new_slot.data_ptr(), count.data_ptr(), ws.data_ptr(), ws_bytes)
+    # the results and the workspace share one allocation; the workspace comes first (256-byte aligned)
+    buf = torch.empty((ws_bytes // 4 + num_slots + 1,), dtype=torch.int32, device=live.device)
+    new_slot, count = buf[ws_bytes // 4:-1], buf[-1:]
+    _call(index, lib.kda_slots_compact, base, size, n, num_slots, live.data_ptr(),
+          new_slot.data_ptr(), count.data_ptr(), buf.data_ptr(), ws_bytes)
     return new_slot, count
 
 

@@ -45,7 +45,7 @@ hipError_t launch_conv_fwd(const ConvArgs& p, hipStream_t stream);
 hipError_t launch_conv_bwd(const ConvArgs& p, const void* dy, int64_t lddy, const void* dfinal,
                            float* dweight, float* dbias, void* workspace, hipStream_t stream);
 hipError_t launch_conv_step(const ConvArgs& p, const ConvStep& st, hipStream_t stream);
-size_t conv_bwd_workspace_bytes(int T, int D, int W, bool bf);
+size_t conv_bwd_workspace_bytes(int T, int D, int W);
 hipError_t launch_ssm_prefill(SsmArgs a, void* workspace, hipStream_t stream);
 size_t ssm_prefill_workspace_bytes(int T, int N, bool packed, int H, int HV, int K, int V, bool bf);
 hipError_t launch_ssm_step(const SsmArgs& a, hipStream_t stream);
@@ -550,7 +550,7 @@ int kda_conv_fwd(const void* x, int64_t x_stride, const float* weight, const flo
 
 size_t kda_conv_bwd_workspace_size(int T, int D, int W, int dtype) {
   if (check_conv(1, T, D, W, nullptr, 0u, dtype) != KDA_OK) return 0;
-  return kda::conv_bwd_workspace_bytes(T, D, W, dtype == KDA_DTYPE_BF16);
+  return kda::conv_bwd_workspace_bytes(T, D, W);
 }
 
 int kda_conv_bwd(const void* x, int64_t x_stride, const float* weight, const float* bias,

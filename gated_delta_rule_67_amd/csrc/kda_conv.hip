@@ -25,6 +25,7 @@ namespace conv {
 constexpr int kThreads = 256;
 constexpr int kLanes = 64;                  // column vectors of a workgroup, one per lane
 constexpr int kSlices = kThreads / kLanes;  // its waves take consecutive slices of the row block
+constexpr int kMinRows = 4;                 // rows of a slice at least: fewer would mostly read its halo
 constexpr int kRows = 4;                    // rows whose loads are issued before any is used
 
 template <typename T, int VEC> struct Row {
@@ -100,7 +101,7 @@ __device__ __forceinline__ void outside(const Args& a, int r, int end, int col) 
 }
 
 // Forward. grid.x: column blocks, grid.y: row blocks, then blocks of sequences (final states).
-template <typename T, int VEC, int W>
+template <typename T, int VEC, int W, bool SILU>
 __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a) {
   typedef row_t<T, VEC> vec_t;
   const int lane = threadIdx.x % kLanes, slice = threadIdx.x / kLanes;
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a) {
 #pragma unroll
         for (int k = 0; k + 1 < W - 1; ++k) win[k][e] = win[k + 1][e];
         win[W - 2][e] = xe;
-        put<T, VEC>(yv, e, a.silu ? pre * logistic(pre) : pre);
+        put<T, VEC>(yv, e, SILU ? pre * logistic(pre) : pre);
       }
       *reinterpret_cast<vec_t*>(out) = yv;  // cached: the recurrence reads it next
     };
@@ -185,7 +186,7 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a) {
 // slice starts inside a sequence leaves the rows before its slice to the wave before it; a row is
 // therefore written once, always by the wave whose slice holds it (rows of the initial state: by
 // the wave that holds the sequence's first token).
-template <typename T, int VEC, int W>
+template <typename T, int VEC, int W, bool SILU>
 __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a) {
   typedef row_t<T, VEC> vec_t;
   __shared__ float s_sum[kSlices][W + 1][VEC][kLanes];
@@ -231,7 +232,6 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a) {
         r = s.bos;
         continue;
       }
-      const int len = s.eos - s.bos;
       const int first = r == s.bos ? s.bos - (W - 1) : r;
       const int own = min(s.eos, r1);  // tokens [r, own) enter the sums, rows [first, own) are written
       float win[W - 1][VEC], dp[W - 1][VEC];  // x, and dpre, of the W - 1 rows before t
@@ -245,37 +245,28 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a) {
         }
       }
       // row `row` (a token, or a row of the initial state below s.bos) with its sum
-      auto emit = [&](int row, float (&sum)[VEC]) {
-        const int v = row - s.bos + (W - 1);  // place in (state ; sequence)
-        if (a.dfinal && v >= len) {
-          const vec_t f = *reinterpret_cast<const vec_t*>(
-              static_cast<const T*>(a.dfinal) + ((int64_t)seq * (W - 1) + v - len) * a.D + col);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) sum[e] += at<T, VEC>(f, e);
-        }
+      auto emit = [&](int row, const float (&sum)[VEC]) {
         vec_t o;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) put<T, VEC>(o, e, sum[e]);
         if (row >= s.bos)
           __builtin_nontemporal_store(o, reinterpret_cast<vec_t*>(static_cast<T*>(a.out) + (int64_t)row * a.D + col));
         else if (a.out_state)
-          *reinterpret_cast<vec_t*>(static_cast<T*>(a.out_state) + ((int64_t)seq * (W - 1) + v) * a.D + col) = o;
+          *reinterpret_cast<vec_t*>(static_cast<T*>(a.out_state) + ((int64_t)seq * (W - 1) + row - s.bos + W - 1) * a.D + col) = o;
       };
-      // dpre of token t; the row W - 1 places before it gets its sum
-      auto token = [&](int t, const vec_t& xv, const vec_t& gv) {
-        const bool mine = t < own;
-        float sum[VEC];
+      // dpre of a token (into the sums if it is this wave's); the sum of the row W - 1 places before it
+      auto token = [&](const vec_t& xv, const vec_t& gv, bool mine, float (&sum)[VEC]) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const float xe = at<T, VEC>(xv, e);
-          float pre = b[e];
-#pragma unroll
-          for (int k = 0; k < W - 1; ++k) pre = fmaf(w[k][e], win[k][e], pre);
-          pre = fmaf(w[W - 1][e], xe, pre);
           float d = at<T, VEC>(gv, e);
-          if (a.silu) {
+          if constexpr (SILU) {
+            float pre = b[e];
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) pre = fmaf(w[k][e], win[k][e], pre);
+            pre = fmaf(w[W - 1][e], xe, pre);
             const float sg = logistic(pre);
-            d *= sg * (1.f + pre * (1.f - sg));
+            d *= fmaf(pre * sg, 1.f - sg, sg);
           }
           if (mine) {
 #pragma unroll
@@ -295,26 +286,41 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a) {
           win[W - 2][e] = xe;
           dp[W - 2][e] = d;
         }
-        if (t - (W - 1) >= first) emit(t - (W - 1), sum);
       };
       const int stop = min(s.eos, own + (W - 1));
       const T* xp = x + (int64_t)r * a.ldx;
       const T* gp = dy + (int64_t)r * a.lddy;
       int t = r;
-      for (; t + kRows <= stop; t += kRows) {
+      auto single = [&] {
+        float sum[VEC];
+        token(*reinterpret_cast<const vec_t*>(xp), *reinterpret_cast<const vec_t*>(gp), t < own, sum);
+        if (t - (W - 1) >= first) emit(t - (W - 1), sum);
+        ++t, xp += a.ldx, gp += a.lddy;
+      };
+      const int head = min(r + W - 1, stop);  // tokens whose row is the state's, or the wave's before
+      while (t < head) single();
+      T* op = static_cast<T*>(a.out) + (int64_t)(t - (W - 1)) * a.D + col;
+      for (; t + kRows <= own; t += kRows) {  // all of them this wave's, and their rows too
         vec_t xv[kRows], gv[kRows];
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-          xv[u] = *reinterpret_cast<const vec_t*>(xp + u * a.ldx);
-          gv[u] = *reinterpret_cast<const vec_t*>(gp + u * a.lddy);
+          xv[u] = __builtin_nontemporal_load(reinterpret_cast<const vec_t*>(xp + u * a.ldx));
+          gv[u] = __builtin_nontemporal_load(reinterpret_cast<const vec_t*>(gp + u * a.lddy));
         }
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) token(t + u, xv[u], gv[u]);
+        for (int u = 0; u < kRows; ++u) {
+          float sum[VEC];
+          token(xv[u], gv[u], true, sum);
+          vec_t o;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) put<T, VEC>(o, e, sum[e]);
+          __builtin_nontemporal_store(o, reinterpret_cast<vec_t*>(op + (int64_t)u * a.D));
+        }
         xp += kRows * a.ldx;
         gp += kRows * a.lddy;
+        op += (int64_t)kRows * a.D;
       }
-      for (; t < stop; ++t, xp += a.ldx, gp += a.lddy)
-        token(t, *reinterpret_cast<const vec_t*>(xp), *reinterpret_cast<const vec_t*>(gp));
+      while (t < stop) single();
       if (stop == s.eos) {  // the sequence's last rows: no token behind them
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
@@ -327,6 +333,13 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a) {
 #pragma unroll
             for (int k = j; k < W - 1; ++k) o = fmaf(w[W - 1 - (k - j)][e], dp[k][e], o);
             sum[e] = o;
+          }
+          if (a.dfinal) {  // these rows are the final state's
+           
+            const vec_t fv = *reinterpret_cast<const vec_t*>(
+                static_cast<const T*>(a.dfinal) + ((int64_t)seq * (W - 1) + j) * a.D + col);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) sum[e] += at<T, VEC>(fv, e);
           }
           emit(row, sum);
         }
@@ -394,53 +407,73 @@ __global__ __launch_bounds__(kThreads) void reduce_kernel(const float* __restric
 }
 
 // One token per request: the state's rows (the W - 1 inputs before it) and the token give y, and
-// the state moves on by one row in place. slots: as kda_recurrent_step_slots.
-template <typename T, int VEC, int W>
-__global__ __launch_bounds__(kThreads) void step_kernel(const T* __restrict__ x, int64_t ldx,
-                                                        const float* __restrict__ weight,
-                                                        const float* __restrict__ bias,
-                                                        T* __restrict__ pool,
-                                                        const int* __restrict__ slots, int nslots,
-                                                        T* __restrict__ y, int D, int silu) {
+// the state moves on by one row in place. slots: as kda_recurrent_step_slots. A lane takes its
+// channels of REQ requests, so that their taps (five times the bytes of a row) are read once for
+// all of them and all their loads are in flight together.
+constexpr int kStepThreads = 64;
+
+template <typename T, int VEC, int W, int REQ>
+__global__ __launch_bounds__(kStepThreads) void step_kernel(const T* __restrict__ x, int64_t ldx,
+                                                            const float* __restrict__ weight,
+                                                            const float* __restrict__ bias,
+                                                            T* __restrict__ pool,
+                                                            const int* __restrict__ slots, int nslots,
+                                                            T* __restrict__ y, int B, int D, int silu) {
   typedef row_t<T, VEC> vec_t;
-  const int col = (blockIdx.x * kThreads + threadIdx.x) * VEC;
+  const int col = (blockIdx.x * kStepThreads + threadIdx.x) * VEC;
   if (col >= D) return;
-  const int64_t n = blockIdx.y;
-  vec_t yv = vec_t{};
-  const int64_t slot = slots ? slots[n] : n;
-  if (slot >= 0 && slot < nslots) {
-    T* st = pool + slot * (W - 1) * D + col;
-    vec_t v[W];
+  const int64_t n0 = (int64_t)blockIdx.y * REQ;
+  vec_t v[REQ][W];
+  int64_t slot[REQ];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) v[k] = *reinterpret_cast<const vec_t*>(st + (int64_t)k * D);
-    v[W - 1] = *reinterpret_cast<const vec_t*>(x + n * ldx + col);
-    float pre[VEC];
+  for (int u = 0; u < REQ; ++u) {
+    const int64_t n = n0 + u;
+    slot[u] = n >= B ? -1 : slots ? slots[n] : n;
+    if (slot[u] >= nslots) slot[u] = -1;
+    if (slot[u] < 0) continue;
+    const T* st = pool + slot[u] * (W - 1) * D + col;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      pre[e] = bias ? bias[col + e] : 0.f;
-#pragma unroll
-      for (int k = 0; k < W; ++k) pre[e] = fmaf(weight[(size_t)(col + e) * W + k], at<T, VEC>(v[k], e), pre[e]);
-    }
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) *reinterpret_cast<vec_t*>(st + (int64_t)k * D) = v[k + 1];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) put<T, VEC>(yv, e, silu ? pre[e] * logistic(pre[e]) : pre[e]);
+    for (int k = 0; k < W - 1; ++k) v[u][k] = *reinterpret_cast<const vec_t*>(st + (int64_t)k * D);
+    v[u][W - 1] = *reinterpret_cast<const vec_t*>(x + n * ldx + col);
   }
-  *reinterpret_cast<vec_t*>(y + n * D + col) = yv;
+  float w[W][VEC], b[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k][e] = weight[(size_t)(col + e) * W + k];
+    b[e] = bias ? bias[col + e] : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < REQ; ++u) {
+    if (n0 + u >= B) break;
+    vec_t yv = vec_t{};
+    if (slot[u] >= 0) {
+      T* st = pool + slot[u] * (W - 1) * D + col;
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k) *reinterpret_cast<vec_t*>(st + (int64_t)k * D) = v[u][k + 1];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float pre = b[e];
+#pragma unroll
+        for (int k = 0; k < W; ++k) pre = fmaf(w[k][e], at<T, VEC>(v[u][k], e), pre);
+        put<T, VEC>(yv, e, silu ? pre * logistic(pre) : pre);
+      }
+    }
+    *reinterpret_cast<vec_t*>(y + (n0 + u) * D + col) = yv;
+  }
 }
 
 // ---- launchers
 
-// Elements a lane takes: the most (up to 16 bytes) that D, the strides and the pointers allow.
-inline int vec_of(int esize, int D, int64_t strides, const void* const* ptrs, int nptrs) {
-  int vec = 16 / esize;
+// Elements a lane takes: `vec` or the most that D, the strides and the pointers allow.
+inline int vec_of(int vec, int esize, int D, int64_t strides, const void* const* ptrs, int nptrs) {
   uintptr_t bits = 0;
   for (int i = 0; i < nptrs; ++i) bits |= reinterpret_cast<uintptr_t>(ptrs[i]);
   while (vec > 1 && (D % vec || strides % vec || bits % ((size_t)vec * esize))) vec /= 2;
   return vec;
 }
 
-// Row blocks: enough workgroups to fill the GPU (target), at least kSlices rows each.
+// Row blocks: enough workgroups to fill the GPU (target), kMinRows rows a slice at least.
 struct Grid {
   int ncb, nrb;
   int64_t rpb;
@@ -452,21 +485,32 @@ inline Grid make_grid(int T, int D, int vec, int target) {
   g.rpb = 1;
   if (T == 0) return g;
   int64_t nrb = target / g.ncb;
-  const int64_t most = ((int64_t)T + kSlices - 1) / kSlices;
+  const int64_t most = ((int64_t)T + kSlices * kMinRows - 1) / (kSlices * kMinRows);
   nrb = nrb < 1 ? 1 : nrb > most ? most : nrb;
   g.rpb = ((int64_t)T + nrb - 1) / nrb;
   g.nrb = (int)((T + g.rpb - 1) / g.rpb);
   return g;
 }
 
-constexpr int kFwdBlocks = 4096, kBwdBlocks = 1024;
+constexpr int kFwdBlocks = 4096, kBwdBlocks = 3 * 256;
+// The backward holds 3 W - 1 floats a channel, so four channels a lane, not eight of bf16, and the
+// resulting three workgroups a CU are launched in one round: 238 us at 32768 x 6144, bf16 (5.1
+// TB/s), against 284 with eight channels and 277 with 1024 workgroups (a third of them in a second
+// round). The forward (162 us, 5.0 TB/s) is fastest with several rounds of eight channels a lane.
+constexpr int kBwdVec = 4;
 
 template <typename T, int VEC, int W>
 hipError_t run(int what, Args a, const ConvStep* st, float* dweight, float* dbias, hipStream_t stream) {
   if (what == 2) {
-    hipLaunchKernelGGL((step_kernel<T, VEC, W>), dim3((a.D / VEC + kThreads - 1) / kThreads, st->B),
-                       dim3(kThreads), 0, stream, static_cast<const T*>(a.x), a.ldx, a.weight, a.bias,
-                       static_cast<T*>(st->pool), st->slots, st->nslots, static_cast<T*>(a.out), a.D, a.silu);
+    const int ncb = (a.D / VEC + kStepThreads - 1) / kStepThreads;
+    auto go = [&](auto kernel, int req) {
+      hipLaunchKernelGGL(kernel, dim3(ncb, (st->B + req - 1) / req), dim3(kStepThreads), 0, stream,
+                         static_cast<const T*>(a.x), a.ldx, a.weight, a.bias, static_cast<T*>(st->pool),
+                         st->slots, st->nslots, static_cast<T*>(a.out), st->B, a.D, a.silu);
+    };
+    // several requests a lane where that leaves two waves a CU or more
+    if ((int64_t)ncb * st->B >= 4 * 512) go(step_kernel<T, VEC, W, 4>, 4);
+    else go(step_kernel<T, VEC, W, 1>, 1);
     return hipGetLastError();
   }
   const Grid g = make_grid(a.T, a.D, VEC, what == 0 ? kFwdBlocks : kBwdBlocks);
@@ -475,8 +519,9 @@ hipError_t run(int what, Args a, const ConvStep* st, float* dweight, float* dbia
   const dim3 grid(g.ncb, g.nrb + (a.out_state ? (a.N + kSlices - 1) / kSlices : 0));
   hipError_t e = hipSuccess;
   if (grid.y > 0) {
-    if (what == 0) hipLaunchKernelGGL((fwd_kernel<T, VEC, W>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((bwd_kernel<T, VEC, W>), grid, dim3(kThreads), 0, stream, a);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a); };
+    if (what == 0) a.silu ? go(fwd_kernel<T, VEC, W, true>) : go(fwd_kernel<T, VEC, W, false>);
+    else if constexpr (VEC <= kBwdVec) a.silu ? go(bwd_kernel<T, VEC, W, true>) : go(bwd_kernel<T, VEC, W, false>);
     e = hipGetLastError();
   }
   if (what == 0) return e;
@@ -511,9 +556,9 @@ inline hipError_t dispatch(int what, const Args& a, int W, bool bf, int vec, con
 }  // namespace conv
 
 // Partial sums of the backward: sized for the narrowest vector (the most row blocks).
-size_t conv_bwd_workspace_bytes(int T, int D, int W, bool bf) {
+size_t conv_bwd_workspace_bytes(int T, int D, int W) {
   int64_t nrb = 0;
-  for (int vec = bf ? 8 : 4; vec >= 1; vec /= 2) {
+  for (int vec = conv::kBwdVec; vec >= 1; vec /= 2) {
     if (D % vec) continue;
     const conv::Grid g = conv::make_grid(T, D, vec, conv::kBwdBlocks);
     nrb = nrb > g.nrb ? nrb : g.nrb;
@@ -526,7 +571,7 @@ hipError_t launch_conv_fwd(const ConvArgs& p, hipStream_t stream) {
   a.x = p.x, a.ldx = p.ldx, a.weight = p.weight, a.bias = p.bias, a.init = p.init, a.seqs = make_sequences(p.cu, p.N, p.T);
   a.N = p.N, a.T = p.T, a.D = p.D, a.silu = p.silu, a.zero_rest = p.zero_rest, a.out_state = p.out_state, a.out = p.out;
   const void* ptrs[] = {p.x, p.init, p.out_state, p.out};
-  const int vec = conv::vec_of(p.bf ? 2 : 4, p.D, p.ldx, ptrs, 4);
+  const int vec = conv::vec_of(p.bf ? 8 : 4, p.bf ? 2 : 4, p.D, p.ldx, ptrs, 4);
   return conv::dispatch(0, a, p.W, p.bf, vec, nullptr, nullptr, nullptr, stream);
 }
 
@@ -537,7 +582,7 @@ hipError_t launch_conv_bwd(const ConvArgs& p, const void* dy, int64_t lddy, cons
   a.N = p.N, a.T = p.T, a.D = p.D, a.silu = p.silu, a.zero_rest = p.zero_rest, a.out_state = p.out_state, a.out = p.out;
   a.dy = dy, a.lddy = lddy, a.dfinal = dfinal, a.part = static_cast<float*>(workspace);
   const void* ptrs[] = {p.x, p.init, p.out_state, p.out, dy, dfinal};
-  const int vec = conv::vec_of(p.bf ? 2 : 4, p.D, p.ldx | lddy, ptrs, 6);
+  const int vec = conv::vec_of(conv::kBwdVec, p.bf ? 2 : 4, p.D, p.ldx | lddy, ptrs, 6);
   return conv::dispatch(1, a, p.W, p.bf, vec, nullptr, dweight, dbias, stream);
 }
 
@@ -546,7 +591,7 @@ hipError_t launch_conv_step(const ConvArgs& p, const ConvStep& st, hipStream_t s
   a.x = p.x, a.ldx = p.ldx, a.weight = p.weight, a.bias = p.bias;
   a.D = p.D, a.silu = p.silu, a.out = p.out;
   const void* ptrs[] = {p.x, st.pool, p.out};
-  const int vec = conv::vec_of(p.bf ? 2 : 4, p.D, p.ldx, ptrs, 3);
+  const int vec = conv::vec_of(p.bf ? 8 : 4, p.bf ? 2 : 4, p.D, p.ldx, ptrs, 3);
   return conv::dispatch(2, a, p.W, p.bf, vec, &st, nullptr, nullptr, stream);
 }
 

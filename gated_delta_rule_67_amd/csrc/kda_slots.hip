@@ -4,14 +4,17 @@
 // is [num_slots] slots of slot_bytes bytes; one call moves the same slots of many pools (a
 // model's layers), in one launch per kMaxPools of them.
 //
-// The work is one read and one write of what moves, so HBM bounds it. Its items (pool, pair,
-// 32 KB piece) are dealt out to at most kBlocks workgroups of 256 lanes, each lane with eight
-// 16-byte loads in flight before its stores.
+// The work is one read and one write of what moves, so HBM bounds it: 24 slots of 1 MB in each of
+// 18 pools take 158 us (5.7 TB/s). Its items (pool, pair, piece of a slot) are dealt out to at most
+// kBlocks workgroups of 256 lanes, each lane with up to eight 16-byte loads in flight before its
+// stores; pieces are 32 KB, or smaller where there would be too few items for the GPU.
 //
 // The pairs of one call apply in order. Where no destination is named twice or is another pair's
 // source, the order does not matter and all items run side by side. Every workgroup finds that
 // out for itself, once, with a bitmap of the destinations in LDS; where it does matter, each
 // piece of a slot is taken through all pairs, in order, by the same lanes of one workgroup.
+#include <type_traits>
+
 #include "kda_device.h"
 
 namespace kda {
@@ -19,7 +22,8 @@ namespace slots {
 
 constexpr int kThreads = 256;
 constexpr int kBlocks = 2048;       // eight workgroups a CU
-constexpr int kPiece = 32 << 10;    // bytes of an item: eight 16-byte accesses a lane
+constexpr int kPiece = 32 << 10;    // bytes of an item at most: eight 16-byte accesses a lane
+constexpr int kSmallPiece = 4 << 10;
 constexpr int kMaxPools = 64;       // pools of a launch (their table is a kernel argument)
 
 struct Pools {
@@ -32,21 +36,25 @@ template <typename U>
 __device__ __forceinline__ void move_piece(char* to, const char* from, int len) {
   constexpr int kStep = kThreads * (int)sizeof(U);
   int i = threadIdx.x * (int)sizeof(U);
-  for (; i + 7 * kStep < len; i += 8 * kStep) {
-    U v[8];
+  auto batch = [&](auto count) {
+    constexpr int kCount = decltype(count)::value;
+    for (; i + (kCount - 1) * kStep < len; i += kCount * kStep) {
+      U v[kCount];
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      v[u] = from ? __builtin_nontemporal_load(reinterpret_cast<const U*>(from + i + u * kStep)) : U{};
+      for (int u = 0; u < kCount; ++u)
+        v[u] = from ? __builtin_nontemporal_load(reinterpret_cast<const U*>(from + i + u * kStep)) : U{};
 #pragma unroll
-    for (int u = 0; u < 8; ++u) __builtin_nontemporal_store(v[u], reinterpret_cast<U*>(to + i + u * kStep));
-  }
-  for (; i < len; i += kStep)
-    *reinterpret_cast<U*>(to + i) = from ? *reinterpret_cast<const U*>(from + i) : U{};
+      for (int u = 0; u < kCount; ++u) __builtin_nontemporal_store(v[u], reinterpret_cast<U*>(to + i + u * kStep));
+    }
+  };
+  batch(std::integral_constant<int, 8>{});
+  batch(std::integral_constant<int, 4>{});
+  batch(std::integral_constant<int, 1>{});
 }
 
-__device__ __forceinline__ void move_item(char* base, int64_t bytes, int piece, int from, int to) {
-  const int64_t off = (int64_t)piece * kPiece;
-  const int len = (int)(bytes - off < kPiece ? bytes - off : kPiece);
+__device__ __forceinline__ void move_item(char* base, int64_t bytes, int size, int piece, int from, int to) {
+  const int64_t off = (int64_t)piece * size;
+  const int len = (int)(bytes - off < size ? bytes - off : size);
   char* d = base + (int64_t)to * bytes + off;
   const char* s = from < 0 ? nullptr : base + (int64_t)from * bytes + off;
   const uintptr_t bits = reinterpret_cast<uintptr_t>(base) | (uintptr_t)bytes;
@@ -57,7 +65,7 @@ __device__ __forceinline__ void move_item(char* base, int64_t bytes, int piece, 
 }
 
 // moves: device count of pairs that are known to be independent (compaction), or null: n pairs.
-__global__ __launch_bounds__(kThreads) void copy_kernel(Pools pools, int npools, int pieces,
+__global__ __launch_bounds__(kThreads) void copy_kernel(Pools pools, int npools, int pieces, int size,
                                                         const int* __restrict__ src,
                                                         const int* __restrict__ dst, int n,
                                                         const int* __restrict__ moves, int nslots) {
@@ -90,14 +98,14 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(Pools pools, int npools,
     const int64_t rest = it / pieces;
     const int pool = (int)(rest % npools);
     const int64_t bytes = pools.bytes[pool];
-    if ((int64_t)piece * kPiece >= bytes) continue;
+    if ((int64_t)piece * size >= bytes) continue;
     if (!order) {
       const int i = (int)(rest / npools);
-      if (valid(i)) move_item(pools.base[pool], bytes, piece, src[i], dst[i]);
+      if (valid(i)) move_item(pools.base[pool], bytes, size, piece, src[i], dst[i]);
     } else {
       for (int i = 0; i < n; ++i)
         if (valid(i)) {
-          move_item(pools.base[pool], bytes, piece, src[i], dst[i]);
+          move_item(pools.base[pool], bytes, size, piece, src[i], dst[i]);
           // a lane reads back only what it wrote itself; the fence keeps its accesses in order
           __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
         }
@@ -163,17 +171,21 @@ hipError_t launch_copy(void* const* base, const size_t* bytes, int npools, int n
   for (int p0 = 0; p0 < npools; p0 += kMaxPools) {
     Pools pools{};
     const int np = npools - p0 < kMaxPools ? npools - p0 : kMaxPools;
-    int64_t most = 0;
+    int64_t most = 0, total = 0;
     for (int i = 0; i < np; ++i) {
       pools.base[i] = static_cast<char*>(base[p0 + i]);
       pools.bytes[i] = (int64_t)bytes[p0 + i];
       most = most > pools.bytes[i] ? most : pools.bytes[i];
+      total += pools.bytes[i];
     }
-    const int64_t pieces = (most + kPiece - 1) / kPiece;
+    // an item for every workgroup, if pieces of 4 KB or more can do that
+    const int64_t each = total / kBlocks > kPiece / n ? kPiece : total * n / kBlocks;
+    const int size = each >= kPiece ? kPiece : each <= kSmallPiece ? kSmallPiece : (int)(each / kSmallPiece * kSmallPiece);
+    const int64_t pieces = (most + size - 1) / size;
     const int64_t items = pieces * np * n;
     const int lds = moves || n < 2 ? 0 : (nslots + 31) / 32 * 4;
     hipLaunchKernelGGL(copy_kernel, dim3((unsigned)(items < kBlocks ? items : kBlocks)), dim3(kThreads), lds,
-                       stream, pools, np, (int)pieces, src, dst, n, moves, nslots);
+                       stream, pools, np, (int)pieces, size, src, dst, n, moves, nslots);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
