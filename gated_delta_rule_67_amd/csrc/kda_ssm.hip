@@ -79,13 +79,14 @@ struct Stage {
   static constexpr bool kEven = kPieces * THREADS == ROWS * kRow;  // every thread holds as many
   u32x4 v[kPieces];
 
-  // src: row 0, column 0; ld: elements between rows; rows behind `rows` and columns behind
-  // `width` of a block read zeros.
-  __device__ __forceinline__ void load(const T* src, int64_t ld, int rows, int width) {
+  // base: column 0 of token 0; ld: elements between tokens (<= 2^24); tokens behind t0 + rows and
+  // columns behind `width` of a block read zeros.
+  __device__ __forceinline__ void load(const T* base, int ld, int t0, int rows, int width) {
     constexpr int kBlocks = COLS / PAD;
-    const __amdgpu_buffer_rsrc_t r =
-        make_rsrc(src, rows ? (unsigned)((((int64_t)rows - 1) * ld + (int64_t)kBlocks * width) * sizeof(T)) : 0u);
-    const unsigned rowb = (unsigned)(ld * sizeof(T));
+    // up to the last row's last column, without a branch; nothing for no rows
+    const unsigned elems = (unsigned)(rows * ld) - (unsigned)(min(rows, 1) * (ld - kBlocks * width));
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(base + (int64_t)t0 * ld, elems * (unsigned)sizeof(T));
+    const unsigned rowb = (unsigned)ld * (unsigned)sizeof(T);
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
       const int piece = threadIdx.x + THREADS * e, row = piece / kRow, c = piece % kRow * kElem;
@@ -204,6 +205,7 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
   // row lengths with the fewest bank conflicts for these (cycles of a 1 KB read: c 4 instead of 6
   // at 272 bytes a row, b 6 and, transposed, 3.4 instead of 6)
   constexpr int LDC = BF ? NP + 16 : NP + 4, LDB = BF ? (NT == 8 ? 160 : 104) : NP + 4;
+  static_assert(BF || PT == 1, "float32 products take the wave's columns in order");
   static_assert(XC <= 16 * PT * NW && NT % 2 == 0 && PP % (16 * PT) == 0, "tile shape");
   __shared__ __attribute__((aligned(16))) T Xs[kTok * LDX];
   __shared__ __attribute__((aligned(16))) T Bs[kTok * LDB];
@@ -280,13 +282,13 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
   Stage<T, kThreads, kTok, XC, PP, VEC> xr;
   Stage<T, kThreads, kTok, NP, NP, VEC> br, cr;
   T dtr = from_f32<T>(0.f);
+  const int ldx = (int)a.ldx, ldb = (int)a.ldb, ldc = (int)a.ldc, lddt = (int)a.lddt;
   auto load = [&](const Tile& t) {
-    xr.load(static_cast<const T*>(a.x) + (int64_t)t.t0 * a.ldx + (int64_t)h0 * V + v0, a.ldx, t.rows, width);
-    br.load(static_cast<const T*>(a.b) + (int64_t)t.t0 * a.ldb + (int64_t)grp * K, a.ldb, t.rows, K);
-    if constexpr (OUT)
-      cr.load(static_cast<const T*>(a.c) + (int64_t)t.t0 * a.ldc + (int64_t)grp * K, a.ldc, t.rows, K);
-    const __amdgpu_buffer_rsrc_t rd = make_rsrc(static_cast<const T*>(a.dt) + (int64_t)t.t0 * a.lddt + h0, 0x7fffffffu);
-    const unsigned off = dw >= 0 && lane < t.rows ? (unsigned)(lane * a.lddt + dw) * (unsigned)sizeof(T) : kOutOfRange;
+    xr.load(static_cast<const T*>(a.x) + (int64_t)h0 * V + v0, ldx, t.t0, t.rows, width);
+    br.load(static_cast<const T*>(a.b) + (int64_t)grp * K, ldb, t.t0, t.rows, K);
+    if constexpr (OUT) cr.load(static_cast<const T*>(a.c) + (int64_t)grp * K, ldc, t.t0, t.rows, K);
+    const __amdgpu_buffer_rsrc_t rd = make_rsrc(static_cast<const T*>(a.dt) + (int64_t)t.t0 * lddt + h0, 0x7fffffffu);
+    const unsigned off = dw >= 0 && lane < t.rows ? (unsigned)(lane * lddt + dw) * (unsigned)sizeof(T) : kOutOfRange;
     if constexpr (BF) dtr = __builtin_bit_cast(T, (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(rd, off, 0, 0));
     else dtr = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(rd, off, 0, 0));
   };
@@ -297,7 +299,10 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
   }
   const float skip = a.D ? a.D[hv] : 0.f;
 
-  // column 16 pt + lr of the wave's; rows 16 nt + 4 lq .. + 3, or, for bf16, in the order in which
+  // Columns of the wave's 16 PT: index 4 q + r of tile pt is column 4 PT q + 4 pt + r, so that the four
+  // consecutive rows that a lane holds of each tile of y^T join to 4 PT consecutive columns.
+  auto column = [](int pt, int q, int r) { return 4 * PT * q + 4 * pt + r; };
+  // column index lr; rows 16 nt + 4 lq .. + 3, or, for bf16, in the order in which
   // two tiles make an operand of the next product: 32 (nt / 2) + 8 lq + 4 (nt % 2) .. + 3
   f32x4 S[PT][NT];
   // this wave's part of a [K, V] float32 state in memory; elements outside of it read zeros and
@@ -308,7 +313,7 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
     asm volatile("" : "+v"(n));  // the offsets are made here, not kept over the tile loop
 #pragma unroll
     for (int pt = 0; pt < PT; ++pt) {
-      const int p = p0 + 16 * pt + lr;
+      const int p = p0 + column(pt, lr >> 2, lr & 3);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -452,32 +457,34 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
 
     if (active) {
       // y of 16 tokens and this wave's columns (rows p), from accumulators that hold it transposed
-      const unsigned yrow = (unsigned)(ldy * sizeof(T));
-      const __amdgpu_buffer_rsrc_t yb = make_rsrc(y + (int64_t)cur.t0 * ldy + (int64_t)hv * V, 0x7fffffffu);
-      auto store_y = [&](int i, const f32x4 (&acc)[PT]) {
+      const unsigned yrow = (unsigned)ldy * (unsigned)sizeof(T);
+      // the buffer ends with the tile's last row; columns behind V lie out of its range
+      const __amdgpu_buffer_rsrc_t yb = make_rsrc(y + (int64_t)cur.t0 * ldy + (int64_t)hv * V,
+                                                  (unsigned)(cur.rows - 1) * yrow + (unsigned)V * (unsigned)sizeof(T));
+      const int py = p0 + column(0, lq, 0);  // the first of this lane's columns of y
+      const unsigned yoff = (unsigned)lr * yrow + (py < V ? (unsigned)py * (unsigned)sizeof(T) : kOutOfRange);
+      auto store_y = [&](int it, const f32x4 (&acc)[PT]) {
+        const unsigned at = yoff + (unsigned)(16 * it) * yrow;
+        if constexpr (VEC && BF && PT == 2) {
+          const u32x4 o = {pack2(acc[0][0], acc[0][1]), pack2(acc[0][2], acc[0][3]),
+                           pack2(acc[PT - 1][0], acc[PT - 1][1]), pack2(acc[PT - 1][2], acc[PT - 1][3])};
+          __builtin_amdgcn_raw_buffer_store_b128(o, yb, at, 0, 0);
+        } else if constexpr (VEC && BF) {
+          typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+          const u32x2 o = {pack2(acc[0][0], acc[0][1]), pack2(acc[0][2], acc[0][3])};
+          __builtin_amdgcn_raw_buffer_store_b64(o, yb, at, 0, 0);
+        } else if constexpr (VEC) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[0]), yb, at, 0, 0);
+        } else {
 #pragma unroll
-        for (int pt = 0; pt < PT; ++pt) {
-          const int p = p0 + 16 * pt + 4 * lq;
-          const unsigned off = (unsigned)i * yrow + (unsigned)p * sizeof(T);
-          if constexpr (VEC) {
-            unsigned at = i < cur.rows && p < V ? off : kOutOfRange;
-            asm volatile("" : "+v"(at));  // stays a select: a branch would leave the number of stores open
-            if constexpr (BF) {
-              typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-              const u32x2 o = {pack2(acc[pt][0], acc[pt][1]), pack2(acc[pt][2], acc[pt][3])};
-              __builtin_amdgcn_raw_buffer_store_b64(o, yb, at, 0, 0);
-            } else {
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[pt]), yb, at, 0, 0);
-            }
-          } else {
+          for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const unsigned at = i < cur.rows && p + r < V ? off + r * (unsigned)sizeof(T) : kOutOfRange;
+              const unsigned off = py + 4 * pt + r < V ? at + (4 * pt + r) * (unsigned)sizeof(T) : kOutOfRange;
               const T o = from_f32<T>(acc[pt][r]);
-              if constexpr (BF) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, o), yb, at, 0, 0);
-              else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, o), yb, at, 0, 0);
+              if constexpr (BF) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, o), yb, off, 0, 0);
+              else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, o), yb, off, 0, 0);
             }
-          }
         }
       };
       // 2^(G_i) (S^T c_i) + D x_i, ahead of the products inside the tile
@@ -487,7 +494,7 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
         for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            acc[pt][r] = acc[pt][r] * eg + skip * to_f32(Xs[i * LDX + col0 + 16 * pt + 4 * lq + r]);
+            acc[pt][r] = acc[pt][r] * eg + skip * to_f32(Xs[i * LDX + col0 + column(pt, lq, r)]);
       };
       const float ga = fast_exp2(dec[hh].end);
       if constexpr (BF) {
@@ -497,7 +504,7 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
         for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks) {
-            const bf16* src = Xs + (32 * ks + 8 * lq + (lr >> 2)) * LDX + col0 + 16 * pt + 4 * (lr & 3);
+            const bf16* src = Xs + (32 * ks + 8 * lq + (lr >> 2)) * LDX + col0 + column(pt, lr & 3, 0);
             xf[pt][ks] = join(load_tr4(src), load_tr4(src + 4 * LDX));
           }
         if constexpr (OUT) {
@@ -529,7 +536,7 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
 #pragma unroll
               for (int pt = 0; pt < PT; ++pt) acc[pt] = mfma(xf[pt][ks], mv, acc[pt]);
             }
-            store_y(i, acc);
+            store_y(it, acc);
           }
         }
         // the next tile's loads go out here: their registers are free only now
@@ -552,7 +559,7 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
               float a0 = low(xu[e]) * (e < 2 ? wa[2 * e] : wb[2 * e - 4]);
               float a1 = high(xu[e]) * (e < 2 ? wa[2 * e + 1] : wb[2 * e - 3]);
               const unsigned u0 = pack2(a0, a1);
-              a0 -= low(u0), a1 -= high(u0);
+              a0 = a0 - low(u0), a1 = a1 - high(u0);
               const unsigned u1 = pack2(a0, a1);
               w0[pt][e] = u0;
               w1[pt][e] = u1;
@@ -595,7 +602,7 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
 #pragma unroll
               for (int pt = 0; pt < PT; ++pt)
                 acc[pt] = mfma(Xs[(j + lq) * LDX + col0 + 16 * pt + lr], Ms[i * LDM + j + lq], acc[pt]);
-            store_y(i, acc);
+            store_y(it, acc);
           }
           load(nxt);
         }
