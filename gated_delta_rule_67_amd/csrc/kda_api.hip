@@ -595,10 +595,10 @@ static int check_ssm(int H, int HV, int K, int V, int dtype) {
   return HV > (1 << 16) ? KDA_ERR_UNSUPPORTED : KDA_OK;
 }
 
-// Token strides (elements) of n > 1 tokens: no overlap, and a tile's offsets fit 31 bits.
-static int check_stride(int64_t stride, int64_t width, int n) {
-  if (n > 1 && stride < width) return KDA_ERR_INVALID;
-  return stride < 0 || stride > (1 << 24) ? KDA_ERR_UNSUPPORTED : KDA_OK;
+// Elements between tokens: no overlap, and a tile's offsets fit 31 bits.
+static int check_stride(int64_t stride, int64_t width) {
+  if (stride < width) return KDA_ERR_INVALID;
+  return stride > (1 << 24) ? KDA_ERR_UNSUPPORTED : KDA_OK;
 }
 
 size_t kda_ssm_chunk_fwd_workspace_size(int N, int T, int packed, int H, int HV, int K, int V, int dtype) {
@@ -617,10 +617,12 @@ int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* dt, int64_t d
   int rc = check_ssm(H, HV, K, V, dtype);
   if (rc != KDA_OK) return rc;
   if (!A_log || (T > 0 && (!x || !dt || !b || !c || !y))) return KDA_ERR_INVALID;
-  const int64_t strides[] = {x_stride, dt_stride, b_stride, c_stride};
   const int64_t widths[] = {(int64_t)HV * V, HV, (int64_t)H * K, (int64_t)H * K};
-  for (int i = 0; i < 4; ++i)
-    if ((rc = check_stride(strides[i], widths[i], T)) != KDA_OK) return rc;
+  int64_t* strides[] = {&x_stride, &dt_stride, &b_stride, &c_stride};
+  for (int i = 0; i < 4; ++i) {
+    if (T < 2) *strides[i] = widths[i];  // one token: its stride has no meaning
+    if ((rc = check_stride(*strides[i], widths[i])) != KDA_OK) return rc;
+  }
   if (N > (1 << 20)) return KDA_ERR_UNSUPPORTED;
   const size_t need = kda_ssm_chunk_fwd_workspace_size(N, T, cu_seqlens != nullptr, H, HV, K, V, dtype);
   if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_INVALID;
@@ -631,6 +633,7 @@ int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* dt, int64_t d
   a.s0 = initial_state, a.seqs = kda::make_sequences(cu_seqlens, N, T), a.N = N, a.T = T, a.H = H, a.HV = HV, a.K = K, a.V = V;
   a.sT = final_state, a.y = y, a.bf = dtype == KDA_DTYPE_BF16, a.zero_rest = (flags & KDA_ZERO_REST) != 0;
   const hipError_t e = kda::launch_ssm_prefill(a, workspace, static_cast<hipStream_t>(stream));
+  if (e == hipErrorNotSupported) return KDA_ERR_UNSUPPORTED;  // more workgroups than a launch takes
   return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 

@@ -13,13 +13,22 @@
 // reads are rounded to bf16, as y is; the state itself keeps float32 accuracy: b is bf16 as given,
 // and the weighted x of its update is split into three bf16 terms (8 bits each), three products.
 //
-// A workgroup of four waves owns 64 PT columns: one or more value heads of one b / c pair, whose
-// b, c and c . b products they share, and carries the state in accumulators (16 PT columns a
-// wave) over the tiles of one segment of the token axis. Segments have equal lengths whatever the
-// sequences: a tile ends at the sequence's end. float32 inputs take the same steps with tiles of
-// 32 tokens, 16x16x4 float32 products and nothing rounded. With more than one segment, a pass over the tiles
+// A workgroup of four waves owns 64 or 128 columns: one or two value heads of one b / c pair, whose
+// b, c and c . b products they share, and carries the state in accumulators (16 PT columns a wave)
+// over the tiles of one segment of the token axis. Segments have equal lengths whatever the
+// sequences: a tile ends at the sequence's end. With more than one segment, a pass over the tiles
 // of each boundary's sequence without outputs (OUT = false) gives the state that leaves the
 // segment, a scan composes them, and the pass with outputs starts from the composed states.
+// float32 inputs take the same steps with tiles of 32 tokens, 16x16x4 float32 products and nothing
+// rounded.
+//
+// Measured at 4 x 8192 tokens, 64 heads x 64, K = 128, 8 pairs, bf16: 355 us (251 pass with
+// outputs, 90 without, 13 scan) for 684 MB, 115 us at a copy's rate. A tile of two heads takes a
+// workgroup about 14,000 cycles beside a second one on its CU: 2,000 for M, 3,500 for y, 3,800 for
+// the state (its 96 products of a wave are at 0.9 of the matrix cores' rate, two waves a SIMD), 2,000
+// until the next tile's loads are issued, 800 for LDS stores. No single pipeline is full (VALU 45%,
+// matrix cores 30%, LDS 34% of the cycles); tiles of 32 tokens, eight waves of 16 columns and one or
+// three workgroups a CU were slower or the same.
 #include "kda_ssm.h"
 
 namespace kda {
@@ -28,7 +37,7 @@ namespace ssm {
 // Tokens of a tile. float32 takes half as many: its products are 16 times as expensive, and those
 // inside a tile grow with it.
 template <typename T> constexpr int kTokens = sizeof(T) == 2 ? 64 : 32;
-constexpr int kCompose = 256;  // threads of a composing workgroup
+constexpr int kThreads = 256;
 constexpr unsigned kOutOfRange = 0x80000000u;  // buffer loads there read zeros
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -72,11 +81,11 @@ struct Tile {
 // A ROWS x COLS matrix on its way from memory to LDS: each thread holds pieces of 16 bytes.
 // Columns are blocks of PAD, of which `width` are real. VEC: every real row of a block is whole
 // 16-byte pieces, aligned in memory.
-template <typename T, int THREADS, int ROWS, int COLS, int PAD, bool VEC>
+template <typename T, int ROWS, int COLS, int PAD, bool VEC>
 struct Stage {
   static constexpr int kElem = 16 / sizeof(T), kRow = COLS / kElem;
-  static constexpr int kPieces = (ROWS * kRow + THREADS - 1) / THREADS;
-  static constexpr bool kEven = kPieces * THREADS == ROWS * kRow;  // every thread holds as many
+  static constexpr int kPieces = (ROWS * kRow + kThreads - 1) / kThreads;
+  static constexpr bool kEven = kPieces * kThreads == ROWS * kRow;  // every thread holds as many
   u32x4 v[kPieces];
 
   // base: column 0 of token 0; ld: elements between tokens (<= 2^24); tokens behind t0 + rows and
@@ -89,7 +98,7 @@ struct Stage {
     const unsigned rowb = (unsigned)ld * (unsigned)sizeof(T);
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
-      const int piece = threadIdx.x + THREADS * e, row = piece / kRow, c = piece % kRow * kElem;
+      const int piece = threadIdx.x + kThreads * e, row = piece / kRow, c = piece % kRow * kElem;
       const int blk = c / PAD, p = c - blk * PAD;
       const unsigned off = (unsigned)row * rowb + (unsigned)(blk * width + p) * sizeof(T);
       auto in = [&](int k) { return p + k < width && (kEven || row < ROWS) ? off + k * (unsigned)sizeof(T) : kOutOfRange; };
@@ -112,7 +121,7 @@ struct Stage {
   __device__ __forceinline__ void store(T* dst, int ldd) const {
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
-      const int piece = threadIdx.x + THREADS * e, row = piece / kRow, c = piece % kRow * kElem;
+      const int piece = threadIdx.x + kThreads * e, row = piece / kRow, c = piece % kRow * kElem;
       if (kEven || row < ROWS) *reinterpret_cast<u32x4*>(dst + row * ldd + c) = v[e];
     }
   }
@@ -124,11 +133,15 @@ struct Decay {
   float eg[64], w[64];  // 2^G, and D 2^(G_63 - G)
   float end, pad[3];    // G_63, the whole tile's
 };
+constexpr float kFactorSpan = 64.f;
 struct Inner {
   float dt[64], hi[64], lo[64];  // D, and G as a sum of two floats (log2 units)
-  // between blocks of 16 tokens, over the last token q = 16 it - 1 in front of block it:
-  // row[i] = 2^(G_i - G_q) for i in it, col[8 it (it - 1) + j] = D_j 2^(G_q - G_j) for j <= q
-  float row[64], col[96];
+  // M between token i of a block of 16 tokens and token j at or in front of its end, over the last
+  // token q in front of the block (G_q = 0 for the first): row[i] = 2^(G_i - G_q) <= 1, and
+  // col[8 it (it + 1) + j] = D_j 2^(G_q - G_j) for block it. For j inside the block that factor is
+  // at most 2^kFactorSpan D_j, unless `wide` says that some block decays further than that.
+  float row[64], col[160];
+  int wide, pad[3];
 };
 
 // v of the lane `OP` names (a DPP control); lanes without one, or masked out, get 0.
@@ -175,12 +188,15 @@ __device__ __forceinline__ void make_decay(Decay& d, Inner& m, float raw, bool i
   if constexpr (BLOCKS) {
     double before = 0.0;  // G of the token in front of this lane's block
 #pragma unroll
-    for (int it = 1; it < 4; ++it) {
-      const double q = read_lane(g, 16 * it - 1);
-      if (lane < 16 * it) m.col[8 * it * (it - 1) + lane] = dt * fast_exp2((float)(q - g));
-      else before = q;
+    for (int it = 0; it < 4; ++it) {
+      const double q = it ? read_lane(g, 16 * it - 1) : 0.0;
+      if (lane >= 16 * it) before = q;
+      if (lane < 16 * (it + 1)) m.col[8 * it * (it + 1) + lane] = dt * fast_exp2((float)(q - g));
     }
-    m.row[lane] = fast_exp2((float)(g - before));
+    const float f = (float)(g - before);
+    m.row[lane] = fast_exp2(f);
+    const bool wide = wave_any(!(f >= -kFactorSpan));
+    if (lane == 0) m.wide = wide;
   }
 }
 
@@ -191,13 +207,10 @@ __device__ __forceinline__ unsigned pack2(float a, float b) {
 __device__ __forceinline__ float low(unsigned u) { return __builtin_bit_cast(float, u << 16); }
 __device__ __forceinline__ float high(unsigned u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
 
-// Waves of a workgroup: 16 PT columns each, four at least.
-template <int PP, int HB, int PT> constexpr int kWaves = PP * HB > 64 * PT ? PP * HB / (16 * PT) : 4;
-
 // NT: K in tiles of 16; HB heads of PP columns; PT tiles of 16 columns a wave.
 template <typename T, int NT, int PP, int HB, int PT, bool OUT, bool VEC>
-__global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8 ? 4 : 2)) void prefill_kernel(SsmArgs a, int hblocks) {
-  constexpr int NW = kWaves<PP, HB, PT>, kThreads = 64 * NW;
+__global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hblocks) {
+  constexpr int NW = kThreads / 64;
   constexpr bool BF = sizeof(T) == 2;
   constexpr int kTok = kTokens<T>, kPad = 16 / sizeof(T);
   constexpr int XC = HB * PP, NP = 16 * NT, LDX = XC + kPad, LDM = kTok + kPad, KS = NT / 2;
@@ -279,8 +292,8 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
         y[t * ldy + (int64_t)(h0 + i / width) * V + v0 + i % width] = from_f32<T>(0.f);
   };
 
-  Stage<T, kThreads, kTok, XC, PP, VEC> xr;
-  Stage<T, kThreads, kTok, NP, NP, VEC> br, cr;
+  Stage<T, kTok, XC, PP, VEC> xr;
+  Stage<T, kTok, NP, NP, VEC> br, cr;
   T dtr = from_f32<T>(0.f);
   const int ldx = (int)a.ldx, ldb = (int)a.ldb, ldc = (int)a.ldc, lddt = (int)a.lddt;
   auto load = [&](const Tile& t) {
@@ -397,7 +410,7 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
       // c . b transposed (rows j, columns i) in blocks of 16, then M of each head. The blocks at
       // and below the diagonal, dealt out evenly; those above are read as part of a product of 32
       // tokens only where they are zeros from the start.
-      constexpr int kBlocks = !BF ? 1 : NW == 8 ? 2 : 3;  // a wave's blocks: i and j, four bits each, lowest first
+      constexpr int kBlocks = BF ? 3 : 1;  // a wave's blocks: i and j, four bits each, lowest first
       int fresh = 0;
       asm volatile("" : "+v"(fresh));  // as above: made in every tile
       const int wv = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) + fresh);
@@ -405,12 +418,24 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
       if constexpr (!BF) {
         its = wv == 0 ? 0x0 : wv < 3 ? 0x1 : 0xf;
         jts = wv == 2 ? 0x1 : 0x0;
-      } else if constexpr (NW == 8) {
-        its = wv == 0 ? 0x33 : wv == 1 ? 0x22 : wv < 6 ? 0xf0 | (wv - 2) : wv == 6 ? 0xf3 : 0xf1;
-        jts = wv < 2 ? 0x10 : wv < 6 ? 0xf0 | (wv - 2) : wv == 6 ? 0xf2 : 0xf0;
       } else {
         its = wv == 0 ? 0x033 : wv == 1 ? 0x122 : wv == 2 ? 0xf33 : 0xf21;
         jts = wv == 0 ? 0x010 : wv == 1 ? 0x110 : wv == 2 ? 0xf32 : 0xf20;
+      }
+      // m of one block and head, rounded, to LDS
+      auto put_m = [&](int h, int i, int j, const f32x4& m) {
+        T* dst = Ms + (h * kTok + i) * LDM + j;
+        if constexpr (BF) {
+          typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+          *reinterpret_cast<u32x2*>(dst) = u32x2{pack2(m[0], m[1]), pack2(m[2], m[3])};
+        } else {
+          *reinterpret_cast<f32x4*>(dst) = m;
+        }
+      };
+      bool wide = !BF;
+      if constexpr (BF) {
+#pragma unroll
+        for (int h = 0; h < HB; ++h) wide |= __builtin_amdgcn_readfirstlane(s_in[h].wide) != 0;
       }
 #pragma unroll
       for (int k = 0; k < kBlocks; ++k) {
@@ -419,37 +444,49 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
         const int i = 16 * it + lr, j = 16 * jt + 4 * lq;
         f32x4 sc = {0.f, 0.f, 0.f, 0.f};
         if constexpr (BF) {
+          bf16x8 bfr[KS], cfr[KS];
+          f32x4 col[HB];
+          float row[HB];
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
-            sc = mfma(*reinterpret_cast<const bf16x8*>(Bs + (16 * jt + lr) * LDB + 32 * ks + 8 * lq),
-                      *reinterpret_cast<const bf16x8*>(Cs + i * LDC + 32 * ks + 8 * lq), sc);
+          for (int ks = 0; ks < KS; ++ks) {
+            bfr[ks] = *reinterpret_cast<const bf16x8*>(Bs + (16 * jt + lr) * LDB + 32 * ks + 8 * lq);
+            cfr[ks] = *reinterpret_cast<const bf16x8*>(Cs + i * LDC + 32 * ks + 8 * lq);
+          }
+#pragma unroll
+          for (int h = 0; h < HB; ++h) {
+            col[h] = *reinterpret_cast<const f32x4*>(&s_in[h].col[8 * it * (it + 1) + j]);
+            row[h] = s_in[h].row[i];
+          }
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) sc = mfma(bfr[ks], cfr[ks], sc);
+          if (!wide || jt < it) {
+#pragma unroll
+            for (int h = 0; h < HB; ++h) {
+              f32x4 m = sc * col[h] * row[h];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) m[r] = j + r <= i ? m[r] : 0.f;
+              put_m(h, i, j, m);
+            }
+            continue;
+          }
         } else {
 #pragma unroll 4
           for (int n = lq; n < NP; n += 4) sc = mfma(Bs[(16 * jt + lr) * LDB + n], Cs[i * LDC + n], sc);
         }
+        // every pair's decay as one exponential
 #pragma unroll
         for (int h = 0; h < HB; ++h) {
           f32x4 m;
-          if (BF && jt < it) {
-            m = sc * *reinterpret_cast<const f32x4*>(&s_in[h].col[8 * it * (it - 1) + j]) * s_in[h].row[i];
-          } else {
-            const f32x4 hj = *reinterpret_cast<const f32x4*>(s_in[h].hi + j), lj = *reinterpret_cast<const f32x4*>(s_in[h].lo + j);
-            const f32x4 dj = *reinterpret_cast<const f32x4*>(s_in[h].dt + j);
-            const float hi = s_in[h].hi[i], lo = s_in[h].lo[i];
+          const f32x4 hj = *reinterpret_cast<const f32x4*>(s_in[h].hi + j), lj = *reinterpret_cast<const f32x4*>(s_in[h].lo + j);
+          const f32x4 dj = *reinterpret_cast<const f32x4*>(s_in[h].dt + j);
+          const float hi = s_in[h].hi[i], lo = s_in[h].lo[i];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              // j > i gives a positive exponent, possibly inf: not taken
-              const float v = sc[r] * dj[r] * fast_exp2((hi - hj[r]) + (lo - lj[r]));
-              m[r] = j + r <= i ? v : 0.f;
-            }
+          for (int r = 0; r < 4; ++r) {
+            // j > i gives a positive exponent, possibly inf: not taken
+            const float v = sc[r] * dj[r] * fast_exp2((hi - hj[r]) + (lo - lj[r]));
+            m[r] = j + r <= i ? v : 0.f;
           }
-          T* dst = Ms + (h * kTok + i) * LDM + j;
-          if constexpr (BF) {
-            typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-            *reinterpret_cast<u32x2*>(dst) = u32x2{pack2(m[0], m[1]), pack2(m[2], m[3])};
-          } else {
-            *reinterpret_cast<f32x4*>(dst) = m;
-          }
+          put_m(h, i, j, m);
         }
       }
       lds_barrier();
@@ -540,7 +577,11 @@ __global__ __launch_bounds__((64 * kWaves<PP, HB, PT>), (kWaves<PP, HB, PT> == 8
           }
         }
         // the next tile's loads go out here: their registers are free only now
-        if constexpr (OUT) load(nxt);
+        if constexpr (OUT) {
+          __builtin_amdgcn_sched_barrier(0);
+          load(nxt);
+          __builtin_amdgcn_sched_barrier(0);  // not behind the products of the state
+        }
         // the state's update
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt)
@@ -643,10 +684,10 @@ constexpr int kAhead = 8;  // boundaries whose loads are issued before any is us
 
 // Composes the segments' states in order, in place: seg_state[k] becomes the state that enters
 // segment k + 1. One thread an element of [HV, K, V].
-__global__ __launch_bounds__(kCompose) void compose_kernel(float* __restrict__ seg_state,
+__global__ __launch_bounds__(kThreads) void compose_kernel(float* __restrict__ seg_state,
                                                            const float* __restrict__ seg_g, int nb, int HV,
                                                            int64_t sz) {
-  const int64_t n = (int64_t)HV * sz, i = (int64_t)blockIdx.x * kCompose + threadIdx.x;
+  const int64_t n = (int64_t)HV * sz, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= n) return;
   const int hv = (int)(i / sz);
   float s = 0.f;
@@ -674,17 +715,18 @@ __global__ __launch_bounds__(kCompose) void compose_kernel(float* __restrict__ s
 template <typename T, int NT, int PP, int HB, int PT, bool VEC>
 hipError_t run(const SsmArgs& a, hipStream_t stream) {
   const int hblocks = a.HV / HB * ((a.V + PP - 1) / PP);
+  if ((int64_t)hblocks * a.nseg + a.N > INT32_MAX) return hipErrorNotSupported;
   if (a.crossed) {
     hipLaunchKernelGGL((prefill_kernel<T, NT, PP, HB, PT, false, VEC>), dim3(hblocks * (a.nseg - 1)),
-                       dim3(64 * kWaves<PP, HB, PT>), 0, stream, a, hblocks);
+                       dim3(kThreads), 0, stream, a, hblocks);
     const int64_t n = (int64_t)a.HV * a.K * a.V;
-    hipLaunchKernelGGL(compose_kernel, dim3((unsigned)((n + kCompose - 1) / kCompose)), dim3(kCompose), 0, stream,
+    hipLaunchKernelGGL(compose_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream,
                        a.seg_state, a.seg_g, a.nseg - 1, a.HV, (int64_t)a.K * a.V);
   }
   const int empties = (a.seqs.cu || a.T == 0) && a.sT ? a.N : 0;
   if (hblocks * a.nseg + empties == 0) return hipSuccess;
   hipLaunchKernelGGL((prefill_kernel<T, NT, PP, HB, PT, true, VEC>), dim3(hblocks * a.nseg + empties),
-                     dim3(64 * kWaves<PP, HB, PT>), 0, stream, a, hblocks);
+                     dim3(kThreads), 0, stream, a, hblocks);
   return hipGetLastError();
 }
 

@@ -84,7 +84,8 @@ def _check(d, cu, lengths, y, final, dtype, heads=None):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("HV,H,K,V", [(2, 1, 128, 64), (4, 2, 64, 64), (1, 1, 128, 128), (3, 3, 128, 64),
-                                      (4, 1, 32, 32), (3, 1, 40, 27), (2, 2, 33, 100), (1, 1, 1, 1), (2, 1, 16, 8)])
+                                      (4, 1, 32, 32), (3, 1, 40, 27), (2, 2, 33, 100), (1, 1, 1, 1), (2, 1, 16, 8), (2, 1, 24, 40),
+                                      (1, 1, 56, 72), (2, 2, 8, 120)])
 def test_shapes(dtype, HV, H, K, V):
     lengths = [1, 63, 64, 65, 0, 130]
     log(f"ssm {dtype} HV={HV} H={H} K={K} V={V}")
@@ -103,7 +104,7 @@ def test_lengths(dtype, lengths, tail):
 
 
 @pytest.mark.parametrize("kw", [dict(init=False), dict(skip=False, bias=False), dict(pad=8), dict(pad=3),
-                                dict(strides=False), dict(rate=200.0), dict(rate=1e-4)])
+                                dict(strides=False), dict(rate=200.0), dict(rate=1e-4), dict(rate=20.0)])
 def test_options(kw):
     lengths = [400, 77]
     for dtype in ("bf16", "f32"):

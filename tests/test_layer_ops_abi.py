@@ -68,6 +68,50 @@ def test_conv_workspace(lib):
     assert ws(32768, 6144, 4, 1) <= 128 * 5 * 6144 * 4
 
 
+SSM_BAD = [
+    (dict(x=None), INV), (dict(dt=None), INV), (dict(A_log=None), INV), (dict(b=None), INV), (dict(c=None), INV),
+    (dict(y=None), INV), (dict(HV=3), INV), (dict(H=0), INV), (dict(K=0), INV), (dict(V=0), INV), (dict(dtype=2), INV),
+    (dict(K=129, sb=258, sc=258), UNS), (dict(V=136, sx=4 * 136), UNS), (dict(sx=255), INV), (dict(sdt=3), INV),
+    (dict(sb=100), INV), (dict(sc=-5), INV),
+]
+
+
+@pytest.mark.parametrize("bad,rc", SSM_BAD + [
+    (dict(N=0), INV), (dict(T=-1), INV), (dict(T=65), INV), (dict(flags=1), INV), (dict(sx=(1 << 24) + 1), UNS),
+    (dict(T=8192, N=1, ws=None), INV), (dict(T=8192, N=1, ws_bytes=8), INV), (dict(ws=ctypes.c_void_p(0x1010)), INV),
+    (dict(N=1 << 21, T=1 << 21), UNS)])
+def test_ssm_chunk_fwd_refuses(lib, bad, rc):
+    a = dict(x=FAKE, sx=256, dt=FAKE, sdt=4, A_log=FAKE, b=FAKE, sb=128, c=FAKE, sc=128, N=2, y=FAKE, T=64, H=2, HV=4,
+             K=64, V=64, flags=0, dtype=1, ws=FAKE, ws_bytes=1 << 40)
+    a.update(bad)
+    assert lib.kda_ssm_chunk_fwd(a["x"], a["sx"], a["dt"], a["sdt"], a["A_log"], a["b"], a["sb"], a["c"], a["sc"], None,
+                                 None, None, None, a["N"], None, a["y"], a["T"], a["H"], a["HV"], a["K"], a["V"],
+                                 a["flags"], a["dtype"], a["ws"], a["ws_bytes"], None) == rc
+
+
+@pytest.mark.parametrize("bad,rc", SSM_BAD + [
+    (dict(pool=None), INV), (dict(B=0), INV), (dict(nslots=0), INV), (dict(slots=None, nslots=3), INV),
+    (dict(B=1 << 28), UNS)])
+def test_ssm_step_refuses(lib, bad, rc):
+    a = dict(x=FAKE, sx=256, dt=FAKE, sdt=4, A_log=FAKE, b=FAKE, sb=128, c=FAKE, sc=128, pool=FAKE, slots=FAKE, nslots=8,
+             y=FAKE, B=4, H=2, HV=4, K=64, V=64, dtype=1)
+    a.update(bad)
+    assert lib.kda_ssm_step(a["x"], a["sx"], a["dt"], a["sdt"], a["A_log"], a["b"], a["sb"], a["c"], a["sc"], None, None,
+                            a["pool"], a["slots"], a["nslots"], a["y"], a["B"], a["H"], a["HV"], a["K"], a["V"],
+                            a["dtype"], None) == rc
+
+
+def test_ssm_workspace(lib):
+    ws = lib.kda_ssm_chunk_fwd_workspace_size
+    assert ws(1, 256, 0, 1, 1, 64, 64, 1) == 0           # one segment
+    assert ws(4, 4 * 8192, 0, 64, 512, 64, 64, 1) == 0   # whole sequences fill the GPU
+    one = 16 * (128 * 128 + 1) * 4                       # a boundary's states and decays
+    n = ws(1, 8192, 0, 1, 16, 128, 128, 1)
+    assert n > 0 and n % 256 == 0 and n // one == 31     # 32 segments of 256 tokens
+    assert ws(1, 0, 1, 1, 16, 128, 128, 1) == 0 and ws(3, 8192, 0, 1, 16, 128, 128, 1) == 0
+    assert ws(1, 8192, 0, 1, 16, 200, 128, 1) == 0
+
+
 def _arrays(ptrs, sizes):
     return (ctypes.c_void_p * len(ptrs))(*ptrs), (ctypes.c_size_t * len(sizes))(*sizes)
 
@@ -103,6 +147,8 @@ def test_nothing_to_do_returns_ok(lib):
 def test_binding_refuses_host_tensors():
     x, w = torch.zeros(2, 8, 16), torch.zeros(16, 4)
     for call in (lambda: kda.kda_conv_fwd(x, w), lambda: kda.kda_conv_bwd(x, w, x),
+                 lambda: kda.kda_ssm_chunk_fwd(x[..., None], x, w[0], x[..., None], x[..., None]),
+                 lambda: kda.kda_ssm_step(x, x[..., 0], w[0], x, x, x[None]),
                  lambda: kda.kda_conv_step(x[:, 0], w, torch.zeros(2, 3, 16)),
                  lambda: kda.kda_slots_copy(x, torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)),
                  lambda: kda.kda_slots_compact([x], torch.ones(2, dtype=torch.bool)),
