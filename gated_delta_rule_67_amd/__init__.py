@@ -20,6 +20,13 @@ Entry points (same names as the C ABI):
   with that gate applied inside the kernels (the gate's input in place of g)
 * ``kda_chunk_fwd_segmented(q, k, v, g, beta, segments, ...)``: the prefill over segments
   of each sequence composed by a scan (for few heads)
+* ``kda_conv_fwd`` / ``kda_conv_bwd`` / ``kda_conv_step``: the short causal convolution in front
+  of the recurrence (dense batches and packed sequences), its backward, and one token on a pool
+  of states
+* ``kda_ssm_chunk_fwd`` / ``kda_ssm_step``: the selective state space scan with one decay per
+  head, for prompts and for one token on a pool of states
+* ``kda_slots_copy`` / ``kda_slots_compact``: copies, forks, clears and compaction of the slots of
+  many state pools at once
 * ``kda_chunk_fwd_noalloc(q, k, v, g, beta, o, final_state=None, ...)``: the prefill into
   caller-provided outputs, with the workspace taken from the library's fixed per-device
   scratch array (no device allocation anywhere in the call)
@@ -683,14 +690,16 @@ def _sequences(x, cu_seqlens, dims, index):
     if cu_seqlens is None:
         _require(x.dim() == dims, "x must be a batch [B, T, ...] (packed sequences: give cu_seqlens)")
         N, T = x.shape[0], x.shape[0] * x.shape[1]
-        _require(N >= 1, "x must have at least one sequence")
+        _require(N >= 1 and T < 1 << 31, "x must have at least one sequence and fewer than 2^31 tokens")
         return 2, N, T
     _require(cu_seqlens.get_device() == index and cu_seqlens.dtype is torch.int32
              and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous() and cu_seqlens.numel() >= 2,
              "cu_seqlens must be a contiguous int32 vector of at least two offsets on the GPU of x")
     lead = x.dim() - dims + 2
     _require(lead == 1 or (lead == 2 and x.shape[0] == 1), "packed x must be [T, ...] or [1, T, ...]")
-    return lead, cu_seqlens.numel() - 1, x.shape[lead - 1]
+    T = x.shape[lead - 1]
+    _require(T < 1 << 31, "x must have fewer than 2^31 tokens")
+    return lead, cu_seqlens.numel() - 1, T
 
 
 def _gpu(x):

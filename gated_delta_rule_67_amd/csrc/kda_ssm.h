@@ -30,6 +30,7 @@ struct SsmArgs {
   // the prefill's segments of the token axis: seg tokens each, nseg of them; the state entering
   // segment k in seg_state[k - 1], the log2 of its decay since the segment before in seg_g
   int seg, nseg;
+  int per;           // segments of each sequence where they divide it evenly, else 0
   bool crossed;      // whether a sequence may go on over a segment's end
   float* seg_state;  // [nseg - 1][HV][K][V]
   float* seg_g;      // [nseg - 1][HV]

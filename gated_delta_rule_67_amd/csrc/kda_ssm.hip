@@ -168,7 +168,9 @@ __device__ __forceinline__ void make_decay(Decay& d, Inner& m, float raw, bool i
   const int lane = __lane_id();
   float e, r;
   const float dt = in ? softplus_f32(raw + bias, e, r) : 0.f;
-  double g = (double)(neg_rate * dt) * 1.4426950408889634;
+  // a decay below e^-1e6 is 0 in any case; without the bound an infinite one would leave no differences
+  const float rate = in ? neg_rate * dt : 0.f;
+  double g = (double)(rate < -1e6f ? -1e6f : rate) * 1.4426950408889634;
   g += dpp_or_zero<0x111, 0xf>(g);  // inclusive sums within rows of 16 lanes: shifts by 1, 2, 4, 8
   g += dpp_or_zero<0x112, 0xf>(g);
   g += dpp_or_zero<0x114, 0xf>(g);
@@ -228,7 +230,9 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
   __shared__ __attribute__((aligned(16))) Inner s_in[OUT ? HB : 1];  // read in front of a tile's second barrier only
 
   const int K = a.K, V = a.V, vblocks = (V + PP - 1) / PP;
-  const int main_blocks = hblocks * (OUT ? a.nseg : a.nseg - 1);
+  // with outputs: every segment; without: those whose end a sequence may go on over
+  const int inner = a.per > 0 ? a.per - 1 : a.nseg - 1;
+  const int main_blocks = hblocks * (OUT ? a.nseg : a.per > 0 ? a.N * inner : inner);
   int bid = blockIdx.x;
   if (OUT && bid >= main_blocks) {  // empty sequences: the state passes through
     const int n = bid - main_blocks;
@@ -241,7 +245,9 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
   // neighbouring head blocks (which share b and c) on one XCD: workgroups are dealt out
   // round-robin over the 8 of them
   if (main_blocks % 8 == 0) bid = (bid & 7) * (main_blocks / 8) + (bid >> 3);
-  const int segk = bid / hblocks, hb = bid - segk * hblocks;
+  int segk = bid / hblocks;
+  const int hb = bid - segk * hblocks;
+  if (!OUT && a.per > 0) segk = segk / inner * a.per + segk % inner;
   const int h0 = hb / vblocks * HB, v0 = hb % vblocks * PP;  // first head, first column in it
   const int width = min(PP, V - v0);                          // real columns of each head
   const int grp = h0 / (a.HV / a.H);
@@ -685,8 +691,8 @@ constexpr int kAhead = 8;  // boundaries whose loads are issued before any is us
 // Composes the segments' states in order, in place: seg_state[k] becomes the state that enters
 // segment k + 1. One thread an element of [HV, K, V].
 __global__ __launch_bounds__(kThreads) void compose_kernel(float* __restrict__ seg_state,
-                                                           const float* __restrict__ seg_g, int nb, int HV,
-                                                           int64_t sz) {
+                                                           const float* __restrict__ seg_g, int nb, int per,
+                                                           int HV, int64_t sz) {
   const int64_t n = (int64_t)HV * sz, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= n) return;
   const int hv = (int)(i / sz);
@@ -702,8 +708,9 @@ __global__ __launch_bounds__(kThreads) void compose_kernel(float* __restrict__ s
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (k0 + u >= nb) break;
-      // where nothing is carried the product is left out: s may be infinite
-      const bool none = g[u] == kNoCarry;
+      // nothing was made of a sequence's last segment; where nothing is carried the product is left
+      // out: s may be infinite
+      const bool none = g[u] == kNoCarry || (per > 0 && (k0 + u + 1) % per == 0);
       s = none ? 0.f : g[u] > -INFINITY ? v[u] + fast_exp2(g[u]) * s : v[u];
       if (!none) seg_state[(int64_t)(k0 + u) * n + i] = s;
     }
@@ -717,11 +724,11 @@ hipError_t run(const SsmArgs& a, hipStream_t stream) {
   const int hblocks = a.HV / HB * ((a.V + PP - 1) / PP);
   if ((int64_t)hblocks * a.nseg + a.N > INT32_MAX) return hipErrorNotSupported;
   if (a.crossed) {
-    hipLaunchKernelGGL((prefill_kernel<T, NT, PP, HB, PT, false, VEC>), dim3(hblocks * (a.nseg - 1)),
+    hipLaunchKernelGGL((prefill_kernel<T, NT, PP, HB, PT, false, VEC>), dim3(hblocks * (a.per > 0 ? a.N * (a.per - 1) : a.nseg - 1)),
                        dim3(kThreads), 0, stream, a, hblocks);
     const int64_t n = (int64_t)a.HV * a.K * a.V;
     hipLaunchKernelGGL(compose_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream,
-                       a.seg_state, a.seg_g, a.nseg - 1, a.HV, (int64_t)a.K * a.V);
+                       a.seg_state, a.seg_g, a.nseg - 1, a.per, a.HV, (int64_t)a.K * a.V);
   }
   const int empties = (a.seqs.cu || a.T == 0) && a.sT ? a.N : 0;
   if (hblocks * a.nseg + empties == 0) return hipSuccess;
@@ -788,6 +795,7 @@ hipError_t launch_ssm_prefill(SsmArgs a, void* workspace, hipStream_t stream) {
   a.seg = g.len;
   a.nseg = g.n;
   a.crossed = g.crossed;
+  a.per = g.crossed && !a.seqs.cu && a.seqs.len % g.len == 0 ? a.seqs.len / g.len : 0;
   if (g.crossed) {
     a.seg_state = static_cast<float*>(workspace);
     a.seg_g = a.seg_state + (size_t)(g.n - 1) * a.HV * a.K * a.V;

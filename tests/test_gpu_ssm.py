@@ -123,6 +123,60 @@ def test_a_reset_then_slow_decay():
     _check(d, cu, [300], *_fwd(d, cu), "f32")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decays_past_every_float(dtype):
+    """exp(A_log) overflows float32: the state holds the last token alone, and nothing is NaN."""
+    d, cu = _make([70, 300], 2, 1, 64, 64, DT[dtype], seed=12)
+    d["A_log"] = torch.tensor([100.0, 60.0]).cuda()
+    _check(d, cu, [70, 300], *_fwd(d, cu), dtype)
+    pool = d["state"].clone()
+    y = kda.kda_ssm_step(d["x"][:2], d["dt"][:2], d["A_log"], d["b"][:2], d["c"][:2], pool, d["D"], d["dt_bias"])
+    assert bool(y.isfinite().all()) and bool(pool.isfinite().all())
+
+
+def test_rows_in_front_of_and_behind_the_sequences():
+    """Whole segments of rows in no sequence, on both sides."""
+    d, _ = _make([900], 2, 1, 64, 64, torch.bfloat16, seed=13, init=False)
+    cu = torch.tensor([300, 300, 610], dtype=torch.int32).cuda()
+    y, f = kda.kda_ssm_chunk_fwd(d["x"], d["dt"], d["A_log"], d["b"], d["c"], d["D"], d["dt_bias"], None, cu)
+    one = {k: (v[300:610] if k in TOKEN else v) for k, v in d.items()}
+    ry, rf = _fwd(one, torch.tensor([0, 310], dtype=torch.int32).cuda())
+    assert not y[:300].any() and not y[610:].any() and not f[0].any()
+    assert float((y[300:610].float() - ry.float()).abs().max()) <= 2.0 ** -6 * float(ry.float().abs().max())
+    assert float((f[1] - rf[0]).abs().max()) <= 2.0 ** -15 * float(rf.abs().max())
+
+
+def test_binding_refuses():
+    d, cu = _make([64], 2, 1, 64, 64, torch.bfloat16, seed=14)
+    ok = dict(x=d["x"], dt=d["dt"], A_log=d["A_log"], b=d["b"], c=d["c"], D=d["D"], dt_bias=d["dt_bias"],
+              initial_state=d["state"], cu_seqlens=cu)
+    kda.kda_ssm_chunk_fwd(**ok)
+    for bad in (dict(x=d["x"].float()), dict(x=d["x"].transpose(0, 1)), dict(x=d["x"][:1].expand(64, 2, 64)),
+                dict(dt=d["dt"][:-1]), dict(b=d["b"][..., :32]), dict(c=d["c"].cpu()), dict(A_log=d["A_log"].double()),
+                dict(D=d["D"][:1]), dict(initial_state=d["state"].bfloat16()), dict(cu_seqlens=cu.long()),
+                dict(cu_seqlens=cu[:1]), dict(cu_seqlens=None), dict(x=d["x"].half(), dt=d["dt"].half())):
+        with pytest.raises(ValueError):
+            kda.kda_ssm_chunk_fwd(**dict(ok, **bad))
+    pool = d["state"].clone()
+    for bad in (pool.bfloat16(), pool[:, :1], pool.transpose(2, 3)):
+        with pytest.raises(ValueError):
+            kda.kda_ssm_step(d["x"][:1], d["dt"][:1], d["A_log"], d["b"][:1], d["c"][:1], bad)
+    with pytest.raises(ValueError):
+        kda.kda_ssm_step(d["x"][:2], d["dt"][:2], d["A_log"], d["b"][:2], d["c"][:2], pool)  # one state, two requests
+    w = torch.randn(8, 4).cuda()
+    x = torch.randn(2, 6, 8).cuda()
+    for call in (lambda: kda.kda_conv_fwd(x[:, 1:], w), lambda: kda.kda_conv_fwd(x, w.t()), lambda: kda.kda_conv_fwd(x, w.half()),
+                 lambda: kda.kda_conv_fwd(x[..., ::2], w[::2]), lambda: kda.kda_conv_bwd(x, w, x[:1]),
+                 lambda: kda.kda_conv_fwd(x, w, None, x[:, :2]), lambda: kda.kda_conv_step(x[:, 0], w, x[:, :2]),
+                 lambda: kda.kda_slots_copy([x, x], cu[:1], cu[:1]), lambda: kda.kda_slots_copy([x, x[:1]], cu[:1], cu[:1]),
+                 lambda: kda.kda_slots_copy(x.transpose(0, 1), cu[:1], cu[:1]), lambda: kda.kda_slots_copy(x, cu[:1], cu),
+                 lambda: kda.kda_slots_compact(x, cu)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(RuntimeError):
+        kda.kda_conv_fwd(x, torch.randn(8, 5).cuda())  # no kernel of this width
+
+
 @pytest.mark.parametrize("B,T", [(3, 64), (2, 321), (4, 1), (1, 2048), (2, 1024)])
 def test_dense_batches(B, T):
     for dtype in ("bf16", "f32"):
