@@ -22,13 +22,13 @@
 // float32 inputs take the same steps with tiles of 32 tokens, 16x16x4 float32 products and nothing
 // rounded.
 //
-// Measured at 4 x 8192 tokens, 64 heads x 64, K = 128, 8 pairs, bf16: 355 us (251 pass with
-// outputs, 90 without, 13 scan) for 684 MB, 115 us at a copy's rate. A tile of two heads takes a
-// workgroup about 14,000 cycles beside a second one on its CU: 2,000 for M, 3,500 for y, 3,800 for
-// the state (its 96 products of a wave are at 0.9 of the matrix cores' rate, two waves a SIMD), 2,000
-// until the next tile's loads are issued, 800 for LDS stores. No single pipeline is full (VALU 45%,
-// matrix cores 30%, LDS 34% of the cycles); tiles of 32 tokens, eight waves of 16 columns and one or
-// three workgroups a CU were slower or the same.
+// Measured at 4 x 8192 tokens, 64 heads x 64, K = 128, 8 pairs, bf16: 356 us for 684 MB, 114 us at
+// a copy's rate; 258 us without the boundary pass and the composition (traced: 251 pass with
+// outputs, 118 without, 15 composition). A tile of two heads takes a workgroup about 14,300 cycles
+// beside a second one on its CU: 2,050 for M, 3,500 for y, 4,100 for the state, 2,000 until the next
+// tile's loads are issued, 760 for LDS stores. No single pipeline is full (VALU 43%, matrix cores
+// 31%, LDS 35% of the cycles). Tiles of 32 tokens (385 us), 256 or 768 workgroups (466, 405) were
+// slower, eight waves of 16 columns the same.
 #include "kda_ssm.h"
 
 namespace kda {
@@ -85,7 +85,7 @@ template <typename T, int ROWS, int COLS, int PAD, bool VEC>
 struct Stage {
   static constexpr int kElem = 16 / sizeof(T), kRow = COLS / kElem;
   static constexpr int kPieces = (ROWS * kRow + kThreads - 1) / kThreads;
-  static constexpr bool kEven = kPieces * kThreads == ROWS * kRow;  // every thread holds as many
+  static_assert(kPieces * kThreads == ROWS * kRow, "every thread holds as many");
   u32x4 v[kPieces];
 
   // base: column 0 of token 0; ld: elements between tokens (<= 2^24); tokens behind t0 + rows and
@@ -101,7 +101,7 @@ struct Stage {
       const int piece = threadIdx.x + kThreads * e, row = piece / kRow, c = piece % kRow * kElem;
       const int blk = c / PAD, p = c - blk * PAD;
       const unsigned off = (unsigned)row * rowb + (unsigned)(blk * width + p) * sizeof(T);
-      auto in = [&](int k) { return p + k < width && (kEven || row < ROWS) ? off + k * (unsigned)sizeof(T) : kOutOfRange; };
+      auto in = [&](int k) { return p + k < width ? off + k * (unsigned)sizeof(T) : kOutOfRange; };
       if constexpr (VEC) {
         v[e] = __builtin_amdgcn_raw_buffer_load_b128(r, in(0), 0, 0);
       } else {
@@ -122,7 +122,7 @@ struct Stage {
 #pragma unroll
     for (int e = 0; e < kPieces; ++e) {
       const int piece = threadIdx.x + kThreads * e, row = piece / kRow, c = piece % kRow * kElem;
-      if (kEven || row < ROWS) *reinterpret_cast<u32x4*>(dst + row * ldd + c) = v[e];
+      *reinterpret_cast<u32x4*>(dst + row * ldd + c) = v[e];
     }
   }
 };
