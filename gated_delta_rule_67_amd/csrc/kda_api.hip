@@ -529,11 +529,14 @@ static bool valid_sequences(int N, int T, const int* cu_seqlens) {
   return N >= 1 && T >= 0 && (cu_seqlens || T % N == 0);
 }
 
+// Sums of a token's index and a tile's or a segment's length stay in 32 bits.
+constexpr int kMaxTokens = 1 << 30;
+
 static int check_conv(int N, int T, int D, int W, const int* cu_seqlens, unsigned flags, int dtype) {
   if (flags & ~(unsigned)(KDA_CONV_SILU | KDA_ZERO_REST)) return KDA_ERR_INVALID;
   if (!valid_sequences(N, T, cu_seqlens) || !positive(D)) return KDA_ERR_INVALID;
   if (dtype != KDA_DTYPE_F32 && dtype != KDA_DTYPE_BF16) return KDA_ERR_INVALID;
-  if (W < 2 || W > 4 || D > (1 << 20) || N > (1 << 17)) return KDA_ERR_UNSUPPORTED;
+  if (W < 2 || W > 4 || D > (1 << 20) || N > (1 << 17) || T > kMaxTokens) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }
 
@@ -602,7 +605,7 @@ static int check_stride(int64_t stride, int64_t width) {
 }
 
 size_t kda_ssm_chunk_fwd_workspace_size(int N, int T, int packed, int H, int HV, int K, int V, int dtype) {
-  if (N < 1 || T < 0 || (!packed && T % N != 0) || check_ssm(H, HV, K, V, dtype) != KDA_OK) return 0;
+  if (N < 1 || T < 0 || T > kMaxTokens || (!packed && T % N != 0) || check_ssm(H, HV, K, V, dtype) != KDA_OK) return 0;
   return kda::ssm_prefill_workspace_bytes(T, N, packed != 0, H, HV, K, V, dtype == KDA_DTYPE_BF16);
 }
 
@@ -623,7 +626,7 @@ int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* dt, int64_t d
     if (T < 2) *strides[i] = widths[i];  // one token: its stride has no meaning
     if ((rc = check_stride(*strides[i], widths[i])) != KDA_OK) return rc;
   }
-  if (N > (1 << 20)) return KDA_ERR_UNSUPPORTED;
+  if (N > (1 << 20) || T > kMaxTokens) return KDA_ERR_UNSUPPORTED;
   const size_t need = kda_ssm_chunk_fwd_workspace_size(N, T, cu_seqlens != nullptr, H, HV, K, V, dtype);
   if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_INVALID;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return KDA_ERR_INVALID;

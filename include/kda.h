@@ -446,8 +446,8 @@ int kda_chunk_fwd_noalloc(const void* q, const void* k, const void* v, const voi
  *   final_state    [N, W-1, D]  dtype   out, or NULL
  *   y              [T, D]       dtype   out
  *
- * Constraints: N >= 1, T >= 0, D >= 1 (else KDA_ERR_INVALID); 2 <= W <= 4, D <= 2^20, N <= 2^17
- * (else KDA_ERR_UNSUPPORTED). No alignment is required; 16-byte aligned rows are fastest. Outputs
+ * Constraints: N >= 1, T >= 0, D >= 1 (else KDA_ERR_INVALID); 2 <= W <= 4, D <= 2^20, N <= 2^17,
+ * T <= 2^30 (else KDA_ERR_UNSUPPORTED). No alignment is required; 16-byte aligned rows are fastest. Outputs
  * must not overlap inputs (final_state not initial_state either). Nothing is allocated.
  */
 typedef enum {
@@ -517,7 +517,7 @@ int kda_conv_step(const void* x, int64_t x_stride, const float* weight, const fl
  * The token axis is cut into equal segments that run side by side; a scan of the states at their
  * boundaries joins them (as in kda_chunk_fwd_segmented). Results are bitwise reproducible.
  * Constraints: N >= 1, T >= 0, HV % H == 0 (else KDA_ERR_INVALID); K, V <= 128, HV <= 2^16,
- * N <= 2^20 (else KDA_ERR_UNSUPPORTED). Nothing is allocated.
+ * N <= 2^20, T <= 2^30 (else KDA_ERR_UNSUPPORTED). Nothing is allocated.
  */
 size_t kda_ssm_chunk_fwd_workspace_size(int N, int T, int packed, int H, int HV, int K, int V,
                                         int dtype);

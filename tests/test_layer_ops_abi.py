@@ -155,3 +155,15 @@ def test_binding_refuses_host_tensors():
                  lambda: kda.kda_slots_copy([], torch.zeros(1), torch.zeros(1))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_token_limit(lib):
+    """Sums of a token's index and a tile's or a segment's length stay in 32 bits: T <= 2^30."""
+    T = (1 << 30) + 1
+    assert lib.kda_conv_fwd(FAKE, 1, FAKE, None, None, None, 1, None, FAKE, T, 1, 4, 1, 1, None) == UNS
+    assert lib.kda_conv_bwd(FAKE, 1, FAKE, None, None, None, 1, FAKE, 1, None, FAKE, None, None, None, T, 1, 4, 1, 1,
+                            FAKE, 1 << 40, None) == UNS
+    assert lib.kda_ssm_chunk_fwd(FAKE, 1, FAKE, 1, FAKE, FAKE, 1, FAKE, 1, None, None, None, None, 1, None, FAKE, T,
+                                 1, 1, 1, 1, 0, 1, FAKE, 1 << 40, None) == UNS
+    assert lib.kda_conv_bwd_workspace_size(T, 1, 4, 1) == 0
+    assert lib.kda_ssm_chunk_fwd_workspace_size(1, T, 0, 1, 1, 1, 1, 1) == 0
