@@ -653,7 +653,7 @@ int kda_ssm_step(const void* x, int64_t x_stride, const void* dt, int64_t dt_str
   const int64_t widths[] = {(int64_t)HV * V, HV, (int64_t)H * K, (int64_t)H * K};
   for (int i = 0; i < 4; ++i)
     if (B > 1 && strides[i] < widths[i]) return KDA_ERR_INVALID;
-  if ((int64_t)B * HV * 4 > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  if ((int64_t)B * HV >= (1 << 23)) return KDA_ERR_UNSUPPORTED;  // 512 threads a head, under 2^32 a launch
   kda::SsmArgs a{};
   a.x = x, a.ldx = x_stride, a.dt = dt, a.lddt = dt_stride, a.A_log = A_log;
   a.b = b, a.ldb = b_stride, a.c = c, a.ldc = c_stride, a.D = D, a.dt_bias = dt_bias;

@@ -722,7 +722,7 @@ __global__ __launch_bounds__(kThreads) void compose_kernel(float* __restrict__ s
 template <typename T, int NT, int PP, int HB, int PT, bool VEC>
 hipError_t run(const SsmArgs& a, hipStream_t stream) {
   const int hblocks = a.HV / HB * ((a.V + PP - 1) / PP);
-  if ((int64_t)hblocks * a.nseg + a.N > INT32_MAX) return hipErrorNotSupported;
+  if (((int64_t)hblocks * a.nseg + a.N) * kThreads > UINT32_MAX) return hipErrorNotSupported;
   if (a.crossed) {
     hipLaunchKernelGGL((prefill_kernel<T, NT, PP, HB, PT, false, VEC>), dim3(hblocks * (a.per > 0 ? a.N * (a.per - 1) : a.nseg - 1)),
                        dim3(kThreads), 0, stream, a, hblocks);

@@ -517,7 +517,8 @@ int kda_conv_step(const void* x, int64_t x_stride, const float* weight, const fl
  * The token axis is cut into equal segments that run side by side; a scan of the states at their
  * boundaries joins them (as in kda_chunk_fwd_segmented). Results are bitwise reproducible.
  * Constraints: N >= 1, T >= 0, HV % H == 0 (else KDA_ERR_INVALID); K, V <= 128, HV <= 2^16,
- * N <= 2^20, T <= 2^30 (else KDA_ERR_UNSUPPORTED). Nothing is allocated.
+ * N <= 2^20, T <= 2^30, and under 2^24 workgroups (about one per 64 columns of a sequence's or
+ * segment's heads) (else KDA_ERR_UNSUPPORTED). Nothing is allocated.
  */
 size_t kda_ssm_chunk_fwd_workspace_size(int N, int T, int packed, int H, int HV, int K, int V,
                                         int dtype);
@@ -534,8 +535,8 @@ int kda_ssm_chunk_fwd(const void* x, int64_t x_stride, const void* dt, int64_t d
  * One token of kda_ssm_chunk_fwd per request, on slot slots[n] of state_pool [num_slots, HV, K, V]
  * (float32, updated in place): x [B, HV, V], dt [B, HV], b, c [B, H, K], y [B, HV, V] out. slots
  * NULL: request n uses slot n (num_slots >= B). A request whose slot is outside [0, num_slots)
- * gets y = 0 and changes no state; valid slots of one call must be distinct. Otherwise as
- * kda_ssm_chunk_fwd, without the limit on strides.
+ * gets y = 0 and changes no state; valid slots of one call must be distinct. B HV < 2^23 (else
+ * KDA_ERR_UNSUPPORTED), otherwise as kda_ssm_chunk_fwd, without the limit on strides.
  */
 int kda_ssm_step(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride,
                  const float* A_log, const void* b, int64_t b_stride, const void* c,

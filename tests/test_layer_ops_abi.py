@@ -167,3 +167,16 @@ def test_token_limit(lib):
                                  1, 1, 1, 1, 0, 1, FAKE, 1 << 40, None) == UNS
     assert lib.kda_conv_bwd_workspace_size(T, 1, 4, 1) == 0
     assert lib.kda_ssm_chunk_fwd_workspace_size(1, T, 0, 1, 1, 1, 1, 1) == 0
+
+
+def test_launch_limit(lib):
+    """A launch holds fewer than 2^32 threads: what needs more is refused before it."""
+    def step(B, HV):
+        return lib.kda_ssm_step(FAKE, HV, FAKE, HV, FAKE, FAKE, 1, FAKE, 1, None, None, FAKE, FAKE, 1, FAKE, B, 1, HV,
+                                1, 1, 1, None)
+    assert step(1 << 17, 1 << 6) == UNS      # 2^23 heads of 512 threads
+    assert step(1 << 30, 1 << 3) == UNS
+    N, HV = 1 << 19, 64                      # one token each, 32 workgroups of 256 threads a sequence
+    assert lib.kda_ssm_chunk_fwd_workspace_size(N, N, 0, 1, HV, 1, 64, 1) == 0
+    assert lib.kda_ssm_chunk_fwd(FAKE, HV * 64, FAKE, HV, FAKE, FAKE, 1, FAKE, 1, None, None, None, None, N, None, FAKE,
+                                 N, 1, HV, 1, 64, 0, 1, None, 0, None) == UNS
