@@ -5,6 +5,13 @@
 
 namespace kda {
 
+// -exp(A_log), finite: an infinite rate times a step size that underflows to 0 would be NaN. (A
+// NaN stays one.)
+__device__ __forceinline__ float negative_rate(float A_log) {
+  const float rate = -expf(A_log);
+  return rate < -3.402823466e38f ? -3.402823466e38f : rate;
+}
+
 struct SsmArgs {
   const void* x;   // [T, HV, V], ldx elements between tokens
   int64_t ldx;

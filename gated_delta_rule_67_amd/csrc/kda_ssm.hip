@@ -314,7 +314,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
   float bias = 0.f, neg_rate = 0.f;
   if (dw >= 0) {
     bias = a.dt_bias ? a.dt_bias[h0 + dw] : 0.f;
-    neg_rate = -expf(a.A_log[h0 + dw]);
+    neg_rate = negative_rate(a.A_log[h0 + dw]);
   }
   const float skip = a.D ? a.D[hv] : 0.f;
 

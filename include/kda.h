@@ -499,7 +499,7 @@ int kda_conv_step(const void* x, int64_t x_stride, const float* weight, const fl
  *   x              [T, HV, V]   dtype   the tokens of all sequences, x_stride elements apart
  *   dt             [T, HV]      dtype   step sizes before the softplus
  *   b, c           [T, H, K]    dtype   value head hv reads pair hv / (HV / H)
- *   A_log          [HV]         float32
+ *   A_log          [HV]         float32 (an exp(A_log) above the largest float counts as that)
  *   D, dt_bias     [HV]         float32, or NULL: zeros
  *   initial_state  [N, HV, K, V] float32, or NULL: zeros
  *   cu_seqlens     [N+1] int32 DEVICE memory (non-decreasing, within [0, T], empty sequences

@@ -308,3 +308,48 @@ def test_repeats_bit_for_bit_on_a_side_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
         assert all(torch.equal(a, b) for a, b in zip([t.clone() for t in both()], ref))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rate_past_floats(dtype):
+    """exp(A_log) above every float, D_t below: their product is 0 (float64: e^90 e^-200), the decay
+    1, and the tokens add nothing: the states come back and y = S^T c + D x."""
+    HV, H, K, V, L = 2, 1, 32, 32, 70
+    d, cu = _make([L], HV, H, K, V, DT[dtype], seed=11, bias=False)
+    d["A_log"] = torch.full_like(d["A_log"], 90.0)
+    d["dt"] = torch.full_like(d["dt"], -200.0)
+    y, final = _fwd(d, cu)
+    _check(d, cu, [L], y, final, dtype)
+    assert torch.equal(final, d["state"])
+    pool = d["state"].clone()
+    out = kda.kda_ssm_step(d["x"][:1].contiguous(), d["dt"][:1], d["A_log"], d["b"][:1].contiguous(),
+                           d["c"][:1].contiguous(), pool, d["D"], None)
+    assert torch.equal(pool, d["state"]) and bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masked_tokens(dtype):
+    """dt = -inf masks a token: its decay is 1 and it adds nothing, so the states and the other rows
+    are those of the sequence with D_t = 0 there, over tiles and segments that are masked whole."""
+    HV, H, K, V, L = 2, 1, 64, 64, 700
+    d, cu = _make([L], HV, H, K, V, DT[dtype], seed=12)
+    mask = torch.rand(L, generator=torch.Generator().manual_seed(13)) < 0.3
+    mask[100:420] = True
+    d["dt"][mask.cuda()] = float("-inf")
+    _check(d, cu, [L], *_fwd(d, cu), dtype)
+    d["dt"][:] = float("-inf")
+    y, final = _fwd(d, cu)
+    _check(d, cu, [L], y, final, dtype)
+    assert torch.equal(final, d["state"])
+
+
+def test_nan_rate_is_not_hidden():
+    d, cu = _make([70], 2, 1, 32, 32, torch.bfloat16, seed=14)
+    d["A_log"][1] = float("nan")
+    y, final = _fwd(d, cu)
+    assert bool(torch.isnan(final[0, 1]).all()) and bool(torch.isfinite(final[0, 0]).all())
+    assert bool(torch.isfinite(y[:, 0]).all())
+    pool = d["state"].clone()
+    kda.kda_ssm_step(d["x"][:1].contiguous(), d["dt"][:1], d["A_log"], d["b"][:1].contiguous(),
+                     d["c"][:1].contiguous(), pool, d["D"], d["dt_bias"])
+    assert bool(torch.isnan(pool[0, 1]).all()) and bool(torch.isfinite(pool[0, 0]).all())
