@@ -125,6 +125,22 @@ struct Stage {
       *reinterpret_cast<u32x4*>(dst + row * ldd + c) = v[e];
     }
   }
+  // Adds the squares of this thread's values: the sum is finite only if all of them are.
+  __device__ __forceinline__ void add_squares(float& sum) const {
+#pragma unroll
+    for (int e = 0; e < kPieces; ++e)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const unsigned u = v[e][k];
+        if constexpr (sizeof(T) == 4) {
+          sum = fmaf(__builtin_bit_cast(float, u), __builtin_bit_cast(float, u), sum);
+        } else {
+#if __HIP_DEVICE_COMPILE__
+          sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, u), __builtin_bit_cast(bf16x2, u), sum, false);
+#endif
+        }
+      }
+  }
 };
 
 // Per token and head of a tile: what the state's products take, and what M takes. Exponents are of
@@ -160,6 +176,12 @@ __device__ __forceinline__ double read_lane(double v, int lane) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+// max(v, least), but a NaN stays one.
+__device__ __forceinline__ float at_least(float least, float v) { return v < least ? least : v; }
+
+// A decay below e^-1e6 is 0 in any case; without the bound an infinite rate would leave no differences.
+__device__ __forceinline__ float bounded_rate(float rate) { return at_least(-1e6f, rate); }
+
 // One wave: lane = token (those behind the tile's rows have D = 0). G is summed in float64, so
 // that differences of two of its values keep float32 accuracy however large both are.
 // BLOCKS: also what joins blocks of 16 tokens.
@@ -168,9 +190,8 @@ __device__ __forceinline__ void make_decay(Decay& d, Inner& m, float raw, bool i
   const int lane = __lane_id();
   float e, r;
   const float dt = in ? softplus_f32(raw + bias, e, r) : 0.f;
-  // a decay below e^-1e6 is 0 in any case; without the bound an infinite one would leave no differences
-  const float rate = in ? neg_rate * dt : 0.f;
-  double g = (double)(rate < -1e6f ? -1e6f : rate) * 1.4426950408889634;
+  const float rate = in ? bounded_rate(neg_rate * dt) : 0.f;
+  double g = (double)rate * 1.4426950408889634;
   g += dpp_or_zero<0x111, 0xf>(g);  // inclusive sums within rows of 16 lanes: shifts by 1, 2, 4, 8
   g += dpp_or_zero<0x112, 0xf>(g);
   g += dpp_or_zero<0x114, 0xf>(g);
@@ -209,6 +230,189 @@ __device__ __forceinline__ unsigned pack2(float a, float b) {
 __device__ __forceinline__ float low(unsigned u) { return __builtin_bit_cast(float, u << 16); }
 __device__ __forceinline__ float high(unsigned u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
 
+// The part of the work that a workgroup takes: a segment, and columns of HB heads that share b and c.
+struct Place {
+  int segk, seg0, end;   // the segment, and its tokens
+  int h0, v0, width, grp;  // first head, first column in it, real columns of each head, pair of b and c
+  int pos, seq;          // the first token to look at, and its sequence
+  bool carry;            // without outputs: the state that enters the segment reaches its end
+  bool any;              // without outputs: a sequence goes on over the segment's end
+};
+
+// Workgroups that have a segment: with outputs every one, without those whose end a sequence may go on over.
+template <bool OUT>
+__device__ __forceinline__ int main_blocks(const SsmArgs& a, int hblocks) {
+  const int inner = a.per > 0 ? a.per - 1 : a.nseg - 1;
+  return hblocks * (OUT ? a.nseg : a.per > 0 ? a.N * inner : inner);
+}
+
+template <int PP, int HB, bool OUT>
+__device__ __forceinline__ Place place_of(const SsmArgs& a, int hblocks, int bid) {
+  Place w;
+  const int vblocks = (a.V + PP - 1) / PP, inner = a.per > 0 ? a.per - 1 : a.nseg - 1;
+  const int blocks = main_blocks<OUT>(a, hblocks);
+  // neighbouring head blocks (which share b and c) on one XCD: workgroups are dealt out
+  // round-robin over the 8 of them
+  if (blocks % 8 == 0) bid = (bid & 7) * (blocks / 8) + (bid >> 3);
+  w.segk = bid / hblocks;
+  const int hb = bid - w.segk * hblocks;
+  if (!OUT && a.per > 0) w.segk = w.segk / inner * a.per + w.segk % inner;
+  w.h0 = hb / vblocks * HB, w.v0 = hb % vblocks * PP;
+  w.width = min(PP, a.V - w.v0);
+  w.grp = w.h0 / (a.HV / a.H);
+  w.seg0 = w.segk * a.seg;
+  w.end = (int)min((int64_t)w.seg0 + a.seg, (int64_t)a.T);
+  w.pos = w.seg0;
+  w.carry = w.any = true;
+  if constexpr (OUT) {
+    w.seq = a.seqs.find(w.seg0);
+  } else {
+    // only the part of the sequence that goes on behind the segment's end
+    w.seq = a.seqs.find(w.end - 1);
+    const Span s = a.seqs.span(w.seq);
+    w.any = s.eos > w.end && s.bos < w.end;
+    w.carry = s.bos < w.seg0;
+    w.pos = max(w.seg0, s.bos);
+  }
+  return w;
+}
+
+// The tile at or behind token t, looked for from sequence s on: rows == 0 if there is none in front of end.
+template <int ROWS>
+__device__ __forceinline__ Tile tile_at(const SsmArgs& a, int end, int t, int s) {
+  while (t < end && s < a.N) {
+    const Span sp = a.seqs.span(s);
+    if (sp.eos <= t) { ++s; continue; }
+    if (sp.bos > t) { t = sp.bos; continue; }
+    const int rows = min(ROWS, min(sp.eos, end) - t);
+    return Tile{t, rows, s, sp.eos, t == sp.bos, t + rows == sp.eos};
+  }
+  return Tile{end, 0, s, end, false, false};
+}
+
+// A value of x that the products of a tile do not take.
+__device__ __forceinline__ bool odd_value(float v) { return !(fabsf(v) < INFINITY); }
+
+// The sequences of a workgroup's segment that hold an odd x, as the recurrence is defined: token by
+// token. Products of a whole tile are no form of it there: the zeros of M times an infinity are NaN in
+// tokens in front of it, and an infinity less its own first term is NaN in the state. Runs behind the
+// products and writes over what they left in these sequences. It is rare, so it is written for few
+// registers, and not inlined, so that the products' loop is compiled as if it were not there (inlined:
+// 378 us instead of 366 at 4 x 8192 tokens, 64 heads x 64, K = 128).
+// SPLIT threads share a column, each has every SPLIT-th row of the state. args: the kernel's SsmArgs.
+typedef const __attribute__((address_space(4))) unsigned* arg_words;
+template <typename T, int NP, int PP, int HB, bool OUT, int LDX, int LDB, int LDC>
+__device__ __attribute__((noinline)) void by_token(arg_words args, int hblocks, int bid, int tid, T* Xs, T* Bs,
+                                                    T* Cs, Decay* dec, int* s_odd) {
+  constexpr int XC = HB * PP, SPLIT = kThreads / XC, R = NP / SPLIT, kTok = kTokens<T>;
+  static_assert(SPLIT * XC == kThreads && R * SPLIT == NP, "whole columns");
+  static_assert(PP % (64 / SPLIT) == 0, "a wave's columns are of one head");
+  // arguments of a function arrive in vector registers: uniform ones go back to scalar ones
+  const uint64_t words = (uint64_t)args;
+  args = (arg_words)((uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(words >> 32)) << 32 |
+                     (unsigned)__builtin_amdgcn_readfirstlane((int)words));
+  SsmArgs a;
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(a) / 4; ++i) reinterpret_cast<unsigned*>(&a)[i] = args[i];
+  const Place w = place_of<PP, HB, OUT>(a, __builtin_amdgcn_readfirstlane(hblocks), __builtin_amdgcn_readfirstlane(bid));
+  const int K = a.K, V = a.V, k = tid % SPLIT, col = tid / SPLIT, p = col % PP;
+  const int head = __builtin_amdgcn_readfirstlane(col / PP);
+  const int hv = w.h0 + head;
+  const bool real = p < w.width;
+  const int64_t sz = (int64_t)K * V, ldy = (int64_t)a.HV * V;
+  const int at = w.v0 + p;
+  const T* x = static_cast<const T*>(a.x) + (int64_t)w.h0 * V + w.v0;
+  const T* b = static_cast<const T*>(a.b) + (int64_t)w.grp * K;
+  const T* c = static_cast<const T*>(a.c) + (int64_t)w.grp * K;
+  float s[R], gsum = 0.f;  // gsum: log2 of the decay so far
+  // as in the products' pass: elements outside of [K, V] read zeros and are not written
+  const unsigned state_bytes = (unsigned)(K * V * 4);
+  auto each_row = [&](auto f) {
+    unsigned off = real ? (unsigned)(k * V + at) * 4u : kOutOfRange;
+#pragma unroll
+    for (int r = 0; r < R; ++r, off += (unsigned)(SPLIT * V * 4)) {
+      f(r, off);
+      asm volatile("" : "+v"(off));
+    }
+  };
+  auto load_state = [&](const float* src) {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(src, src ? state_bytes : 0u);
+    each_row([&](int r, unsigned off) { s[r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0)); });
+  };
+  auto store_state = [&](float* dst) {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(dst, state_bytes);
+    each_row([&](int r, unsigned off) {
+      const float v = s[r];
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), rs, off, 0, 0);
+    });
+  };
+  load_state(OUT && w.segk > 0 && a.seqs.span(w.seq).bos < w.seg0 ? a.seg_state + ((int64_t)(w.segk - 1) * a.HV + hv) * sz
+                                                                   : nullptr);
+  const float skip = a.D ? a.D[hv] : 0.f;
+  for (Tile t = tile_at<kTok>(a, w.end, w.pos, w.seq); t.rows > 0;) {
+    const int stop = min(t.eos, w.end);  // of the sequence's part
+    bool odd = false;
+    for (int i = t.t0; i < stop; ++i)
+      for (int j = tid; j < HB * w.width; j += kThreads)
+        odd |= odd_value(to_f32(x[i * a.ldx + (int64_t)(j / w.width) * V + j % w.width]));
+    block_barrier();
+    if (tid == 0) *s_odd = 0;
+    block_barrier();
+    if (odd) *s_odd = 1;  // any writer stores the same
+    block_barrier();
+    if (*s_odd == 0) {
+      t = tile_at<kTok>(a, w.end, stop, t.seq);
+      continue;
+    }
+    for (; t.t0 < stop && t.rows > 0; t = tile_at<kTok>(a, w.end, t.t0 + t.rows, t.seq)) {
+      if (t.first) load_state(a.s0 ? a.s0 + ((int64_t)t.seq * a.HV + hv) * sz : nullptr);
+      block_barrier();
+      for (int i = 0; i < t.rows; ++i) {
+        const int64_t row = t.t0 + i;
+        if (tid < XC) Xs[i * LDX + tid] = tid % PP < w.width ? x[row * a.ldx + (int64_t)(tid / PP) * V + tid % PP] : from_f32<T>(0.f);
+        if (tid < NP) Bs[i * LDB + tid] = tid < K ? b[row * a.ldb + tid] : from_f32<T>(0.f);
+        if (OUT && tid < NP) Cs[i * LDC + tid] = tid < K ? c[row * a.ldc + tid] : from_f32<T>(0.f);
+      }
+      if (tid < t.rows)
+        for (int h = 0; h < HB; ++h) {
+          float e, q;
+          const float raw = to_f32(static_cast<const T*>(a.dt)[(int64_t)(t.t0 + tid) * a.lddt + w.h0 + h]);
+          const float dt = softplus_f32(raw + (a.dt_bias ? a.dt_bias[w.h0 + h] : 0.f), e, q);
+          dec[h].w[tid] = dt;
+          dec[h].eg[tid] = bounded_rate(negative_rate(a.A_log[w.h0 + h]) * dt) * kLog2e;
+        }
+      block_barrier();
+#pragma unroll 1
+      for (int i = 0; i < t.rows; ++i) {
+        const float g = dec[head].eg[i], decay = fast_exp2(g), xv = to_f32(Xs[i * LDX + col]), dx = dec[head].w[i] * xv;
+        float sum = 0.f;
+        gsum += g;
+        int left = K - k;  // rows of the state from this thread's first one on
+        asm volatile("" : "+v"(left));  // compared anew for every token: masks would fill the registers
+        const T* bi = Bs + i * LDB + k;
+        const T* ci = Cs + i * LDC + k;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float xr = SPLIT * r < left ? dx : 0.f;
+          s[r] = decay * s[r] + to_f32(bi[SPLIT * r]) * xr;
+          if constexpr (OUT) sum += s[r] * to_f32(ci[SPLIT * r]);
+          if (r % 4 == 3) asm volatile("" : "+v"(left)::"memory");  // few registers rather than speed
+        }
+        if constexpr (OUT) {
+#pragma unroll
+          for (int off = 1; off < SPLIT; off *= 2) sum += __shfl_xor(sum, off);
+          if (k == 0 && real) static_cast<T*>(a.y)[(t.t0 + i) * ldy + (int64_t)hv * V + at] = from_f32<T>(sum + skip * xv);
+        }
+      }
+      if (OUT && t.last && a.sT) store_state(a.sT + ((int64_t)t.seq * a.HV + hv) * sz);
+      if (!OUT && t.t0 + t.rows == w.end) {
+        store_state(a.seg_state + ((int64_t)w.segk * a.HV + hv) * sz);
+        if (at == 0 && k == 0) a.seg_g[(int64_t)w.segk * a.HV + hv] = w.carry ? gsum : -INFINITY;
+      }
+    }
+  }
+}
+
 // NT: K in tiles of 16; HB heads of PP columns; PT tiles of 16 columns a wave.
 template <typename T, int NT, int PP, int HB, int PT, bool OUT, bool VEC>
 __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hblocks) {
@@ -228,68 +432,32 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
   __shared__ __attribute__((aligned(16))) T Ms[OUT ? HB * kTok * LDM : 8];
   __shared__ __attribute__((aligned(16))) Decay s_dec[2][HB];
   __shared__ __attribute__((aligned(16))) Inner s_in[OUT ? HB : 1];  // read in front of a tile's second barrier only
+  __shared__ int s_odd[NW];
 
-  const int K = a.K, V = a.V, vblocks = (V + PP - 1) / PP;
-  // with outputs: every segment; without: those whose end a sequence may go on over
-  const int inner = a.per > 0 ? a.per - 1 : a.nseg - 1;
-  const int main_blocks = hblocks * (OUT ? a.nseg : a.per > 0 ? a.N * inner : inner);
-  int bid = blockIdx.x;
-  if (OUT && bid >= main_blocks) {  // empty sequences: the state passes through
-    const int n = bid - main_blocks;
+  const int K = a.K, V = a.V;
+  if (OUT && (int)blockIdx.x >= main_blocks<OUT>(a, hblocks)) {  // empty sequences: the state passes through
+    const int n = blockIdx.x - main_blocks<OUT>(a, hblocks);
     const Span s = a.seqs.span(n);
     if (s.eos > s.bos) return;
     const int64_t sz = (int64_t)a.HV * K * V;
     for (int64_t i = threadIdx.x; i < sz; i += kThreads) a.sT[n * sz + i] = a.s0 ? a.s0[n * sz + i] : 0.f;
     return;
   }
-  // neighbouring head blocks (which share b and c) on one XCD: workgroups are dealt out
-  // round-robin over the 8 of them
-  if (main_blocks % 8 == 0) bid = (bid & 7) * (main_blocks / 8) + (bid >> 3);
-  int segk = bid / hblocks;
-  const int hb = bid - segk * hblocks;
-  if (!OUT && a.per > 0) segk = segk / inner * a.per + segk % inner;
-  const int h0 = hb / vblocks * HB, v0 = hb % vblocks * PP;  // first head, first column in it
-  const int width = min(PP, V - v0);                          // real columns of each head
-  const int grp = h0 / (a.HV / a.H);
-
+  const Place w = place_of<PP, HB, OUT>(a, hblocks, blockIdx.x);
+  const int segk = w.segk, h0 = w.h0, v0 = w.v0, width = w.width, grp = w.grp, end = w.end;
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int lr = lane & 15, lq = lane >> 4;
   const int col0 = wv * 16 * PT, hh = col0 / PP, p0 = v0 + col0 - hh * PP;
   const bool active = XC == 16 * PT * NW || hh < HB;  // waves behind the last head only help with c . b
   const int hv = h0 + (active ? hh : 0);
   const int dw = wv - (NW - HB);  // the last HB waves prepare the decays of head dw
-
-  const int seg0 = segk * a.seg;
-  const int end = (int)min((int64_t)seg0 + a.seg, (int64_t)a.T);
-  int pos = seg0, seq;
-  bool carry = true;  // OUT = false: the state entering the segment reaches its end
-  if constexpr (OUT) {
-    seq = a.seqs.find(seg0);
-  } else {
-    // only the part of the sequence that goes on behind the segment's end
-    seq = a.seqs.find(end - 1);
-    const Span s = a.seqs.span(seq);
-    if (s.eos <= end || s.bos >= end) {
-      if (wv == 0 && lane < HB && v0 == 0) a.seg_g[(int64_t)segk * a.HV + h0 + lane] = kNoCarry;
-      return;
-    }
-    carry = s.bos < seg0;
-    pos = max(seg0, s.bos);
+  if (!w.any) {
+    if (wv == 0 && lane < HB && v0 == 0) a.seg_g[(int64_t)segk * a.HV + h0 + lane] = kNoCarry;
+    return;
   }
 
   T* y = static_cast<T*>(a.y);
   const int64_t ldy = (int64_t)a.HV * V;
-  // the tile at or behind token t: rows == 0 if the segment holds none
-  auto tile_at = [&](int t, int s) {
-    while (t < end && s < a.N) {
-      const Span sp = a.seqs.span(s);
-      if (sp.eos <= t) { ++s; continue; }
-      if (sp.bos > t) { t = sp.bos; continue; }
-      const int rows = min(kTok, min(sp.eos, end) - t);
-      return Tile{t, rows, s, sp.eos, t == sp.bos, t + rows == sp.eos};
-    }
-    return Tile{end, 0, s, end, false, false};
-  };
   // rows [t, to) lie in no sequence
   auto outside = [&](int t, int to) {
     if (!OUT || !a.zero_rest || t >= to) return;
@@ -363,7 +531,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
   const int64_t sz = (int64_t)K * V;
   zero_state();
   if constexpr (OUT) {
-    if (segk > 0 && a.seqs.span(seq).bos < seg0) {
+    if (segk > 0 && a.seqs.span(w.seq).bos < w.seg0) {
       load_state(a.seg_state + ((int64_t)(segk - 1) * a.HV + hv) * sz);
     }
   }
@@ -376,16 +544,17 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
     }
   }
 
-  Tile cur = tile_at(pos, seq);
-  outside(pos, cur.t0);
+  Tile cur = tile_at<kTok>(a, end, w.pos, w.seq);
+  outside(w.pos, cur.t0);
   if (cur.rows == 0) return;
   load(cur);
   if (dw >= 0)
     make_decay<OUT, OUT && BF>(s_dec[0][dw], s_in[OUT ? dw : 0], to_f32(dtr), lane < cur.rows, bias, neg_rate);
-  float gsum = 0.f;
+  float gsum = 0.f, squares = 0.f;
 
   __builtin_amdgcn_s_waitcnt(0);  // the first tile's loads, so that the wait in the loop is that of later ones
   for (int buf = 0;; buf ^= 1) {
+    xr.add_squares(squares);
     xr.store(Xs, LDX);
     br.store(Bs, LDB);
     if constexpr (OUT) cr.store(Cs, LDC);
@@ -395,7 +564,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
     if (nxt.rows > 0) {
       nxt.last = done + nxt.rows == cur.eos;
     } else {
-      nxt = tile_at(done, cur.seq);
+      nxt = tile_at<kTok>(a, end, done, cur.seq);
       outside(done, nxt.t0);
     }
     if (cur.first) {  // the sequence's initial state
@@ -582,10 +751,11 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
             store_y(it, acc);
           }
         }
-        // the next tile's loads go out here: their registers are free only now
+        // the next tile's loads go out here: their registers are free only now (loads of single elements
+        // take twice as many: behind the state's products, 8192 tokens, 16 heads x 60, K 100: 192 -> 124 us)
         if constexpr (OUT) {
           __builtin_amdgcn_sched_barrier(0);
-          load(nxt);
+          if constexpr (VEC) load(nxt);
           __builtin_amdgcn_sched_barrier(0);  // not behind the products of the state
         }
         // the state's update
@@ -669,6 +839,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
         }
       }
       if (OUT && cur.last && a.sT) store_state(a.sT + ((int64_t)cur.seq * a.HV + hv) * sz);
+      if constexpr (OUT && BF && !VEC) load(nxt);
       gsum += dec[hh].end;
     } else if constexpr (OUT) {
       load(nxt);
@@ -682,7 +853,17 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
   if constexpr (!OUT) {
     store_state(a.seg_state + ((int64_t)segk * a.HV + hv) * sz);
     // a sequence that starts in the segment takes nothing from the segment before
-    if (active && p0 == 0 && lane == 0) a.seg_g[(int64_t)segk * a.HV + hv] = carry ? gsum : -INFINITY;
+    if (active && p0 == 0 && lane == 0) a.seg_g[(int64_t)segk * a.HV + hv] = w.carry ? gsum : -INFINITY;
+  }
+  // a sum of squares that is not finite: some x may be odd (or only too large to square, which
+  // by_token() finds out)
+  if (lane == 0) s_odd[wv] = 0;
+  if (!(squares < INFINITY)) s_odd[wv] = 1;  // any writer stores the same
+  block_barrier();
+  if (__builtin_amdgcn_readfirstlane(s_odd[0] | s_odd[1] | s_odd[2] | s_odd[3]) != 0) {
+    __builtin_amdgcn_s_waitcnt(0);  // what by_token() writes over is written
+    by_token<T, NP, PP, HB, OUT, LDX, LDB, LDC>((arg_words)__builtin_amdgcn_kernarg_segment_ptr(), hblocks, blockIdx.x,
+                                                threadIdx.x, Xs, Bs, Cs, s_dec[0], s_odd);
   }
 }
 

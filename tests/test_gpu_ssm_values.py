@@ -1,0 +1,111 @@
+"""kda_ssm_chunk_fwd where inputs or states are not finite, or too large for products of a whole tile:
+the recurrence, token by token, says which outputs stay finite, and those are what they would be.
+
+Against the float64 oracle: NaN where it has NaN, its infinity where it has one, and elsewhere the
+tolerances of test_gpu_ssm.py (derived there). No decay of these inputs underflows in one token (an
+infinite state times a decay of 0 would be NaN in float32 and infinite in float64): exp(A_log) <= 4 and
+D_t < 8, so a_t > 2^-47, while the product over a tile of 64 tokens or a segment does underflow."""
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_67_amd as kda
+from oracle import selective_scan
+from tests.helpers import log, to64
+from tests.test_gpu_ssm import DT, _fwd, _make
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(2, 1, 128, 64), (1, 1, 128, 128), (3, 1, 64, 64), (4, 1, 32, 32), (2, 2, 33, 27), (1, 1, 1, 5), (2, 1, 72, 100)]
+INF, NAN = float("inf"), float("nan")
+
+
+def _inputs(lengths, HV, H, K, V, dtype, seed, **kw):
+    d, cu = _make(lengths, HV, H, K, V, DT[dtype], seed=seed, **kw)
+    d["A_log"] = torch.log(1 + 3 * torch.rand(HV, generator=torch.Generator().manual_seed(seed))).cuda()
+    for k in ("x", "b", "c", "dt"):
+        d[k] = d[k].contiguous().clone()
+    return d, cu
+
+
+def _compare(got, ref, tol, what):
+    got = to64(got)
+    nan, inf = np.isnan(ref), np.isinf(ref)
+    fin = ~(nan | inf)
+    lost = int((~np.isfinite(got[fin])).sum())
+    assert lost == 0, f"{what}: {lost} values of {int(fin.sum())} are not finite"
+    assert np.isnan(got[nan]).all(), f"{what}: NaN expected"
+    assert np.array_equal(got[inf], ref[inf]), f"{what}: {int((got[inf] != ref[inf]).sum())} infinities lost"
+    ratio = float(np.max(np.abs(got[fin] - ref[fin]) / tol[fin])) if fin.any() else 0.0
+    log(f"    {what}: {int(nan.sum())} NaN, {int(inf.sum())} Inf, worst |err| / tolerance {ratio:.3f}")
+    assert ratio <= 1.0, f"{what}: {ratio}"
+
+
+def _check(d, lengths, y, final, dtype):
+    h = {k: None if v is None else to64(v) for k, v in d.items()}
+    at = 0
+    with np.errstate(all="ignore"):
+        for n, L in enumerate(lengths):
+            one = {k: h[k][at:at + L] for k in ("x", "dt", "b", "c")}
+            ry, rs, ya, sa = selective_scan(**one, A_log=h["A_log"], D=h["D"], dt_bias=h["dt_bias"],
+                                            state=None if h["state"] is None else h["state"][n])
+            f32 = 2.0 ** -15
+            ytol = f32 * ya + 1e-30 + (2.0 ** -8 * (ya + np.abs(ry)) if dtype == "bf16" else 0)
+            _compare(y[at:at + L], ry, ytol, f"y of {n} ({L})")
+            _compare(final[n], rs, f32 * sa + 1e-30, f"state of {n}")
+            at += L
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("HV,H,K,V", SHAPES)
+@pytest.mark.parametrize("value", [INF, NAN])
+def test_tokens_in_front_of_a_non_finite_x(dtype, HV, H, K, V, value):
+    """A row of y holds no later token's x, whatever that is. Two segments, the first ends inside the
+    first sequence; the second sequence's tokens lie in the middle of a tile and at a tile's end."""
+    lengths = [300, 127]
+    log(f"x = {value}, {dtype} HV={HV} H={H} K={K} V={V}")
+    d, cu = _inputs(lengths, HV, H, K, V, dtype, seed=HV + K + V)
+    d["x"][290, 0, V - 1] = value
+    d["x"][300 + 47, HV - 1, 0] = value
+    d["x"][300 + 126, 0, V // 2] = -value
+    y, final = _fwd(d, cu)
+    _check(d, lengths, y, final, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sequences_beside_one_with_a_non_finite_x(dtype):
+    """Many sequences in one segment: those with such an x go as the recurrence says, the others keep
+    their bits, and so do the rows that lie in no sequence."""
+    lengths = [5] * 20 + [90, 0, 200] + [1, 70, 3]
+    T = sum(lengths)
+    d, cu = _inputs(lengths, 4, 2, 64, 32, dtype, seed=21)
+    cu = cu + 7  # rows in front of the first sequence and behind the last one
+    for k in ("x", "b", "c", "dt"):
+        d[k] = torch.cat([d[k][:7], d[k], d[k][:9]])
+    y0, f0 = _fwd(d, cu)
+    bad = {3: 2, 20: 40, 22: 150, 24: 0}
+    start = np.concatenate([[0], np.cumsum(lengths)])
+    for n, at in bad.items():
+        d["x"][7 + int(start[n]) + at, n % 4, 1 + n] = NAN if n == 20 else INF
+    y, f = _fwd(d, cu)
+    for n, L in enumerate(lengths):
+        if n not in bad:
+            rows = slice(7 + int(start[n]), 7 + int(start[n]) + L)
+            assert torch.equal(y[rows], y0[rows]) and torch.equal(f[n], f0[n]), n
+    assert not y[:7].any() and not y[7 + T:].any()
+    inner = dict(d, **{k: d[k][7:7 + T] for k in ("x", "b", "c", "dt")})
+    _check(inner, lengths, y[7:7 + T], f, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,value", [(2, 1024, NAN), (3, 640, NAN)])
+def test_dense_batches_with_a_non_finite_x(dtype, B, T, value):
+    """Segments that divide the sequences evenly; the pass that makes the states of their ends meets the
+    value too."""
+    d, _ = _inputs([T] * B, 4, 2, 64, 64, dtype, seed=T)
+    d["x"][100, 0, 3] = value
+    d["x"][T + T // 2 + 1, 2, 63] = value
+    dense = {k: (v.unflatten(0, (B, T)) if k in ("x", "b", "c", "dt") else v) for k, v in d.items()}
+    y, final = _fwd(dense, None)
+    _check(d, [T] * B, y.flatten(0, 1), final, dtype)
