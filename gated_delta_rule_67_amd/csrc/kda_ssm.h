@@ -12,6 +12,13 @@ __device__ __forceinline__ float negative_rate(float A_log) {
   return rate < -3.402823466e38f ? -3.402823466e38f : rate;
 }
 
+// max(v, least), but a NaN stays one.
+__device__ __forceinline__ float at_least(float least, float v) { return v < least ? least : v; }
+
+// 2^g, what a state keeps of itself: never 0, because an infinite state times 0 would be NaN. The
+// smallest float (2^-149) adds less to a finite one than the error of an exponential that underflows.
+__device__ __forceinline__ float decay_of(float g) { return at_least(0x1p-149f, fast_exp2(g)); }
+
 struct SsmArgs {
   const void* x;   // [T, HV, V], ldx elements between tokens
   int64_t ldx;

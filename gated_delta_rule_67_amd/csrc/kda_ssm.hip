@@ -176,9 +176,6 @@ __device__ __forceinline__ double read_lane(double v, int lane) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// max(v, least), but a NaN stays one.
-__device__ __forceinline__ float at_least(float least, float v) { return v < least ? least : v; }
-
 // A decay below e^-1e6 is 0 in any case; without the bound an infinite rate would leave no differences.
 __device__ __forceinline__ float bounded_rate(float rate) { return at_least(-1e6f, rate); }
 
@@ -203,7 +200,7 @@ __device__ __forceinline__ void make_decay(Decay& d, Inner& m, float raw, bool i
   if (lane == 0) d.end = (float)end;
   if constexpr (OUT) {
     const float hi = (float)g;
-    d.eg[lane] = fast_exp2(hi);
+    d.eg[lane] = decay_of(hi);
     m.dt[lane] = dt;
     m.hi[lane] = hi;
     m.lo[lane] = (float)(g - (double)hi);
@@ -384,7 +381,7 @@ __device__ __attribute__((noinline)) void by_token(arg_words args, int hblocks, 
       block_barrier();
 #pragma unroll 1
       for (int i = 0; i < t.rows; ++i) {
-        const float g = dec[head].eg[i], decay = fast_exp2(g), xv = to_f32(Xs[i * LDX + col]), dx = dec[head].w[i] * xv;
+        const float g = dec[head].eg[i], decay = decay_of(g), xv = to_f32(Xs[i * LDX + col]), dx = dec[head].w[i] * xv;
         float sum = 0.f;
         gsum += g;
         int left = K - k;  // rows of the state from this thread's first one on
@@ -708,7 +705,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
           for (int r = 0; r < 4; ++r)
             acc[pt][r] = acc[pt][r] * eg + skip * to_f32(Xs[i * LDX + col0 + column(pt, lq, r)]);
       };
-      const float ga = fast_exp2(dec[hh].end);
+      const float ga = decay_of(dec[hh].end);
       if constexpr (BF) {
         // x of this wave's columns, transposed: rows p, 8 tokens a lane
         bf16x8 xf[PT][2];
@@ -892,7 +889,7 @@ __global__ __launch_bounds__(kThreads) void compose_kernel(float* __restrict__ s
       // nothing was made of a sequence's last segment; where nothing is carried the product is left
       // out: s may be infinite
       const bool none = g[u] == kNoCarry || (per > 0 && (k0 + u + 1) % per == 0);
-      s = none ? 0.f : g[u] > -INFINITY ? v[u] + fast_exp2(g[u]) * s : v[u];
+      s = none ? 0.f : g[u] > -INFINITY ? v[u] + decay_of(g[u]) * s : v[u];
       if (!none) seg_state[(int64_t)(k0 + u) * n + i] = s;
     }
   }

@@ -54,7 +54,7 @@ __global__ __launch_bounds__(kThreads) void step_kernel(SsmArgs a, int nsplit) {
   }
   float e, q;
   const float dt = softplus_f32(raw + (a.dt_bias ? a.dt_bias[hv] : 0.f), e, q);
-  const float decay = fast_exp2(negative_rate(a.A_log[hv]) * dt * kLog2e);
+  const float decay = decay_of(negative_rate(a.A_log[hv]) * dt * kLog2e);
   vec_t xd = {}, acc = {};
   if (active)
 #pragma unroll

@@ -518,6 +518,7 @@ int kda_conv_step(const void* x, int64_t x_stride, const float* weight, const fl
  * boundaries joins them (as in kda_chunk_fwd_segmented). Results are bitwise reproducible.
  * An x that is not finite reaches the outputs that the recurrence gives it to, as an infinity or a
  * NaN, and no others; its sequence is then taken token by token (more slowly) in that segment.
+ * No decay is quite 0: an infinite state stays infinite (in kda_ssm_step too).
  * Constraints: N >= 1, T >= 0, HV % H == 0 (else KDA_ERR_INVALID); K, V <= 128, HV <= 2^16,
  * N <= 2^20, T <= 2^30, and under 2^24 workgroups (about one per 64 columns of a sequence's or
  * segment's heads) (else KDA_ERR_UNSUPPORTED). Nothing is allocated.

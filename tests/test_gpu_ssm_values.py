@@ -99,7 +99,7 @@ def test_sequences_beside_one_with_a_non_finite_x(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("B,T,value", [(2, 1024, NAN), (3, 640, NAN)])
+@pytest.mark.parametrize("B,T,value", [(2, 1024, NAN), (3, 640, NAN), (2, 1024, INF)])
 def test_dense_batches_with_a_non_finite_x(dtype, B, T, value):
     """Segments that divide the sequences evenly; the pass that makes the states of their ends meets the
     value too."""
@@ -109,3 +109,47 @@ def test_dense_batches_with_a_non_finite_x(dtype, B, T, value):
     dense = {k: (v.unflatten(0, (B, T)) if k in ("x", "b", "c", "dt") else v) for k, v in d.items()}
     y, final = _fwd(dense, None)
     _check(d, [T] * B, y.flatten(0, 1), final, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("HV,H,K,V", SHAPES)
+def test_infinite_states(dtype, HV, H, K, V):
+    """An infinite state stays one while the product of its decays underflows: over tiles, segments
+    and their composition, from the initial state and from a token on."""
+    lengths = [700, 90]
+    d, cu = _inputs(lengths, HV, H, K, V, dtype, seed=31 + K + V)
+    d["state"][0, 0, K - 1, V - 1] = INF
+    d["state"][0, HV - 1, K // 2, 0] = -INF
+    d["state"][1, 0, 0, V // 2] = NAN
+    d["x"][700 + 20, HV - 1, V - 1] = INF
+    _check(d, lengths, *_fwd(d, cu), dtype)
+    dense = {k: (v[:700].unflatten(0, (1, 700)) if k in ("x", "b", "c", "dt") else v) for k, v in d.items()}
+    dense["state"] = d["state"][:1]
+    y, final = _fwd(dense, None)
+    _check(dict(d, state=d["state"][:1]), [700], y[0], final, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinite_states_where_one_decay_underflows(dtype):
+    """Prompts and steps agree: a decay is never quite 0, so the infinity stays and the other values
+    are those of a decay of 0."""
+    HV, H, K, V, B = 2, 1, 64, 32, 3
+    d, cu = _inputs([1] * B, HV, H, K, V, dtype, seed=41)
+    d["A_log"] = torch.full((HV,), 7.0).cuda()  # rate 1097
+    d["dt"] = torch.full_like(d["dt"], 3.0)
+    d["state"][:, 1, 5, 7] = -INF
+    y, final = _fwd(d, cu)
+    pool = d["state"].clone()
+    step = kda.kda_ssm_step(d["x"], d["dt"], d["A_log"], d["b"], d["c"], pool, d["D"], d["dt_bias"])
+    clean = dict(d, state=torch.zeros_like(d["state"]))
+    h = {k: to64(v) for k, v in clean.items()}
+    for n in range(B):
+        one = {k: h[k][n:n + 1] for k in ("x", "dt", "b", "c")}
+        ry, rs, ya, sa = selective_scan(**one, A_log=h["A_log"], D=h["D"], dt_bias=h["dt_bias"])
+        rs[1, 5, 7] = -np.inf
+        ry[0, 1, 7] = -np.inf * np.sign(h["c"][n, 0, 5])
+        f32 = 2.0 ** -15
+        ytol = f32 * ya + 1e-30 + (2.0 ** -8 * (ya + np.abs(ry)) if dtype == "bf16" else 0)
+        for got, state, what in ((y, final, "prompt"), (step, pool, "step")):
+            _compare(got[n:n + 1], ry, ytol, f"y of {what} {n}")
+            _compare(state[n], rs, f32 * sa + 1e-30, f"state of {what} {n}")
