@@ -634,7 +634,8 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
           if (!wide || jt < it) {
 #pragma unroll
             for (int h = 0; h < HB; ++h) {
-              f32x4 m = sc * col[h] * row[h];
+              // the factors first: their product is at most D_j, a score times one of them may overflow
+              f32x4 m = sc * (col[h] * row[h]);
 #pragma unroll
               for (int r = 0; r < 4; ++r) m[r] = j + r <= i ? m[r] : 0.f;
               put_m(h, i, j, m);

@@ -153,3 +153,17 @@ def test_infinite_states_where_one_decay_underflows(dtype):
         for got, state, what in ((y, final, "prompt"), (step, pool, "step")):
             _compare(got[n:n + 1], ry, ytol, f"y of {what} {n}")
             _compare(state[n], rs, f32 * sa + 1e-30, f"state of {what} {n}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [2.0 ** 20, 2.0 ** 34])
+def test_large_products_with_strong_decays(dtype, scale):
+    """c . b times the largest factor of a block of 16 tokens passes float32, what it stands for does not:
+    every token decays by about 2^-3.9, so a block by nearly 2^-60."""
+    lengths = [150]
+    d, cu = _inputs(lengths, 2, 1, 128, 64, dtype, seed=51, init=False, bias=False)
+    d["A_log"] = torch.log(torch.tensor([3.9, 3.7])).cuda()
+    d["dt"] = torch.full_like(d["dt"], float(np.log(np.expm1(np.log(2.0)))))  # D_t = ln 2
+    d["b"] *= scale
+    d["c"] *= scale
+    _check(d, lengths, *_fwd(d, cu), dtype)
