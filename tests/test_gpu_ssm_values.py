@@ -167,3 +167,32 @@ def test_large_products_with_strong_decays(dtype, scale):
     d["b"] *= scale
     d["c"] *= scale
     _check(d, lengths, *_fwd(d, cu), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name,value", [("b", INF), ("b", NAN), ("c", -INF), ("c", NAN), ("dt", INF), ("dt", NAN)])
+def test_tokens_in_front_of_other_non_finite_inputs(dtype, name, value):
+    """b, c and dt: what the recurrence leaves finite stays so, in front of the token and (c) behind it;
+    where it does not, an infinity may have become NaN."""
+    lengths = [300, 127]
+    d, cu = _inputs(lengths, 2, 1, 64, 64, dtype, seed=61)
+    for t in (130, 300 + 47):
+        if name == "dt":
+            d["dt"][t, 1] = value
+        else:
+            d[name][t, 0, 9] = value
+    y, final = _fwd(d, cu)
+    h = {k: to64(v) for k, v in d.items()}
+    at = 0
+    for n, L in enumerate(lengths):
+        one = {k: h[k][at:at + L] for k in ("x", "dt", "b", "c")}
+        with np.errstate(all="ignore"):
+            ry, rs, ya, sa = selective_scan(**one, A_log=h["A_log"], D=h["D"], dt_bias=h["dt_bias"], state=h["state"][n])
+        f32 = 2.0 ** -15
+        ytol = f32 * ya + 1e-30 + (2.0 ** -8 * (ya + np.abs(ry)) if dtype == "bf16" else 0)
+        for got, ref, tol in ((y[at:at + L], ry, ytol), (final[n], rs, f32 * sa + 1e-30)):
+            got, fin = to64(got), np.isfinite(ref)
+            assert np.isfinite(got[fin]).all() and not np.isfinite(got[~fin]).any()
+            assert float(np.max(np.abs(got[fin] - ref[fin]) / tol[fin])) <= 1
+        assert not np.isfinite(ry).all()
+        at += L
