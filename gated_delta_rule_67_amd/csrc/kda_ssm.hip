@@ -125,7 +125,7 @@ struct Stage {
       *reinterpret_cast<u32x4*>(dst + row * ldd + c) = v[e];
     }
   }
-  // Adds the squares of this thread's values: the sum is finite only if all of them are.
+  // Adds the squares of this thread's values: the sum is finite only if all of them are under 2^64.
   __device__ __forceinline__ void add_squares(float& sum) const {
 #pragma unroll
     for (int e = 0; e < kPieces; ++e)
@@ -287,8 +287,9 @@ __device__ __forceinline__ Tile tile_at(const SsmArgs& a, int end, int t, int s)
   return Tile{end, 0, s, end, false, false};
 }
 
-// A value of x that the products of a tile do not take.
-__device__ __forceinline__ bool odd_value(float v) { return !(fabsf(v) < INFINITY); }
+// A value of x that the products of a tile do not take: not finite, or so large that D x may be past the
+// largest bf16. Its square is infinite or NaN.
+__device__ __forceinline__ bool odd_value(float v) { return !(fabsf(v) < 0x1p64f); }
 
 // The sequences of a workgroup's segment that hold an odd x, as the recurrence is defined: token by
 // token. Products of a whole tile are no form of it there: the zeros of M times an infinity are NaN in
@@ -853,8 +854,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
     // a sequence that starts in the segment takes nothing from the segment before
     if (active && p0 == 0 && lane == 0) a.seg_g[(int64_t)segk * a.HV + hv] = w.carry ? gsum : -INFINITY;
   }
-  // a sum of squares that is not finite: some x may be odd (or only too large to square, which
-  // by_token() finds out)
+  // a sum of squares that is not finite: some x may be odd (which by_token() finds out)
   if (lane == 0) s_odd[wv] = 0;
   if (!(squares < INFINITY)) s_odd[wv] = 1;  // any writer stores the same
   block_barrier();

@@ -196,3 +196,22 @@ def test_tokens_in_front_of_other_non_finite_inputs(dtype, name, value):
             assert float(np.max(np.abs(got[fin] - ref[fin]) / tol[fin])) <= 1
         assert not np.isfinite(ry).all()
         at += L
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_x_near_the_largest_float(dtype):
+    """D_t x stays under the largest float32 and passes the largest bf16, in which the state's products
+    hold its first term (token 63: the last of its tile, so that it enters the state undecayed)."""
+    lengths = [100]
+    d, cu = _inputs(lengths, 2, 1, 64, 64, dtype, seed=71, bias=False)
+    d["x"][63, 1, 7] = torch.finfo(torch.bfloat16).max
+    step = float(np.log(np.expm1(1.003)))
+    d["dt"][63, 1] = step
+    if dtype == "bf16":
+        got = float(np.log1p(np.exp(float(d["dt"][63, 1]))))  # dt is rounded: scale it by the bias
+        d["dt_bias"] = torch.tensor([0.0, step - float(d["dt"][63, 1])]).cuda()
+        assert abs(got - 1.003) < 0.01
+    d["b"][63] *= 2.0 ** -20
+    d["c"] *= 2.0 ** -20
+    d["D"] *= 2.0 ** -20
+    _check(d, lengths, *_fwd(d, cu), dtype)
