@@ -29,6 +29,8 @@
 // tile's loads are issued, 760 for LDS stores. No single pipeline is full (VALU 43%, matrix cores
 // 31%, LDS 35% of the cycles). Tiles of 32 tokens (385 us), 256 or 768 workgroups (466, 405) were
 // slower, eight waves of 16 columns the same.
+#include <type_traits>
+
 #include "kda_ssm.h"
 
 namespace kda {
@@ -297,11 +299,13 @@ __device__ __forceinline__ bool odd_value(float v) { return !(fabsf(v) < 0x1p64f
 // products and writes over what they left in these sequences. It is rare, so it is written for few
 // registers, and not inlined, so that the products' loop is compiled as if it were not there (inlined:
 // 378 us instead of 366 at 4 x 8192 tokens, 64 heads x 64, K = 128).
-// SPLIT threads share a column, each has every SPLIT-th row of the state. args: the kernel's SsmArgs.
+// SPLIT threads share a column, each has R rows of the state. args: the kernel's SsmArgs.
 typedef const __attribute__((address_space(4))) unsigned* arg_words;
+template <typename X> using lds = __attribute__((address_space(3))) X;
 template <typename T, int NP, int PP, int HB, bool OUT, int LDX, int LDB, int LDC>
-__device__ __attribute__((noinline)) void by_token(arg_words args, int hblocks, int bid, int tid, T* Xs, T* Bs,
-                                                    T* Cs, Decay* dec, int* s_odd) {
+__device__ __attribute__((noinline)) void by_token(arg_words args, int hblocks, int bid, int tid,
+                                                    lds<T>* Xs, lds<T>* Bs, lds<T>* Cs,
+                                                    lds<Decay>* dec, lds<int>* s_odd) {
   constexpr int XC = HB * PP, SPLIT = kThreads / XC, R = NP / SPLIT, kTok = kTokens<T>;
   static_assert(SPLIT * XC == kThreads && R * SPLIT == NP, "whole columns");
   static_assert(PP % (64 / SPLIT) == 0, "a wave's columns are of one head");
@@ -326,9 +330,9 @@ __device__ __attribute__((noinline)) void by_token(arg_words args, int hblocks, 
   // as in the products' pass: elements outside of [K, V] read zeros and are not written
   const unsigned state_bytes = (unsigned)(K * V * 4);
   auto each_row = [&](auto f) {
-    unsigned off = real ? (unsigned)(k * V + at) * 4u : kOutOfRange;
+    unsigned off = real ? (unsigned)(k * R * V + at) * 4u : kOutOfRange;
 #pragma unroll
-    for (int r = 0; r < R; ++r, off += (unsigned)(SPLIT * V * 4)) {
+    for (int r = 0; r < R; ++r, off += (unsigned)(V * 4)) {
       f(r, off);
       asm volatile("" : "+v"(off));
     }
@@ -350,9 +354,11 @@ __device__ __attribute__((noinline)) void by_token(arg_words args, int hblocks, 
   for (Tile t = tile_at<kTok>(a, w.end, w.pos, w.seq); t.rows > 0;) {
     const int stop = min(t.eos, w.end);  // of the sequence's part
     bool odd = false;
-    for (int i = t.t0; i < stop; ++i)
-      for (int j = tid; j < HB * w.width; j += kThreads)
-        odd |= odd_value(to_f32(x[i * a.ldx + (int64_t)(j / w.width) * V + j % w.width]));
+    // column tid % XC of every (kThreads / XC)-th token
+    const int j = tid % XC / PP * V + tid % PP;
+    if (tid % PP < w.width)
+#pragma unroll 8
+      for (int i = t.t0 + tid / XC; i < stop; i += SPLIT) odd |= odd_value(to_f32(x[i * a.ldx + j]));
     block_barrier();
     if (tid == 0) *s_odd = 0;
     block_barrier();
@@ -365,12 +371,19 @@ __device__ __attribute__((noinline)) void by_token(arg_words args, int hblocks, 
     for (; t.t0 < stop && t.rows > 0; t = tile_at<kTok>(a, w.end, t.t0 + t.rows, t.seq)) {
       if (t.first) load_state(a.s0 ? a.s0 + ((int64_t)t.seq * a.HV + hv) * sz : nullptr);
       block_barrier();
-      for (int i = 0; i < t.rows; ++i) {
-        const int64_t row = t.t0 + i;
-        if (tid < XC) Xs[i * LDX + tid] = tid % PP < w.width ? x[row * a.ldx + (int64_t)(tid / PP) * V + tid % PP] : from_f32<T>(0.f);
-        if (tid < NP) Bs[i * LDB + tid] = tid < K ? b[row * a.ldb + tid] : from_f32<T>(0.f);
-        if (OUT && tid < NP) Cs[i * LDC + tid] = tid < K ? c[row * a.ldc + tid] : from_f32<T>(0.f);
-      }
+      // rows of `width` elements, n of them for every token, to LDS
+      auto stage = [&](lds<T>* dst, int ldd, const T* src, int64_t ld, auto n, int width) {
+        constexpr int kCols = decltype(n)::value;
+        const int e = tid % kCols;
+        if (e % kCols < width)
+#pragma unroll 8
+          for (int i = tid / kCols; i < t.rows; i += kThreads / kCols) dst[i * ldd + e] = src[(t.t0 + i) * ld + e];
+        else
+          for (int i = tid / kCols; i < t.rows; i += kThreads / kCols) dst[i * ldd + e] = from_f32<T>(0.f);
+      };
+      for (int h = 0; h < HB; ++h) stage(Xs + h * PP, LDX, x + (int64_t)h * V, a.ldx, std::integral_constant<int, PP>{}, w.width);
+      stage(Bs, LDB, b, a.ldb, std::integral_constant<int, NP>{}, K);
+      if constexpr (OUT) stage(Cs, LDC, c, a.ldc, std::integral_constant<int, NP>{}, K);
       if (tid < t.rows)
         for (int h = 0; h < HB; ++h) {
           float e, q;
@@ -385,16 +398,22 @@ __device__ __attribute__((noinline)) void by_token(arg_words args, int hblocks, 
         const float g = dec[head].eg[i], decay = decay_of(g), xv = to_f32(Xs[i * LDX + col]), dx = dec[head].w[i] * xv;
         float sum = 0.f;
         gsum += g;
-        int left = K - k;  // rows of the state from this thread's first one on
+        int left = K - k * R;  // rows of the state from this thread's first one on
         asm volatile("" : "+v"(left));  // compared anew for every token: masks would fill the registers
-        const T* bi = Bs + i * LDB + k;
-        const T* ci = Cs + i * LDC + k;
+        const lds<T>* bi = Bs + i * LDB + k * R;
+        const lds<T>* ci = Cs + (OUT ? i * LDC + k * R : 0);
+        typedef T t4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float xr = SPLIT * r < left ? dx : 0.f;
-          s[r] = decay * s[r] + to_f32(bi[SPLIT * r]) * xr;
-          if constexpr (OUT) sum += s[r] * to_f32(ci[SPLIT * r]);
-          if (r % 4 == 3) asm volatile("" : "+v"(left)::"memory");  // few registers rather than speed
+        for (int r = 0; r < R; r += 4) {
+          const t4 b4 = *(const lds<t4>*)(bi + r);
+          const t4 c4 = *(const lds<t4>*)(ci + (OUT ? r : 0));
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float xr = r + u < left ? dx : 0.f;  // rows behind K, which b and c do not have, stay zero
+            s[r + u] = decay * s[r + u] + to_f32(b4[u]) * xr;
+            if constexpr (OUT) sum += s[r + u] * to_f32(c4[u]);
+          }
+          if (r % 8 == 4) asm volatile("" : "+v"(left)::"memory");  // few registers rather than speed
         }
         if constexpr (OUT) {
 #pragma unroll
@@ -861,7 +880,8 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_kernel(SsmArgs a, int hbl
   if (__builtin_amdgcn_readfirstlane(s_odd[0] | s_odd[1] | s_odd[2] | s_odd[3]) != 0) {
     __builtin_amdgcn_s_waitcnt(0);  // what by_token() writes over is written
     by_token<T, NP, PP, HB, OUT, LDX, LDB, LDC>((arg_words)__builtin_amdgcn_kernarg_segment_ptr(), hblocks, blockIdx.x,
-                                                threadIdx.x, Xs, Bs, Cs, s_dec[0], s_odd);
+                                                threadIdx.x, (lds<T>*)Xs, (lds<T>*)Bs, (lds<T>*)Cs,
+                                                (lds<Decay>*)s_dec[0], (lds<int>*)s_odd);
   }
 }
 
