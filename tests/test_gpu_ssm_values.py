@@ -215,3 +215,36 @@ def test_x_near_the_largest_float(dtype):
     d["c"] *= 2.0 ** -20
     d["D"] *= 2.0 ** -20
     _check(d, lengths, *_fwd(d, cu), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_token_by_token_repeats_on_slices_and_in_a_graph(dtype):
+    """The way that sequences with an odd x go: bit for bit the same on slices of a wide activation at
+    any alignment, without the optional inputs, on a side stream and in a graph."""
+    lengths = [700, 33, 300]
+    d, cu = _make(lengths, 4, 2, 64, 40, DT[dtype], seed=81, init=False, skip=False, bias=False, pad=3)
+    for t, h, p in ((40, 0, 39), (650, 3, 0), (733, 1, 7)):
+        d["x"][t, h, p] = INF if h else NAN
+    plain = {k: v if v is None else v.contiguous() for k, v in d.items()}
+    ref = [t.clone() for t in _fwd(plain, cu)]
+    assert bool(ref[0][0].isfinite().all()) and not bool(ref[1][0].isfinite().all())
+
+    def same(got):
+        return all(torch.equal(a.nan_to_num(nan=12345.0), b.nan_to_num(nan=12345.0)) for a, b in zip(got, ref))
+
+    assert same(_fwd(plain, cu)) and same(_fwd(d, cu))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = _fwd(d, cu)
+    side.synchronize()
+    assert same(got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _fwd(d, cu)
+    for _ in range(3):
+        for t in got:
+            t.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(got) and same(_fwd(d, cu))
