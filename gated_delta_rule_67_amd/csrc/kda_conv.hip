@@ -335,7 +335,6 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a) {
             sum[e] = o;
           }
           if (a.dfinal) {  // these rows are the final state's
-           
             const vec_t fv = *reinterpret_cast<const vec_t*>(
                 static_cast<const T*>(a.dfinal) + ((int64_t)seq * (W - 1) + j) * a.D + col);
 #pragma unroll
@@ -408,8 +407,9 @@ __global__ __launch_bounds__(kThreads) void reduce_kernel(const float* __restric
 
 // One token per request: the state's rows (the W - 1 inputs before it) and the token give y, and
 // the state moves on by one row in place. slots: as kda_recurrent_step_slots. A lane takes its
-// channels of REQ requests, so that their taps (five times the bytes of a row) are read once for
-// all of them and all their loads are in flight together.
+// channels of REQ requests, so that their taps (float32: with W = 4 and a bias five times the bytes
+// of a float32 row, ten times those of a bf16 row) are read once for all of them and all their loads
+// are in flight together.
 constexpr int kStepThreads = 64;
 
 template <typename T, int VEC, int W, int REQ>
@@ -496,7 +496,7 @@ constexpr int kFwdBlocks = 4096, kBwdBlocks = 3 * 256;
 // The backward holds 3 W - 1 floats a channel, so four channels a lane, not eight of bf16, and the
 // resulting three workgroups a CU are launched in one round: 238 us at 32768 x 6144, bf16 (5.1
 // TB/s), against 284 with eight channels and 277 with 1024 workgroups (a third of them in a second
-// round). The forward (162 us, 5.0 TB/s) is fastest with several rounds of eight channels a lane.
+// round). The forward (160 us, 5.0 TB/s) is fastest with several rounds of eight channels a lane.
 constexpr int kBwdVec = 4;
 
 template <typename T, int VEC, int W>

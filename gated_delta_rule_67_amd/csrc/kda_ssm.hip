@@ -22,13 +22,17 @@
 // float32 inputs take the same steps with tiles of 32 tokens, 16x16x4 float32 products and nothing
 // rounded.
 //
-// Measured at 4 x 8192 tokens, 64 heads x 64, K = 128, 8 pairs, bf16: 356 us for 684 MB, 114 us at
-// a copy's rate; 258 us without the boundary pass and the composition (traced: 251 pass with
-// outputs, 118 without, 15 composition). A tile of two heads takes a workgroup about 14,300 cycles
-// beside a second one on its CU: 2,050 for M, 3,500 for y, 4,100 for the state, 2,000 until the next
-// tile's loads are issued, 760 for LDS stores. No single pipeline is full (VALU 43%, matrix cores
-// 31%, LDS 35% of the cycles). Tiles of 32 tokens (385 us), 256 or 768 workgroups (466, 405) were
-// slower, eight waves of 16 columns the same.
+// Such products multiply every x of a tile, also with zeros of M, so a sequence with an x that is not
+// finite goes another way (by_token()). The passes find that out from the sum of the squares of all x,
+// 16 dot products a lane and tile: 355 -> 358 us at the sizes below.
+//
+// Measured at 4 x 8192 tokens, 64 heads x 64, K = 128, 8 pairs, bf16: 358 us for 684 MB, 114 us at
+// a copy's rate (traced: 254 pass with outputs, 117 without, 15 composition). Before the squares a tile
+// of two heads took a workgroup about 14,300 cycles beside a second one on its CU: 2,050 for M, 3,500
+// for y, 4,100 for the state, 2,000 until the next tile's loads are issued, 760 for LDS stores. No
+// single pipeline is full (VALU 44%, matrix cores 31%, LDS 34% of the cycles). Tiles of 32 tokens were
+// 5% slower, 256 or 768 workgroups 29% and 12%, each against the kernel of its day; eight waves of 16
+// columns were the same. float32 at these sizes: 1,365 us (50 TFLOP/s of the recurrence's operations).
 #include <type_traits>
 
 #include "kda_ssm.h"
@@ -298,7 +302,8 @@ __device__ __forceinline__ bool odd_value(float v) { return !(fabsf(v) < 0x1p64f
 // tokens in front of it, and an infinity less its own first term is NaN in the state. Runs behind the
 // products and writes over what they left in these sequences. It is rare, so it is written for few
 // registers, and not inlined, so that the products' loop is compiled as if it were not there (inlined:
-// 378 us instead of 366 at 4 x 8192 tokens, 64 heads x 64, K = 128).
+// 378 us instead of 366 at 4 x 8192 tokens, 64 heads x 64, K = 128). One NaN there: 5.9 ms, 4096 tokens
+// in each of the two passes.
 // SPLIT threads share a column, each has R rows of the state. args: the kernel's SsmArgs.
 typedef const __attribute__((address_space(4))) unsigned* arg_words;
 template <typename X> using lds = __attribute__((address_space(3))) X;

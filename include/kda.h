@@ -516,9 +516,17 @@ int kda_conv_step(const void* x, int64_t x_stride, const float* weight, const fl
  *
  * The token axis is cut into equal segments that run side by side; a scan of the states at their
  * boundaries joins them (as in kda_chunk_fwd_segmented). Results are bitwise reproducible.
- * An x that is not finite reaches the outputs that the recurrence gives it to, as an infinity or a
- * NaN, and no others; its sequence is then taken token by token (more slowly) in that segment.
- * No decay is quite 0: an infinite state stays infinite (in kda_ssm_step too).
+ * Accuracy: the states keep float32 accuracy in either type. bf16: two of y's terms are rounded to
+ * bf16 (by 2^-8 at most) before they are multiplied, the products c_i . b_j with their decay and the
+ * state that c reads, and y once more as it is stored. float32, and kda_ssm_step in either type:
+ * float32 throughout. The softplus and the decays come from the hardware's exponential and logarithm
+ * (a relative error of about 1e-6).
+ * Values that are not finite reach the outputs that the recurrence gives them to, and no others (no
+ * token in front of theirs, no other sequence). From x and from states on, infinities and NaN are
+ * those of the recurrence; behind a b, c or dt that is not finite, NaN may stand for an infinity.
+ * Sequences with an x that is not finite, or 2^64 and more, are taken token by token in its segment
+ * (0.7 us a token and pass). No decay is quite 0: an infinite state stays infinite, here and in
+ * kda_ssm_step.
  * Constraints: N >= 1, T >= 0, HV % H == 0 (else KDA_ERR_INVALID); K, V <= 128, HV <= 2^16,
  * N <= 2^20, T <= 2^30, and under 2^24 workgroups (about one per 64 columns of a sequence's or
  * segment's heads) (else KDA_ERR_UNSUPPORTED). Nothing is allocated.
