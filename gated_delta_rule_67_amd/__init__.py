@@ -27,6 +27,12 @@ Entry points (same names as the C ABI):
   head, for prompts and for one token on a pool of states
 * ``kda_slots_copy`` / ``kda_slots_compact``: copies, forks, clears and compaction of the slots of
   many state pools at once
+* ``kda_prenorm_fwd`` / ``kda_prenorm_bwd`` and ``kda_postnorm_fwd`` / ``kda_postnorm_bwd``: the norms
+  in front of and behind a block, with its gate, residual and residual scale
+* ``kda_glr_fwd`` / ``kda_glr_bwd`` / ``kda_glr_step``: the gated linear recurrence with one state
+  per channel, its backward, and one token on a pool of states
+* ``kda_checkpoint_pack`` / ``kda_checkpoint_unpack``: activations kept in 8 bits, which these
+  backward passes read as they are
 * ``kda_chunk_fwd_noalloc(q, k, v, g, beta, o, final_state=None, ...)``: the prefill into
   caller-provided outputs, with the workspace taken from the library's fixed per-device
   scratch array (no device allocation anywhere in the call)
@@ -47,14 +53,18 @@ __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_varlen", "kda_chunk_bwd",
            "kda_chunk_fwd_gated", "kda_recurrent_step_gated", "kda_chunk_fwd_segmented",
            "kda_chunk_fwd_noalloc",
            "kda_conv_fwd", "kda_conv_bwd", "kda_conv_step", "kda_slots_copy",
-           "kda_slots_compact", "kda_ssm_chunk_fwd", "kda_ssm_step", "NOALLOC_SCRATCH_BYTES", "library", "library_path", "status_string",
+           "kda_slots_compact", "kda_ssm_chunk_fwd", "kda_ssm_step",
+           "kda_prenorm_fwd", "kda_prenorm_bwd", "kda_postnorm_fwd", "kda_postnorm_bwd",
+           "kda_checkpoint_pack", "kda_checkpoint_unpack", "kda_glr_fwd", "kda_glr_bwd", "kda_glr_step",
+           "NOALLOC_SCRATCH_BYTES", "library", "library_path", "status_string",
            "KDA_OK", "KDA_ERR_INVALID", "KDA_ERR_UNSUPPORTED", "KDA_ERR_HIP", "KDA_ERR_SCRATCH",
            "KDA_FLAG_QK_L2NORM", "KDA_FLAG_BETA_SIGMOID"]
 
 KDA_OK, KDA_ERR_INVALID, KDA_ERR_UNSUPPORTED, KDA_ERR_HIP, KDA_ERR_SCRATCH = 0, -1, -2, -3, -4
 NOALLOC_SCRATCH_BYTES = 64 << 20  # KDA_NOALLOC_SCRATCH_BYTES
 KDA_FLAG_QK_L2NORM, KDA_FLAG_BETA_SIGMOID = 1, 2
-KDA_CONV_SILU, KDA_ZERO_REST = 1, 2
+KDA_CONV_SILU, KDA_ZERO_REST, KDA_GLR_NORMALISE, KDA_NORM_SILU = 1, 2, 4, 1
+GLR_BLOCK = 64  # tokens between the states that kda_glr_fwd keeps for kda_glr_bwd
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 library_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
@@ -146,6 +156,31 @@ def library():
     lib.kda_slots_compact_workspace_size.restype = sz
     lib.kda_slots_compact.argtypes = [vp] * 2 + [i, i] + [vp] * 4 + [sz, vp]
     lib.kda_slots_compact.restype = i
+    u = ctypes.c_uint
+    rows = [i64, i, i, f]  # T, G, D, eps
+    lib.kda_prenorm_fwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp] + rows + [i, vp]
+    lib.kda_postnorm_fwd.argtypes = [vp, i64, vp, vp, i64, vp, i64, vp, vp] + rows + [u, i, vp]
+    lib.kda_norm_bwd_workspace_size.argtypes = [i64, i, i]
+    lib.kda_norm_bwd_workspace_size.restype = sz
+    kept = [vp, vp, i64]   # a tensor or codes, scales, stride
+    lib.kda_prenorm_bwd.argtypes = (kept + [vp, vp, i64, vp, i64] + kept + [vp] * 5 + rows
+                                    + [i, vp, sz, vp])
+    lib.kda_postnorm_bwd.argtypes = (kept + [vp] + kept + [vp, i64] + [vp] * 5 + rows
+                                     + [u, i, vp, sz, vp])
+    lib.kda_checkpoint_pack.argtypes = [vp, i64, vp, vp, i64, i, i, vp]
+    lib.kda_checkpoint_unpack.argtypes = [vp, vp, vp, i64, i, i, vp]
+    lib.kda_glr_fwd_workspace_size.argtypes = [i, i]
+    lib.kda_glr_fwd_workspace_size.restype = sz
+    lib.kda_glr_bwd_workspace_size.argtypes = [i, i, i]
+    lib.kda_glr_bwd_workspace_size.restype = sz
+    lib.kda_glr_fwd.argtypes = ([vp, i64, vp, i64, vp, vp, vp, i64, vp, vp, i, vp, vp, vp, i, i, u, i]
+                                + [vp, sz, vp])
+    lib.kda_glr_bwd.argtypes = (kept + kept + [vp, vp] + kept + [vp, vp, i, vp, i64] + [vp] * 8
+                                + [i, i, u, i, vp, sz, vp])
+    lib.kda_glr_step.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, vp, vp, i, vp, i, i, u, i, vp]
+    for name in ("prenorm_fwd", "prenorm_bwd", "postnorm_fwd", "postnorm_bwd", "checkpoint_pack",
+                 "checkpoint_unpack", "glr_fwd", "glr_bwd", "glr_step"):
+        getattr(lib, "kda_" + name).restype = i
     lib.kda_version.argtypes = []
     lib.kda_version.restype = ctypes.c_char_p
     _lib = lib
@@ -910,6 +945,261 @@ def kda_slots_compact(pools, live):
     _call(index, lib.kda_slots_compact, base, size, n, num_slots, live.data_ptr(),
           new_slot.data_ptr(), count.data_ptr(), buf.data_ptr(), ws_bytes)
     return new_slot, count
+
+
+def _checkpoint(name, t, shape, index):
+    """(codes, scales) must be a checkpoint, as kda_checkpoint_pack gives it, of a tensor of this shape."""
+    codes, scales = t
+    _require(shape[-1] % 32 == 0, f"{name}: checkpoints have a multiple of 32 channels")
+    if codes.dtype is not torch.float8_e4m3fn or codes.shape != shape or codes.get_device() != index or not codes.is_contiguous():
+        raise ValueError(f"{name}: codes must be a contiguous float8_e4m3fn tensor {list(shape)} on the GPU of the gradients")
+    if (scales.dtype is not torch.uint8 or scales.shape != shape[:-1] + (shape[-1] // 32,)
+            or scales.get_device() != index or not scales.is_contiguous()):
+        raise ValueError(f"{name}: scales must be a contiguous uint8 tensor {list(shape[:-1])} + [channels / 32]")
+    return codes.data_ptr(), scales.data_ptr()
+
+
+def _row_layout(like, named):
+    """(tokens, rows a token, {name: elements between tokens}) of the tensors (or None) in `named`,
+    each shaped and typed like `like` and on its GPU: rows are their last dimension, and a tensor may
+    be a slice of a wider activation, of whole rows or of the rows of a token."""
+    shape, dtype, index = like.shape, like.dtype, like.get_device()
+    given = [(n, t) for n, t in named if t is not None]
+    dense = True
+    for n, t in given:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+            raise ValueError(f"{n} must be {list(shape)}, {dtype}, on the GPU of the others")
+        dense = dense and t.is_contiguous()
+    D = shape[-1]
+    rows = like.numel() // D if D else 0
+    if dense:
+        return rows, 1, {n: D for n, _ in given}
+    lead = len(shape) - 1
+    try:
+        return rows, 1, {n: _token_stride(n, t, lead, D) for n, t in given}
+    except ValueError:
+        if lead < 2:
+            raise
+        G = shape[-2]
+        return rows // G, G, {n: _token_stride(n, t, lead - 1, G * D) for n, t in given}
+
+
+def _norm_args(x, weight, scale):
+    index, code = _gpu(x)
+    _require(x.dim() >= 1 and x.shape[-1] >= 1, "x must have at least one column")
+    D = x.shape[-1]
+    _dense("weight", weight, (D,), torch.float32, index)
+    _dense("scale", scale, (D,), torch.float32, index)
+    return index, code, D
+
+
+def kda_prenorm_fwd(x, weight, residual=None, scale=None, eps=1e-6):
+    """The norm in front of a block, joined with the residual addition behind the block before it:
+    h = residual + scale * x, y = weight * h / sqrt(mean(h^2) + eps) over the last dimension. x
+    [..., D] (float32 or bf16; slices of a wider activation allowed); weight [D] float32; residual
+    like x, or None: zeros; scale [D] float32, or None: ones. Returns (y, h), shaped and typed like
+    x; h is x itself where neither residual nor scale is given."""
+    index, code, D = _norm_args(x, weight, scale)
+    T, G, ld = _row_layout(x, (("x", x), ("residual", residual)))
+    y = _fresh(x)
+    h = None if residual is None and scale is None else _fresh(x)
+    _call(index, library().kda_prenorm_fwd, x.data_ptr(), ld["x"], _addr(residual), ld.get("residual", 0),
+          weight.data_ptr(), _addr(scale), y.data_ptr(), _addr(h), T, G, D, eps, code)
+    return y, x if h is None else h
+
+
+def kda_postnorm_fwd(x, weight, gate=None, residual=None, scale=None, activation="sigmoid", eps=1e-6):
+    """The norm behind a block, under its gate and into the residual:
+    y = residual + scale * (weight * act(gate) * x / sqrt(mean(x^2) + eps)) over the last dimension,
+    act the sigmoid or "silu". x, gate and residual [..., D] (gate None: no factor; residual None:
+    zeros); weight, scale [D] float32 (scale None: ones). Returns y like x."""
+    index, code, D = _norm_args(x, weight, scale)
+    _require(activation in ("sigmoid", "silu"), "activation must be 'sigmoid' or 'silu'")
+    T, G, ld = _row_layout(x, (("x", x), ("gate", gate), ("residual", residual)))
+    y = _fresh(x)
+    _call(index, library().kda_postnorm_fwd, x.data_ptr(), ld["x"], weight.data_ptr(), _addr(gate), ld.get("gate", 0),
+          _addr(residual), ld.get("residual", 0), _addr(scale), y.data_ptr(), T, G, D, eps,
+          KDA_NORM_SILU if activation == "silu" else 0, code)
+    return y
+
+
+def _kept(name, t, like, index):
+    """(address, scales' address) of a checkpoint, or (None, None): the tensor itself is meant."""
+    return _checkpoint(name, t, like.shape, index) if isinstance(t, (tuple, list)) else (None, None)
+
+
+def _norm_sums(T, G, D, weight, scale):
+    """Outputs and workspace of the sums over rows."""
+    n = library().kda_norm_bwd_workspace_size(T, G, D)
+    ws = torch.empty(n, dtype=torch.uint8, device=weight.device) if n else None
+    return torch.empty_like(weight), None if scale is None else torch.empty_like(scale), ws, n
+
+
+def kda_prenorm_bwd(h, weight, dy, dh=None, x=None, scale=None, eps=1e-6):
+    """Gradients of <y, dy> + <h, dh> for kda_prenorm_fwd's inputs. h: as it returned it; x, needed
+    where scale is given: its input; both may be checkpoints (codes, scales). dh None: zeros. Returns
+    (dresidual, dx, dweight [D], dscale [D]); dx is dresidual, and dscale None, without a scale."""
+    index, code, D = _norm_args(dy, weight, scale)
+    _require(scale is None or x is not None, "a scale's gradient needs x")
+    x = None if scale is None else x
+    (hp, hs), (xp, xs) = _kept("h", h, dy, index), _kept("x", x, dy, index)
+    _require(x is None or (hs is None) == (xs is None), "h and x must both be checkpoints, or neither")
+    T, G, ld = _row_layout(dy, (("dy", dy), ("dh", dh), ("h", h if hs is None else None),
+                                ("x", x if xs is None else None)))
+    dweight, dscale, ws, n = _norm_sums(T, G, D, weight, scale)
+    dres = _fresh(dy)
+    dx = dres if scale is None else _fresh(dy)
+    _call(index, library().kda_prenorm_bwd, hp if hs is not None else h.data_ptr(), hs, ld.get("h", 0),
+          weight.data_ptr(), dy.data_ptr(), ld["dy"], _addr(dh), ld.get("dh", 0), xp if xs is not None else _addr(x), xs,
+          ld.get("x", 0), _addr(scale), dres.data_ptr(), dx.data_ptr(), dweight.data_ptr(), _addr(dscale), T, G, D,
+          eps, code, _addr(ws), n)
+    return dres, dx, dweight, dscale
+
+
+def kda_postnorm_bwd(x, weight, dy, gate=None, scale=None, activation="sigmoid", eps=1e-6):
+    """Gradients of <y, dy> for kda_postnorm_fwd's inputs (the residual's is dy as it is). x and gate
+    may be checkpoints (codes, scales). Returns (dx, dgate, dweight [D], dscale [D]); dgate and dscale
+    are None where gate and scale are."""
+    index, code, D = _norm_args(dy, weight, scale)
+    _require(activation in ("sigmoid", "silu"), "activation must be 'sigmoid' or 'silu'")
+    (xp, xs), (gp, gs) = _kept("x", x, dy, index), _kept("gate", gate, dy, index)
+    _require(gate is None or (xs is None) == (gs is None), "x and gate must both be checkpoints, or neither")
+    T, G, ld = _row_layout(dy, (("dy", dy), ("x", x if xs is None else None),
+                                ("gate", gate if gs is None else None)))
+    dweight, dscale, ws, n = _norm_sums(T, G, D, weight, scale)
+    dx = _fresh(dy)
+    dgate = None if gate is None else _fresh(dy)
+    _call(index, library().kda_postnorm_bwd, xp if xs is not None else x.data_ptr(), xs, ld.get("x", 0),
+          weight.data_ptr(), gp if gs is not None else _addr(gate), gs, ld.get("gate", 0), dy.data_ptr(), ld["dy"],
+          _addr(scale), dx.data_ptr(), _addr(dgate), dweight.data_ptr(), _addr(dscale), T, G, D, eps,
+          KDA_NORM_SILU if activation == "silu" else 0, code, _addr(ws), n)
+    return dx, dgate, dweight, dscale
+
+
+def kda_checkpoint_pack(x):
+    """x [..., D] (float32 or bf16, D a multiple of 32; a slice of a wider activation allowed) in 8
+    bits: (codes float8_e4m3fn [..., D], scales uint8 [..., D / 32]). 32 neighbours share the power of
+    two 2^(scale - 127), the smallest that brings the largest finite magnitude to 448 at most."""
+    index, code = _gpu(x)
+    _require(x.dim() >= 1 and x.shape[-1] % 32 == 0 and x.shape[-1] > 0, "x must have a multiple of 32 channels")
+    T, G, ld = _row_layout(x, (("x", x),))
+    codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    scales = torch.empty(x.shape[:-1] + (x.shape[-1] // 32,), dtype=torch.uint8, device=x.device)
+    _call(index, library().kda_checkpoint_pack, x.data_ptr(), ld["x"], codes.data_ptr(), scales.data_ptr(), T,
+          G * x.shape[-1], code)
+    return codes, scales
+
+
+def kda_checkpoint_unpack(codes, scales, dtype=torch.bfloat16):
+    """The values that a checkpoint of kda_checkpoint_pack stands for, as float32 or bf16 [..., D]."""
+    index = codes.get_device()
+    _require(index >= 0, "inputs must be on a GPU")
+    _require(codes.dim() >= 1 and codes.shape[-1] > 0, "codes must have at least one channel")
+    _require(dtype in _DTYPE, f"unsupported dtype {dtype}")
+    _checkpoint("checkpoint", (codes, scales), codes.shape, index)
+    x = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+    D = codes.shape[-1]
+    _call(index, library().kda_checkpoint_unpack, codes.data_ptr(), scales.data_ptr(), x.data_ptr(),
+          codes.numel() // D, D, _DTYPE[dtype])
+    return x
+
+
+def _glr_params(D, A_log, dt_bias, index):
+    _require(D >= 1, "x must have at least one channel")
+    _dense("A_log", A_log, (D,), torch.float32, index)
+    _dense("dt_bias", dt_bias, (D,), torch.float32, index)
+
+
+def kda_glr_fwd(x, gate_x, A_log, dt_bias=None, in_gate=None, initial_state=None, cu_seqlens=None, normalise=True,
+                output_final_state=True, output_block_states=False):
+    """Gated linear recurrence with one state per channel: with a_t = exp(-exp(A_log) softplus(gate_x_t
+    + dt_bias)), h_t = a_t h_{t-1} + w_t sigmoid(in_gate_t) x_t and y_t = h_t, where w_t is
+    sqrt(1 - a_t^2), or 1 with normalise=False. x, gate_x, in_gate [B,T,D] (float32 or bf16; slices of a
+    wider activation allowed; in_gate None: factor 1), or packed [T,D] / [1,T,D] with cu_seqlens int32
+    [N+1]; A_log, dt_bias [D] float32; initial_state [N,D] float32. Returns (y like x, final_state [N,D]
+    float32 or None); y rows in no packed sequence are zero. output_block_states: also returns the states
+    [ceil(tokens / 64), D] that kda_glr_bwd takes, so that it need not compute them again."""
+    index, code = _gpu(x)
+    lead, N, T = _sequences(x, cu_seqlens, 3, index)
+    D = x.shape[-1]
+    _glr_params(D, A_log, dt_bias, index)
+    ldx = _token_stride("x", x, lead, D)
+    ldr = _tokens("gate_x", gate_x, x.shape, x, index, lead, D)
+    ldi = 0 if in_gate is None else _tokens("in_gate", in_gate, x.shape, x, index, lead, D)
+    _dense("initial_state", initial_state, (N, D), torch.float32, index)
+    lib = library()
+    y = _fresh(x)
+    final = torch.empty((N, D), dtype=torch.float32, device=x.device) if output_final_state else None
+    states = (torch.empty(((T + GLR_BLOCK - 1) // GLR_BLOCK, D), dtype=torch.float32, device=x.device)
+              if output_block_states else None)
+    n = lib.kda_glr_fwd_workspace_size(T, D)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+    _call(index, lib.kda_glr_fwd, x.data_ptr(), ldx, gate_x.data_ptr(), ldr, A_log.data_ptr(), _addr(dt_bias),
+          _addr(in_gate), ldi, _addr(initial_state), _addr(cu_seqlens), N, _addr(final), y.data_ptr(), _addr(states), T, D,
+          KDA_ZERO_REST | (KDA_GLR_NORMALISE if normalise else 0), code, _addr(ws), n)
+    return (y, final, states) if output_block_states else (y, final)
+
+
+def kda_glr_bwd(x, gate_x, A_log, dy, dt_bias=None, in_gate=None, initial_state=None, dfinal_state=None,
+                cu_seqlens=None, normalise=True, block_states=None):
+    """Gradients of <y, dy> + <final_state, dfinal_state> for kda_glr_fwd's inputs. x, gate_x and in_gate
+    may be checkpoints (codes, scales), all of them or none. block_states: as kda_glr_fwd returned them for
+    these inputs, or None: they are computed again. Returns (dx, dgate_x, din_gate, dA_log [D], ddt_bias
+    [D], dinitial_state [N,D]); din_gate, ddt_bias and dinitial_state are None where their inputs are, and
+    rows in no packed sequence are zero."""
+    index, code = _gpu(dy)
+    lead, N, T = _sequences(dy, cu_seqlens, 3, index)
+    D = dy.shape[-1]
+    _glr_params(D, A_log, dt_bias, index)
+    args, packed = [], []
+    for name, t in (("x", x), ("gate_x", gate_x), ("in_gate", in_gate)):
+        if t is None:
+            args.append((None, None, 0))
+        elif isinstance(t, (tuple, list)):
+            args.append(_checkpoint(name, t, dy.shape, index) + (D,))
+            packed.append(True)
+        else:
+            args.append((t.data_ptr(), None, _tokens(name, t, dy.shape, dy, index, lead, D)))
+            packed.append(False)
+    _require(len(set(packed)) == 1, "x, gate_x and in_gate must all be checkpoints, or none of them")
+    lddy = _token_stride("dy", dy, lead, D)
+    _dense("initial_state", initial_state, (N, D), torch.float32, index)
+    _dense("dfinal_state", dfinal_state, (N, D), torch.float32, index)
+    _dense("block_states", block_states, ((T + GLR_BLOCK - 1) // GLR_BLOCK, D), torch.float32, index)
+    lib = library()
+    dx, dr = _fresh(dy), _fresh(dy)
+    din = None if in_gate is None else _fresh(dy)
+    dA = torch.empty_like(A_log)
+    db = None if dt_bias is None else torch.empty_like(dt_bias)
+    dinit = None if initial_state is None else torch.empty_like(initial_state)
+    n = lib.kda_glr_bwd_workspace_size(T, D, 0 if block_states is None else 1)
+    ws = torch.empty(n, dtype=torch.uint8, device=dy.device) if n else None
+    _call(index, lib.kda_glr_bwd, *args[0], *args[1], A_log.data_ptr(), _addr(dt_bias), *args[2], _addr(initial_state),
+          _addr(cu_seqlens), N, dy.data_ptr(), lddy, _addr(dfinal_state), _addr(block_states), dx.data_ptr(),
+          dr.data_ptr(), _addr(din), dA.data_ptr(), _addr(db), _addr(dinit), T, D,
+          KDA_ZERO_REST | (KDA_GLR_NORMALISE if normalise else 0), code, _addr(ws), n)
+    return dx, dr, din, dA, db, dinit
+
+
+def kda_glr_step(x, gate_x, A_log, state_pool, dt_bias=None, in_gate=None, slots=None, normalise=True):
+    """One token of kda_glr_fwd per request. x, gate_x, in_gate [B,D]; state_pool [num_slots,D] float32,
+    updated in place; slots int32 [B] (a slot outside [0, num_slots) gives y = 0 and no update), or
+    None: request n uses slot n. Returns y [B,D]."""
+    index, code = _gpu(x)
+    _require(x.dim() == 2 and x.numel() > 0 and state_pool.dim() == 2, "x must be [B, D], state_pool [num_slots, D]")
+    B, D = x.shape
+    _glr_params(D, A_log, dt_bias, index)
+    ldx = _token_stride("x", x, 1, D)
+    ldr = _tokens("gate_x", gate_x, x.shape, x, index, 1, D)
+    ldi = 0 if in_gate is None else _tokens("in_gate", in_gate, x.shape, x, index, 1, D)
+    num_slots = state_pool.shape[0]
+    _dense("state_pool", state_pool, (num_slots, D), torch.float32, index)
+    at = _slots(slots, B, num_slots, index)
+    y = _fresh(x)
+    _call(index, library().kda_glr_step, x.data_ptr(), ldx, gate_x.data_ptr(), ldr, A_log.data_ptr(), _addr(dt_bias),
+          _addr(in_gate), ldi, state_pool.data_ptr(), at, num_slots, y.data_ptr(), B, D,
+          KDA_GLR_NORMALISE if normalise else 0, code)
+    return y
 
 
 def stream_copy(src, dst):

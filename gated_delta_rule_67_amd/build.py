@@ -19,7 +19,8 @@ OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_api.hip", "kda_decode.hip", "kda_prefill.hip", "kda_chunk_bf16.hip",
            "kda_chunk_wy.hip", "kda_chunk_bwd.hip", "kda_gate.hip", "kda_stream.hip",
-           "kda_conv.hip", "kda_slots.hip", "kda_ssm.hip", "kda_ssm_step.hip"]
+           "kda_conv.hip", "kda_slots.hip", "kda_ssm.hip", "kda_ssm_step.hip",
+           "kda_norm.hip", "kda_norm_bwd.hip", "kda_checkpoint.hip", "kda_glr.hip", "kda_glr_bwd.hip"]
 
 
 def hipcc():

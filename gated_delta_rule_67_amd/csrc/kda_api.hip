@@ -1,5 +1,6 @@
 // C ABI of the KDA library: argument validation, then kernel dispatch.
 // Nothing here allocates device memory or synchronises.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -7,6 +8,8 @@
 
 #include "../../include/kda.h"
 #include "kda_device.h"
+#include "kda_glr.h"
+#include "kda_norm.h"
 #include "kda_ssm.h"
 
 namespace kda {
@@ -55,6 +58,10 @@ size_t slots_compact_workspace_bytes(int nslots);
 hipError_t launch_slots_compact(void* const* pools, const size_t* slot_bytes, int npools, int nslots,
                                 const uint8_t* live, int* new_slot, int* count, void* workspace,
                                 hipStream_t stream);
+hipError_t launch_checkpoint_pack(const void* x, int64_t ldx, uint8_t* codes, uint8_t* scales, int64_t rows, int D,
+                                  bool bf, hipStream_t stream);
+hipError_t launch_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, void* x, int64_t rows, int D,
+                                    bool bf, hipStream_t stream);
 }  // namespace kda
 
 namespace {
@@ -700,6 +707,234 @@ int kda_slots_compact(void* const* pools, const size_t* slot_bytes, int num_pool
   const hipError_t e = kda::launch_slots_compact(pools, slot_bytes, num_pools, num_slots, live, new_slot,
                                                  count, workspace, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+// ---- Norms around a block
+
+static bool valid_dtype(int dtype) { return dtype == KDA_DTYPE_F32 || dtype == KDA_DTYPE_BF16; }
+
+static int check_norm(int64_t T, int G, int D, float eps, int dtype) {
+  if (T < 0 || !positive(G) || !positive(D) || !valid_dtype(dtype)) return KDA_ERR_INVALID;
+  if (!(eps >= FLT_MIN) || !isfinite(eps)) return KDA_ERR_INVALID;
+  if (D > kda::kNormMaxDim || T > kMaxTokens || T * G > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+// A tensor of T tokens of `width` elements that a call reads, or its checkpoint (dense): false where its
+// tokens overlap.
+static bool source(kda::Source* s, const void* p, const void* scales, int64_t stride, int64_t T, int64_t width) {
+  *s = kda::Source{p, static_cast<const uint8_t*>(scales), !p ? 0 : T < 2 || scales ? width : stride};
+  return !p || s->ld >= width;
+}
+
+static int norm_status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
+
+int kda_prenorm_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                    const float* weight, const float* scale, void* y, void* h, int64_t T, int G, int D, float eps,
+                    int dtype, void* stream) {
+  const int rc = check_norm(T, G, D, eps, dtype);
+  if (rc != KDA_OK) return rc;
+  if (!weight || (T > 0 && (!x || !y))) return KDA_ERR_INVALID;
+  kda::NormArgs a{};
+  const int64_t width = (int64_t)G * D;
+  if (!source(&a.v, x, nullptr, x_stride, T, width) || !source(&a.other, residual, nullptr, residual_stride, T, width))
+    return KDA_ERR_INVALID;
+  a.rows = T * G, a.G = G, a.D = D, a.eps = eps, a.weight = weight, a.scale = scale, a.y = y, a.extra = h;
+  a.bf = dtype == KDA_DTYPE_BF16;
+  return norm_status(kda::launch_norm_fwd(a, false, static_cast<hipStream_t>(stream)));
+}
+
+int kda_postnorm_fwd(const void* x, int64_t x_stride, const float* weight, const void* gate, int64_t gate_stride,
+                     const void* residual, int64_t residual_stride, const float* scale, void* y, int64_t T, int G,
+                     int D, float eps, unsigned flags, int dtype, void* stream) {
+  const int rc = check_norm(T, G, D, eps, dtype);
+  if (rc != KDA_OK) return rc;
+  if (!weight || (T > 0 && (!x || !y)) || (flags & ~(unsigned)KDA_NORM_SILU)) return KDA_ERR_INVALID;
+  kda::NormArgs a{};
+  const int64_t width = (int64_t)G * D;
+  if (!source(&a.v, x, nullptr, x_stride, T, width) || !source(&a.gate, gate, nullptr, gate_stride, T, width) ||
+      !source(&a.other, residual, nullptr, residual_stride, T, width))
+    return KDA_ERR_INVALID;
+  a.rows = T * G, a.G = G, a.D = D, a.eps = eps, a.weight = weight, a.scale = scale, a.y = y;
+  a.silu = (flags & KDA_NORM_SILU) != 0, a.bf = dtype == KDA_DTYPE_BF16;
+  return norm_status(kda::launch_norm_fwd(a, true, static_cast<hipStream_t>(stream)));
+}
+
+size_t kda_norm_bwd_workspace_size(int64_t T, int G, int D) {
+  if (T < 1 || check_norm(T, G, D, 1.f, KDA_DTYPE_F32) != KDA_OK) return 0;
+  return kda::norm_bwd_workspace_bytes(T * G, D);
+}
+
+// What the backward norms share once their sources are set: the rest of the checks, and the launch.
+static int norm_bwd(kda::NormArgs* a, bool behind, bool packed_ok, int64_t T, int G, int D, float eps, int dtype,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (!packed_ok) return KDA_ERR_INVALID;
+  if (a->packed && D % kda::kScaleBlock != 0) return KDA_ERR_UNSUPPORTED;
+  a->rows = T * G, a->G = G, a->D = D, a->eps = eps, a->bf = dtype == KDA_DTYPE_BF16;
+  if (T > 0 && (a->dweight || a->dscale)) {
+    if (!workspace || workspace_bytes < kda_norm_bwd_workspace_size(T, G, D)) return KDA_ERR_INVALID;
+    a->part = static_cast<float*>(workspace);
+  }
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0) return KDA_ERR_INVALID;
+  return norm_status(kda::launch_norm_bwd(*a, behind, static_cast<hipStream_t>(stream)));
+}
+
+// Kept tensors are all checkpoints, or none (an absent one is either).
+static bool same_kind(const kda::Source& a, const kda::Source& b) { return !a.p || !b.p || !a.scales == !b.scales; }
+
+int kda_prenorm_bwd(const void* h, const void* h_scales, int64_t h_stride, const float* weight, const void* dy,
+                    int64_t dy_stride, const void* dh, int64_t dh_stride, const void* x, const void* x_scales,
+                    int64_t x_stride, const float* scale, void* dresidual, void* dx, float* dweight, float* dscale,
+                    int64_t T, int G, int D, float eps, int dtype, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  const int rc = check_norm(T, G, D, eps, dtype);
+  if (rc != KDA_OK) return rc;
+  if (!weight || (T > 0 && (!h || !dy || !dresidual))) return KDA_ERR_INVALID;
+  if (T > 0 && scale && (!x || !dx)) return KDA_ERR_INVALID;
+  kda::NormArgs a{};
+  const int64_t width = (int64_t)G * D;
+  if (!source(&a.v, h, h_scales, h_stride, T, width) || !source(&a.dy, dy, nullptr, dy_stride, T, width) ||
+      !source(&a.dh, dh, nullptr, dh_stride, T, width) ||
+      !source(&a.other, scale ? x : nullptr, x_scales, x_stride, T, width))
+    return KDA_ERR_INVALID;
+  a.weight = weight, a.scale = scale, a.y = dresidual, a.extra = scale ? dx : nullptr;
+  a.dweight = dweight, a.dscale = scale ? dscale : nullptr, a.packed = a.v.scales != nullptr;
+  return norm_bwd(&a, false, same_kind(a.v, a.other), T, G, D, eps, dtype, workspace, workspace_bytes, stream);
+}
+
+int kda_postnorm_bwd(const void* x, const void* x_scales, int64_t x_stride, const float* weight, const void* gate,
+                     const void* gate_scales, int64_t gate_stride, const void* dy, int64_t dy_stride,
+                     const float* scale, void* dx, void* dgate, float* dweight, float* dscale, int64_t T, int G, int D,
+                     float eps, unsigned flags, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_norm(T, G, D, eps, dtype);
+  if (rc != KDA_OK) return rc;
+  if (!weight || (T > 0 && (!x || !dy || !dx)) || (flags & ~(unsigned)KDA_NORM_SILU)) return KDA_ERR_INVALID;
+  if (T > 0 && gate && !dgate) return KDA_ERR_INVALID;
+  kda::NormArgs a{};
+  const int64_t width = (int64_t)G * D;
+  if (!source(&a.v, x, x_scales, x_stride, T, width) || !source(&a.gate, gate, gate_scales, gate_stride, T, width) ||
+      !source(&a.dy, dy, nullptr, dy_stride, T, width))
+    return KDA_ERR_INVALID;
+  a.weight = weight, a.scale = scale, a.y = dx, a.extra = gate ? dgate : nullptr;
+  a.dweight = dweight, a.dscale = scale ? dscale : nullptr;
+  a.silu = (flags & KDA_NORM_SILU) != 0, a.packed = a.v.scales != nullptr;
+  return norm_bwd(&a, true, same_kind(a.v, a.gate), T, G, D, eps, dtype, workspace, workspace_bytes, stream);
+}
+
+// ---- Activation checkpoints in 8 bits
+
+static int check_checkpoint(int64_t T, int D, int dtype) {
+  if (T < 0 || !positive(D) || !valid_dtype(dtype)) return KDA_ERR_INVALID;
+  if (D % kda::kScaleBlock != 0 || T > kMaxTokens || T * (D / kda::kScaleBlock) > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+int kda_checkpoint_pack(const void* x, int64_t x_stride, void* codes, void* scales, int64_t T, int D, int dtype,
+                        void* stream) {
+  const int rc = check_checkpoint(T, D, dtype);
+  if (rc != KDA_OK) return rc;
+  kda::Source s;
+  if ((T > 0 && (!x || !codes || !scales)) || !source(&s, x, nullptr, x_stride, T, D)) return KDA_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(codes) & 7) != 0) return KDA_ERR_INVALID;
+  return norm_status(kda::launch_checkpoint_pack(x, s.ld, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), T,
+                                                 D, dtype == KDA_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+int kda_checkpoint_unpack(const void* codes, const void* scales, void* x, int64_t T, int D, int dtype, void* stream) {
+  const int rc = check_checkpoint(T, D, dtype);
+  if (rc != KDA_OK) return rc;
+  if (T > 0 && (!x || !codes || !scales)) return KDA_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(codes) & 7) != 0) return KDA_ERR_INVALID;
+  return norm_status(kda::launch_checkpoint_unpack(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales),
+                                                   x, T, D, dtype == KDA_DTYPE_BF16, static_cast<hipStream_t>(stream)));
+}
+
+// ---- Gated linear recurrence
+
+static int check_glr(int64_t N, int T, int D, unsigned flags, int dtype) {
+  if (flags & ~(unsigned)(KDA_ZERO_REST | KDA_GLR_NORMALISE)) return KDA_ERR_INVALID;
+  if (N < 1 || T < 0 || !positive(D) || !valid_dtype(dtype)) return KDA_ERR_INVALID;
+  if (D > (1 << 20) || N > (1 << 17) || T > kMaxTokens) return KDA_ERR_UNSUPPORTED;
+  // workgroups of 512 threads, 64 tokens or 128 sequences by 64 channels at least: under 2^32 threads a launch
+  const int64_t tiles = ((int64_t)T / kda::kGlrBlock + 1 + N / 128 + 1) * (D / 64 + 1);
+  return tiles >= (1 << 23) ? KDA_ERR_UNSUPPORTED : KDA_OK;
+}
+
+size_t kda_glr_fwd_workspace_size(int T, int D) {
+  return check_glr(1, T, D, 0u, KDA_DTYPE_F32) == KDA_OK ? kda::glr_fwd_workspace_bytes(T, D) : 0;
+}
+
+size_t kda_glr_bwd_workspace_size(int T, int D, int kept_states) {
+  return check_glr(1, T, D, 0u, KDA_DTYPE_F32) == KDA_OK ? kda::glr_bwd_workspace_bytes(T, D, kept_states != 0) : 0;
+}
+
+static bool valid_workspace(const void* p, size_t bytes, size_t need) {
+  return (need == 0 || (p && bytes >= need)) && (reinterpret_cast<uintptr_t>(p) & 255) == 0;
+}
+
+int kda_glr_fwd(const void* x, int64_t x_stride, const void* gate_x, int64_t gate_x_stride, const float* A_log,
+                const float* dt_bias, const void* in_gate, int64_t in_gate_stride, const float* initial_state,
+                const int* cu_seqlens, int N, float* final_state, void* y, float* block_states, int T, int D,
+                unsigned flags, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_glr(N, T, D, flags, dtype);
+  if (rc != KDA_OK) return rc;
+  if (!valid_sequences(N, T, cu_seqlens) || !A_log || (T > 0 && (!x || !gate_x || !y))) return KDA_ERR_INVALID;
+  kda::GlrArgs a{};
+  if (!source(&a.x, x, nullptr, x_stride, T, D) || !source(&a.r, gate_x, nullptr, gate_x_stride, T, D) ||
+      !source(&a.in, in_gate, nullptr, in_gate_stride, T, D))
+    return KDA_ERR_INVALID;
+  if (!valid_workspace(workspace, workspace_bytes, kda_glr_fwd_workspace_size(T, D))) return KDA_ERR_INVALID;
+  a.A_log = A_log, a.dt_bias = dt_bias, a.init = initial_state, a.seqs = kda::make_sequences(cu_seqlens, N, T);
+  a.N = N, a.T = T, a.D = D, a.states = block_states, a.final = final_state, a.y = y;
+  a.zero_rest = (flags & KDA_ZERO_REST) != 0, a.normalise = (flags & KDA_GLR_NORMALISE) != 0;
+  a.bf = dtype == KDA_DTYPE_BF16;
+  return norm_status(kda::launch_glr_fwd(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int kda_glr_bwd(const void* x, const void* x_scales, int64_t x_stride, const void* gate_x, const void* gate_x_scales,
+                int64_t gate_x_stride, const float* A_log, const float* dt_bias, const void* in_gate,
+                const void* in_gate_scales, int64_t in_gate_stride, const float* initial_state, const int* cu_seqlens,
+                int N, const void* dy, int64_t dy_stride, const float* dfinal_state, const float* block_states,
+                void* dx, void* dgate_x, void* din_gate, float* dA_log, float* ddt_bias, float* dinitial_state, int T,
+                int D, unsigned flags, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_glr(N, T, D, flags, dtype);
+  if (rc != KDA_OK) return rc;
+  if (!valid_sequences(N, T, cu_seqlens) || !A_log) return KDA_ERR_INVALID;
+  if (T > 0 && (!x || !gate_x || !dy || !dx || !dgate_x || (in_gate && !din_gate))) return KDA_ERR_INVALID;
+  kda::GlrArgs a{};
+  if (!source(&a.x, x, x_scales, x_stride, T, D) || !source(&a.r, gate_x, gate_x_scales, gate_x_stride, T, D) ||
+      !source(&a.in, in_gate, in_gate_scales, in_gate_stride, T, D) || !source(&a.dy, dy, nullptr, dy_stride, T, D))
+    return KDA_ERR_INVALID;
+  if (!same_kind(a.x, a.r) || !same_kind(a.x, a.in)) return KDA_ERR_INVALID;
+  a.packed = a.x.scales != nullptr;
+  if (a.packed && D % kda::kScaleBlock != 0) return KDA_ERR_UNSUPPORTED;
+  if (!valid_workspace(workspace, workspace_bytes, kda_glr_bwd_workspace_size(T, D, block_states != nullptr)))
+    return KDA_ERR_INVALID;
+  a.A_log = A_log, a.dt_bias = dt_bias, a.init = initial_state, a.seqs = kda::make_sequences(cu_seqlens, N, T);
+  a.N = N, a.T = T, a.D = D, a.states = const_cast<float*>(block_states), a.dfinal = dfinal_state;
+  a.dx = dx, a.dr = dgate_x, a.din = in_gate ? din_gate : nullptr, a.dinit = dinitial_state;
+  a.dA_log = dA_log, a.ddt_bias = ddt_bias;
+  a.zero_rest = (flags & KDA_ZERO_REST) != 0, a.normalise = (flags & KDA_GLR_NORMALISE) != 0;
+  a.bf = dtype == KDA_DTYPE_BF16;
+  return norm_status(kda::launch_glr_bwd(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int kda_glr_step(const void* x, int64_t x_stride, const void* gate_x, int64_t gate_x_stride, const float* A_log,
+                 const float* dt_bias, const void* in_gate, int64_t in_gate_stride, float* state_pool, const int* slots,
+                 int num_slots, void* y, int B, int D, unsigned flags, int dtype, void* stream) {
+  if (!positive(B) || (flags & KDA_ZERO_REST)) return KDA_ERR_INVALID;
+  const int rc = check_glr(1, 0, D, flags, dtype);
+  if (rc != KDA_OK) return rc;
+  if (num_slots < 1 || (!slots && num_slots < B)) return KDA_ERR_INVALID;
+  if (!x || !gate_x || !A_log || !state_pool || !y) return KDA_ERR_INVALID;
+  kda::GlrArgs a{};
+  if (!source(&a.x, x, nullptr, x_stride, B, D) || !source(&a.r, gate_x, nullptr, gate_x_stride, B, D) ||
+      !source(&a.in, in_gate, nullptr, in_gate_stride, B, D))
+    return KDA_ERR_INVALID;
+  if ((int64_t)B * (D / 256 + 1) >= (1 << 23)) return KDA_ERR_UNSUPPORTED;
+  a.A_log = A_log, a.dt_bias = dt_bias, a.pool = state_pool, a.slots = slots, a.nslots = num_slots, a.B = B, a.D = D;
+  a.y = y, a.normalise = (flags & KDA_GLR_NORMALISE) != 0, a.bf = dtype == KDA_DTYPE_BF16;
+  return norm_status(kda::launch_glr_step(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

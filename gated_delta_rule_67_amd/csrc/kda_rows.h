@@ -1,0 +1,119 @@
+// Rows of channels as the layer operators read them: elements of float32 or bf16, a vector of them a
+// lane, or an 8-bit checkpoint of such a tensor (e4m3 codes, a power of two for every 32 neighbours).
+#pragma once
+
+#include "kda_device.h"
+
+namespace kda {
+
+// A tensor of tokens, or its checkpoint.
+struct Source {
+  const void* p;          // elements, or codes
+  const uint8_t* scales;  // exponents of the codes' powers of two, or null: p holds elements
+  int64_t ld;             // elements between tokens
+};
+
+constexpr int kScaleBlock = 32;  // neighbours that share a scale
+
+// 2^(byte - 127), the scale that a checkpoint's byte stands for (byte <= 254; 0 is 2^-127).
+__device__ __forceinline__ float scale_of(unsigned byte) {
+  return __uint_as_float(byte ? byte << 23 : 1u << 22);
+}
+
+template <typename T, int VEC> struct RowVec {
+  typedef T type __attribute__((ext_vector_type(VEC)));
+};
+template <typename T> struct RowVec<T, 1> { typedef T type; };
+
+// VEC elements in the memory's type, and their float32 values.
+template <typename T, int VEC> struct Piece {
+  typename RowVec<T, VEC>::type raw;
+
+  __device__ __forceinline__ void load(const void* p, int64_t off) {
+    raw = *reinterpret_cast<const typename RowVec<T, VEC>::type*>(static_cast<const T*>(p) + off);
+  }
+  __device__ __forceinline__ void load(const Source& s, int64_t off) { load(s.p, off); }
+  __device__ __forceinline__ void get(float (&v)[VEC]) const {
+    if constexpr (VEC == 1) v[0] = to_f32(raw);
+    else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = to_f32(raw[e]);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[VEC]) {
+    if constexpr (VEC == 1) raw = from_f32<T>(v[0]);
+    else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) raw[e] = from_f32<T>(v[e]);
+    }
+  }
+  __device__ __forceinline__ void store(void* p, int64_t off) const {
+    *reinterpret_cast<typename RowVec<T, VEC>::type*>(static_cast<T*>(p) + off) = raw;
+  }
+  __device__ __forceinline__ void store_stream(void* p, int64_t off) const {
+    __builtin_nontemporal_store(raw, reinterpret_cast<typename RowVec<T, VEC>::type*>(static_cast<T*>(p) + off));
+  }
+};
+
+// VEC codes of a checkpoint and their scale; off is a multiple of VEC, so that one scale serves them.
+template <int VEC> struct PackedPiece {
+  static constexpr int kWords = VEC > 4 ? VEC / 4 : 1;
+  unsigned word[kWords];
+  unsigned byte;
+
+  __device__ __forceinline__ void load(const Source& s, int64_t off) {
+    const uint8_t* c = static_cast<const uint8_t*>(s.p) + off;
+    if constexpr (VEC == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(c);
+      word[0] = v.x, word[1] = v.y;
+    } else if constexpr (VEC == 4) word[0] = *reinterpret_cast<const unsigned*>(c);
+    else if constexpr (VEC == 2) word[0] = *reinterpret_cast<const unsigned short*>(c);
+    else word[0] = *c;
+    byte = s.scales[off / kScaleBlock];
+  }
+  __device__ __forceinline__ void get(float (&v)[VEC]) const {
+    const float f = scale_of(byte);
+    if constexpr (VEC == 1) v[0] = f * __builtin_amdgcn_cvt_f32_fp8(word[0], 0);
+    else {
+#pragma unroll
+      for (int e = 0; e < VEC; e += 2) {
+        const auto two = (e & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8(word[e / 4], true)
+                                 : __builtin_amdgcn_cvt_pk_f32_fp8(word[e / 4], false);
+        v[e] = f * two[0];
+        v[e + 1] = f * two[1];
+      }
+    }
+  }
+};
+
+// What a backward pass reads of the forward's inputs: elements, or a checkpoint of them.
+template <typename T, int VEC, bool CK> struct KeptPiece { typedef Piece<T, VEC> type; };
+template <typename T, int VEC> struct KeptPiece<T, VEC, true> { typedef PackedPiece<VEC> type; };
+
+// logistic(z) and 1 - logistic(z), each to float32 accuracy of its own.
+__device__ __forceinline__ void logistic_pair(float z, float& s, float& rest) {
+  const float e = fast_exp2(-fabsf(z) * kLog2e), r = __builtin_amdgcn_rcpf(1.f + e), l = e * r;
+  s = z >= 0.f ? r : l;
+  rest = z >= 0.f ? l : r;
+}
+
+// Column sums in a fixed order: out[k][c] = sum over the nb row blocks j of part[j][k][c], for K
+// vectors of D columns (a null out is not wanted).
+struct ColumnSums {
+  const float* part;  // [nb][K][D]
+  float* out[2];
+  int nb, K, D;
+};
+hipError_t launch_column_sums(const ColumnSums& a, hipStream_t stream);
+
+// The largest vector, of at most `most` elements (4 bytes or 16 of them, or one), that the widths and
+// strides (or-ed together) and the addresses allow.
+inline int vector_width(int most, int esize, int64_t widths, const void* const* ptrs, int n) {
+  uintptr_t bits = 0;
+  for (int i = 0; i < n; ++i) bits |= reinterpret_cast<uintptr_t>(ptrs[i]);
+  int vec = most;
+  while (vec > 1 && (widths % vec || bits % ((size_t)vec * esize))) vec /= 2;
+  return vec;
+}
+
+}  // namespace kda

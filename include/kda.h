@@ -452,7 +452,9 @@ int kda_chunk_fwd_noalloc(const void* q, const void* k, const void* v, const voi
  */
 typedef enum {
   KDA_CONV_SILU = 1, /* convolution: y = silu(pre); otherwise y = pre */
-  KDA_ZERO_REST = 2  /* convolution and scan: set the output rows that lie in no sequence to zero */
+  KDA_ZERO_REST = 2, /* convolution, scan and recurrence: zeros in the output rows that lie in no sequence */
+  KDA_GLR_NORMALISE = 4, /* gated linear recurrence: inputs weighted by sqrt(1 - a^2) */
+  KDA_NORM_SILU = 1      /* kda_postnorm: the gate's activation is silu; otherwise the logistic */
 } kda_layer_flags;
 
 int kda_conv_fwd(const void* x, int64_t x_stride, const float* weight, const float* bias,
@@ -597,6 +599,158 @@ size_t kda_slots_compact_workspace_size(int num_slots);
 int kda_slots_compact(void* const* pools, const size_t* slot_bytes, int num_pools, int num_slots,
                       const unsigned char* live, int* new_slot, int* count, void* workspace,
                       size_t workspace_bytes, void* stream);
+
+/*
+ * Norms around a block, joined with its gate, its residual and the residual's scale (DM-KDAGQA-1.7B-SD
+ * model card, Model table: RMSNorm; the recurrence's outputs are normed per head under an output gate).
+ * Rows of D columns: T tokens of G rows each. All sums are float32, an output is rounded once.
+ *
+ * In front of a block, with the residual addition behind the block before it:
+ *     h = residual + scale x,   y = weight h / sqrt(mean(h^2) + eps)
+ *
+ *   x              [T, G, D]  dtype, x_stride elements between tokens (>= G D: a slice of a wider
+ *                             activation may be given); every *_stride here likewise
+ *   residual       [T, G, D]  dtype, or NULL: h = scale x
+ *   weight, scale  [D]        float32; scale may be NULL: ones
+ *   y              [T, G, D]  dtype out (the norm is that of h before its rounding)
+ *   h              [T, G, D]  dtype out, or NULL; may be the residual's memory where its stride is G D
+ *   eps            finite, at least the smallest normal float (1.2e-38)
+ *
+ * Behind a block, under its gate and into the residual:
+ *     y = residual + scale (weight act(gate) x / sqrt(mean(x^2) + eps))
+ * act is the logistic, or silu with KDA_NORM_SILU; gate NULL: no factor; residual, scale NULL as above; y may
+ * be the residual's memory where its stride is G D.
+ *
+ * T >= 0, G, D >= 1 (else KDA_ERR_INVALID); D <= 8192, T <= 2^30, T G < 2^31 (else KDA_ERR_UNSUPPORTED). No
+ * alignment is required; rows of whole 16-byte pieces, 16-byte aligned, are fastest. Rows whose sum of
+ * squares leaves the float32 range (magnitudes from about 2^63 / sqrt(D)) give zeros for their norm. Apart
+ * from the two cases named, outputs must not overlap inputs. Nothing is allocated.
+ */
+int kda_prenorm_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                    const float* weight, const float* scale, void* y, void* h, int64_t T, int G,
+                    int D, float eps, int dtype, void* stream);
+
+int kda_postnorm_fwd(const void* x, int64_t x_stride, const float* weight, const void* gate,
+                     int64_t gate_stride, const void* residual, int64_t residual_stride,
+                     const float* scale, void* y, int64_t T, int G, int D, float eps,
+                     unsigned flags, int dtype, void* stream);
+
+/*
+ * Backward of kda_prenorm_fwd for dy reaching y and dh (or NULL: zeros) reaching h, from the h that it
+ * returned (x itself where it had neither residual nor scale): dresidual [T, G, D] (the gradient of h: of
+ * the residual, and of x where scale is NULL), and where scale is given, with x, dx = scale dresidual and
+ * dscale [D]; dweight [D] (float32). dweight and dscale may be NULL.
+ * Backward of kda_postnorm_fwd for dy reaching y (which is the residual's gradient as it is): dx, dgate
+ * (where a gate is given), dweight and dscale.
+ *
+ * What the forward pass kept (h and x; x and gate) may be 8-bit checkpoints (kda_checkpoint_pack): *_scales
+ * not NULL, codes in the tensor's place, dense. All of a call's are checkpoints or none (else
+ * KDA_ERR_INVALID), D % 32 == 0 (else KDA_ERR_UNSUPPORTED). Gradients are those at the values they stand for.
+ * The sums over rows are taken in a fixed order (bitwise reproducible). workspace: device memory of
+ * kda_norm_bwd_workspace_size() bytes, 256-byte aligned, caller-owned, overwritten; NULL where dweight and
+ * dscale are. Otherwise as the forward calls.
+ */
+size_t kda_norm_bwd_workspace_size(int64_t T, int G, int D);
+
+int kda_prenorm_bwd(const void* h, const void* h_scales, int64_t h_stride, const float* weight,
+                    const void* dy, int64_t dy_stride, const void* dh, int64_t dh_stride,
+                    const void* x, const void* x_scales, int64_t x_stride, const float* scale,
+                    void* dresidual, void* dx, float* dweight, float* dscale, int64_t T, int G,
+                    int D, float eps, int dtype, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+int kda_postnorm_bwd(const void* x, const void* x_scales, int64_t x_stride, const float* weight,
+                     const void* gate, const void* gate_scales, int64_t gate_stride,
+                     const void* dy, int64_t dy_stride, const float* scale, void* dx, void* dgate,
+                     float* dweight, float* dscale, int64_t T, int G, int D, float eps,
+                     unsigned flags, int dtype, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/*
+ * Activation checkpoints in 8 bits: what a forward pass keeps for the backward pass (which reads it as it
+ * is: kda_prenorm_bwd, kda_postnorm_bwd, kda_glr_bwd), in 33 bytes for 32 elements. 32 neighbours of a
+ * token share the smallest power of two 2^(byte - 127), byte >= 0, that brings their largest finite
+ * magnitude to 448 or less; a code is an element divided by it, rounded to nearest even in e4m3 (off by
+ * 2^-4 of the element at most, or 2^-10 of the scale for codes below 2^-6). Infinities and NaN become NaN.
+ *
+ *   x       [T, D]     dtype, x_stride elements between tokens (pack); dense (unpack, out)
+ *   codes   [T, D]     e4m3 bytes, 8-byte aligned
+ *   scales  [T, D/32]  bytes
+ *
+ * unpack writes code x 2^(byte - 127), in bf16 rounded to nearest even where that is below its range.
+ * T >= 0, D >= 1 (else KDA_ERR_INVALID); D % 32 == 0, T <= 2^30, T D / 32 < 2^31 (else KDA_ERR_UNSUPPORTED).
+ */
+int kda_checkpoint_pack(const void* x, int64_t x_stride, void* codes, void* scales, int64_t T,
+                        int D, int dtype, void* stream);
+
+int kda_checkpoint_unpack(const void* codes, const void* scales, void* x, int64_t T, int D,
+                          int dtype, void* stream);
+
+/*
+ * Gated linear recurrence with one state per channel: the elementwise layer that hybrid stacks put beside
+ * the gated delta rule, under the standard decay gate (K3 README, roadmap row L5). Per channel, float32:
+ *
+ *     g_t = -exp(A_log) softplus(gate_x_t + dt_bias),   a_t = exp(g_t)
+ *     h_t = a_t h_{t-1} + w_t logistic(in_gate_t) x_t,   y_t = h_t
+ * with w_t = sqrt(1 - a_t^2) with KDA_GLR_NORMALISE, else 1.
+ *
+ *   x, gate_x, in_gate  [T, D]  dtype, *_stride elements between tokens (>= D); in_gate may be NULL: factor 1
+ *   A_log, dt_bias      [D]     float32 (an exp(A_log) of 3e38 and more counts as 3e38); dt_bias may be NULL
+ *   initial_state       [N, D]  float32, or NULL: zeros
+ *   cu_seqlens          as for kda_conv_fwd (NULL: N sequences of T / N tokens each)
+ *   final_state         [N, D]  float32 out, or NULL; must not overlap initial_state
+ *   y                   [T, D]  dtype out; rows in no sequence are left as they were, or zeros with
+ *                               KDA_ZERO_REST
+ *   block_states        [ceil(T / 64), D] float32 out, or NULL: the state in front of every 64th token, for
+ *                               kda_glr_bwd (unspecified where that token begins a sequence or lies in none)
+ *   workspace           device memory of kda_glr_fwd_workspace_size() bytes, 256-byte aligned, caller-owned,
+ *                               overwritten; NULL where that size is 0
+ *
+ * The token axis is scanned in one pass of the data; results are bitwise reproducible. Tokens of other
+ * sequences, and tokens behind, do not reach an output, finite or not; behind a state that is not finite,
+ * NaN may stand for an infinity. The softplus, decays and weights have a relative error of about 1e-6.
+ * N >= 1, T >= 0, D >= 1 (else KDA_ERR_INVALID); N <= 2^17, D <= 2^20, T <= 2^30, T D under about 2^35 (else
+ * KDA_ERR_UNSUPPORTED). No alignment is required. Nothing is allocated.
+ */
+size_t kda_glr_fwd_workspace_size(int T, int D);
+
+int kda_glr_fwd(const void* x, int64_t x_stride, const void* gate_x, int64_t gate_x_stride,
+                const float* A_log, const float* dt_bias, const void* in_gate,
+                int64_t in_gate_stride, const float* initial_state, const int* cu_seqlens, int N,
+                float* final_state, void* y, float* block_states, int T, int D, unsigned flags,
+                int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of kda_glr_fwd for dy reaching y and dfinal_state (or NULL: zeros) reaching the final state:
+ * dx, dgate_x and (where in_gate is given) din_gate [T, D] dtype, dA_log and ddt_bias [D] float32 (either
+ * may be NULL), dinitial_state [N, D] float32 (may be NULL). Rows in no sequence are treated as y rows are
+ * there. block_states: those that the forward call with the same arguments left, or NULL (they are
+ * computed once more). x, gate_x and in_gate may be 8-bit checkpoints, as for kda_prenorm_bwd (the
+ * block_states are then best left NULL: those of the unrounded inputs belong to other gradients).
+ * The sums over tokens are taken in a fixed order. workspace: kda_glr_bwd_workspace_size() bytes
+ * (kept_states: whether block_states are given), otherwise as kda_glr_fwd.
+ */
+size_t kda_glr_bwd_workspace_size(int T, int D, int kept_states);
+
+int kda_glr_bwd(const void* x, const void* x_scales, int64_t x_stride, const void* gate_x,
+                const void* gate_x_scales, int64_t gate_x_stride, const float* A_log,
+                const float* dt_bias, const void* in_gate, const void* in_gate_scales,
+                int64_t in_gate_stride, const float* initial_state, const int* cu_seqlens, int N,
+                const void* dy, int64_t dy_stride, const float* dfinal_state,
+                const float* block_states, void* dx, void* dgate_x, void* din_gate, float* dA_log,
+                float* ddt_bias, float* dinitial_state, int T, int D, unsigned flags, int dtype,
+                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token of kda_glr_fwd per request, on slot slots[n] of state_pool [num_slots, D] (float32, updated in
+ * place): x, gate_x, in_gate (or NULL) and y [B, D]. slots NULL: request n uses slot n (num_slots >= B). A
+ * request whose slot is outside [0, num_slots) gets y = 0 and changes no state; valid slots of one call must
+ * be distinct. flags: 0 or KDA_GLR_NORMALISE. B ceil(D / 256) < 2^23, otherwise as kda_glr_fwd.
+ */
+int kda_glr_step(const void* x, int64_t x_stride, const void* gate_x, int64_t gate_x_stride,
+                 const float* A_log, const float* dt_bias, const void* in_gate,
+                 int64_t in_gate_stride, float* state_pool, const int* slots, int num_slots,
+                 void* y, int B, int D, unsigned flags, int dtype, void* stream);
 
 /*
  * A plain streaming copy of `bytes` bytes from src to dst (device memory, 16-byte aligned,
