@@ -46,14 +46,14 @@ hipError_t launch_glr_step(const GlrArgs& a, hipStream_t stream);
 
 namespace glr {
 
-// ---- Gates. Per channel: neg_rate = -exp(A_log) (an exp(A_log) above the largest float counts as
-// that) in units of log2, and the bias.
+// ---- Gates. Per channel: -exp(A_log) in units of log2 (an exp(A_log) above 2e38 counts as that, so
+// that the product is finite), and the bias.
 struct Channel {
   float neg_rate2, bias;
 };
 __device__ __forceinline__ Channel channel(const GlrArgs& a, int c) {
   const float rate = expf(a.A_log[c]);
-  return {-(rate > 3.0e38f ? 3.0e38f : rate) * kLog2e, a.dt_bias ? a.dt_bias[c] : 0.f};
+  return {-(rate > 2.0e38f ? 2.0e38f : rate) * kLog2e, a.dt_bias ? a.dt_bias[c] : 0.f};
 }
 
 // log2 of the decay, g2 <= 0, for the gate's input; also what the softplus leaves for its slope, the

@@ -695,7 +695,7 @@ int kda_checkpoint_unpack(const void* codes, const void* scales, void* x, int64_
  * with w_t = sqrt(1 - a_t^2) with KDA_GLR_NORMALISE, else 1.
  *
  *   x, gate_x, in_gate  [T, D]  dtype, *_stride elements between tokens (>= D); in_gate may be NULL: factor 1
- *   A_log, dt_bias      [D]     float32 (an exp(A_log) of 3e38 and more counts as 3e38); dt_bias may be NULL
+ *   A_log, dt_bias      [D]     float32 (an exp(A_log) above 2e38 counts as 2e38); dt_bias may be NULL
  *   initial_state       [N, D]  float32, or NULL: zeros
  *   cu_seqlens          as for kda_conv_fwd (NULL: N sequences of T / N tokens each)
  *   final_state         [N, D]  float32 out, or NULL; must not overlap initial_state

@@ -25,6 +25,9 @@ Three independent CPU formulations, all in float64 numpy:
 * ``conv`` / ``conv_bwd``: the short causal convolution in front of the recurrence, and
   its gradients.
 * ``selective_scan``: the selective state space scan with a scalar decay per head.
+* ``prenorm`` / ``postnorm`` (``_bwd``): the norms in front of and behind a block, and their gradients.
+* ``glr`` / ``glr_bwd``: the gated linear recurrence with one state per channel, and its gradients.
+* ``checkpoint_pack`` / ``checkpoint_unpack``: activations in 8 bits, from the table of codes.
 * ``transforms``: the optional in-operator input transforms (q/k L2
   normalisation, beta sigmoid) that ``recurrent`` / ``decode_step`` apply on
   request.
@@ -42,6 +45,9 @@ from .backward import recurrent_bwd
 from .gate import gate, gate_bwd
 from .conv import conv, conv_bwd
 from .ssm import selective_scan
+from .norm import postnorm, postnorm_bwd, prenorm, prenorm_bwd
+from .glr import glr, glr_bwd, glr_gates
+from .checkpoint import checkpoint_pack, checkpoint_unpack
 
 __all__ = [
     "decode_step",
@@ -57,4 +63,13 @@ __all__ = [
     "conv",
     "conv_bwd",
     "selective_scan",
+    "prenorm",
+    "prenorm_bwd",
+    "postnorm",
+    "postnorm_bwd",
+    "glr",
+    "glr_bwd",
+    "glr_gates",
+    "checkpoint_pack",
+    "checkpoint_unpack",
 ]

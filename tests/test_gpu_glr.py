@@ -1,0 +1,351 @@
+"""GPU parity of kda_glr_fwd / kda_glr_bwd / kda_glr_step against the float64 oracle.
+
+Tolerance, per element, with u = 2^-24. The gates: softplus within 17 u relatively and |z| u for its
+rounded input; with rate and products g is within e_g = (24 + |z|) u, so the decay within
+e_a = |g| e_g + 4 u, w within e_g / 2 + 20 u (|g| a^2 / w^2 <= 1/2; series, root or 1 - a^2), the
+logistic within (6 + 2 |in_gate|) u, and the input b = w s x within their sum e_b. States: with H the
+recurrence of the absolute values (H_t = a H_{t-1} + |b_t|, which bounds every partial sum whatever
+the split of the tokens), E_t = a E_{t-1} + a H_{t-1} e_a + |b| e_b + 4 u H_t: each product of decays
+carries the sum of its tokens' e_a, each sum one rounding. The gradient G runs the same recurrence
+against the tokens. Products of these carry the sum of their factors' errors, and column sums a
+rounding for each of their terms. On top, half a step of the output type."""
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_67_amd as kda
+from oracle import glr, glr_bwd, glr_gates
+from tests.helpers import log, to64
+from tests.test_gpu_norm import HALF, U, close
+
+pytestmark = pytest.mark.gpu
+
+
+def _make(lengths, D, dtype, seed, init=True, in_gate=True, bias=True, tail=0, head=0, pad=0, rate=0.0):
+    g = torch.Generator().manual_seed(seed)
+    T = head + sum(lengths) + tail
+    N = len(lengths)
+    tok = lambda: torch.randn((T, D + pad), generator=g).to(dtype)  # noqa: E731
+    d = dict(x=tok(), gate_x=tok(), in_gate=2 * tok() if in_gate else None, dy=tok(),
+             A_log=rate + torch.randn(D, generator=g), dt_bias=torch.randn(D, generator=g) - 2 if bias else None,
+             init=torch.randn((N, D), generator=g) if init else None, dfinal=torch.randn((N, D), generator=g) if init else None,
+             cu=torch.tensor(head + np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32))
+    d = {k: None if v is None else v.cuda() for k, v in d.items()}
+    for k in ("x", "gate_x", "in_gate", "dy"):
+        if d[k] is not None:
+            d[k] = d[k][:, pad:]
+    return d
+
+
+def _bounds(x, r, A, b, i, h0, dy, df, normalise):
+    """Of one sequence: (errors of y, h behind it; of dx, dr, di, dinit; absolute terms and errors of dA, db)."""
+    z, g, a, w, s = glr_gates(r, A, b, i, normalise)
+    T, D = x.shape
+    eg = (24 + np.abs(z)) * U
+    ea = np.abs(g) * eg + 4 * U
+    ew = eg / 2 + 20 * U if normalise else 0 * eg
+    es = 0 * eg if i is None else (6 + 2 * np.abs(i)) * U
+    rest = 0 * s if i is None else 1 - s
+    B, eb = np.abs(w * s * x), ew + es + 4 * U
+    H, E = np.zeros(D) if h0 is None else np.abs(h0), np.zeros(D)
+    hb, Eb, Ey = np.zeros((T, D)), np.zeros((T, D)), np.zeros((T, D))
+    for t in range(T):
+        hb[t], Eb[t] = H, E
+        E = a[t] * E + a[t] * H * ea[t] + B[t] * eb[t]
+        H = a[t] * H + B[t]
+        E = E + 4 * U * H
+        Ey[t] = E
+    G, F = np.zeros(D) if df is None else np.abs(df), np.zeros(D)
+    Gt, Ft = np.zeros((T, D)), np.zeros((T, D))
+    for t in reversed(range(T)):
+        Gt[t] = np.abs(dy[t]) + G
+        Ft[t] = F + 4 * U * Gt[t]
+        F = a[t] * Ft[t] + a[t] * Gt[t] * ea[t]
+        G = a[t] * Gt[t]
+    q = np.abs(s * x)
+    ratio = np.divide(a * a, w, out=np.zeros_like(w), where=w > 0) if normalise else 0 * a
+    Edx = Ft * s * w + Gt * s * w * (ew + es + 4 * U)
+    Edi = np.abs(x) * w * s * rest * (Ft + Gt * (ew + 2 * es + 8 * U))
+    dg = Gt * a * hb + Gt * q * ratio
+    Edg = (Ft * (a * hb + q * ratio) + Gt * a * (Eb + hb * (ea + 6 * U)) + Gt * q * ratio * (2 * ea + ew + es + 8 * U))
+    l = np.exp(-np.logaddexp(0.0, -z))
+    rate = np.exp(A)
+    el = (10 + 2 * np.abs(z)) * U
+    Edr = rate * l * (Edg + dg * (el + 8 * U))
+    EdA = (Edg * np.abs(g) + dg * np.abs(g) * (eg + 6 * U)).sum(0)
+    return Ey, E, Edx, Edr, Edi, F + U * G, (dg * np.abs(g)).sum(0), EdA, (rate * l * dg).sum(0), Edr.sum(0)
+
+
+def _value(t):
+    if isinstance(t, tuple):
+        return to64(kda.kda_checkpoint_unpack(t[0], t[1], torch.float32))
+    return None if t is None else to64(t)
+
+
+def _check(d, dtype, normalise=True, packed=False, dense=False, states=True):
+    half, cu = HALF[dtype], d["cu"].cpu().numpy()
+    N, T = len(cu) - 1, d["x"].shape[0]
+    kept = {k: d[k] for k in ("x", "gate_x", "in_gate")}
+    if packed:
+        kept = {k: None if v is None else kda.kda_checkpoint_pack(v) for k, v in kept.items()}
+    shaped = lambda v: v if v is None or not dense else (  # noqa: E731
+        tuple(shaped(u) for u in v) if isinstance(v, tuple) else v.unflatten(0, (N, -1)))
+    off = None if dense else d["cu"]
+    y, final, st = kda.kda_glr_fwd(shaped(d["x"]), shaped(d["gate_x"]), d["A_log"], d["dt_bias"], shaped(d["in_gate"]),
+                                   d["init"], off, normalise=normalise, output_block_states=True)
+    args = (shaped(kept["x"]), shaped(kept["gate_x"]), d["A_log"], shaped(d["dy"]), d["dt_bias"], shaped(kept["in_gate"]),
+            d["init"], d["dfinal"], off)
+    got = kda.kda_glr_bwd(*args, normalise=normalise, block_states=st if states and not packed else None)
+    if states and not packed:  # the states computed again are the same
+        for a, b in zip(got, kda.kda_glr_bwd(*args, normalise=normalise)):
+            assert (a is None and b is None) or torch.equal(a, b)
+    torch.cuda.synchronize()
+    h = {k: _value(v) for k, v in d.items()}
+    hk = {k: _value(v) for k, v in kept.items()}
+    flat = lambda v: None if v is None else v.reshape(d["dy"].shape)  # noqa: E731
+    y, (dx, dr, di, dA, db, dinit) = flat(y), (flat(got[0]), flat(got[1]), flat(got[2])) + got[3:]
+    sA = sb = rA = rb = 0.0
+    ref = {k: np.zeros(h["x"].shape) for k in ("y", "dx", "dr", "di")}
+    tol = {k: np.zeros(h["x"].shape) for k in ref}
+    rf, tf, ri, ti = (np.zeros((N, h["x"].shape[1])) for _ in range(4))
+    row = lambda v, n: None if v is None else v[n]  # noqa: E731
+    for n in range(N):
+        t = slice(cu[n], cu[n + 1])
+        part = lambda v: None if v is None else v[t]  # noqa: E731
+        ref["y"][t], rf[n] = glr(h["x"][t], h["gate_x"][t], h["A_log"], h["dt_bias"], part(h["in_gate"]), row(h["init"], n), normalise)
+        b = _bounds(h["x"][t], h["gate_x"][t], h["A_log"], h["dt_bias"], part(h["in_gate"]), row(h["init"], n), h["dy"][t],
+                    row(h["dfinal"], n), normalise)
+        tol["y"][t], tf[n] = b[0], b[1]
+        if packed:
+            b = _bounds(hk["x"][t], hk["gate_x"][t], h["A_log"], h["dt_bias"], part(hk["in_gate"]), row(h["init"], n), h["dy"][t],
+                        row(h["dfinal"], n), normalise)
+        tol["dx"][t], tol["dr"][t], tol["di"][t], ti[n] = b[2:6]
+        r = glr_bwd(hk["x"][t], hk["gate_x"][t], h["A_log"], h["dy"][t], h["dt_bias"], part(hk["in_gate"]), row(h["init"], n),
+                    row(h["dfinal"], n), normalise)
+        ref["dx"][t], ref["dr"][t], ref["di"][t], ri[n] = r[0], r[1], r[2], r[5]
+        rA, rb = rA + r[3], rb + r[4]
+        sA, sb = sA + T * U * b[6] + b[7], sb + T * U * b[8] + b[9]
+    for name, out in (("y", y), ("dx", dx), ("dr", dr), ("di", di)):
+        if out is not None:
+            close(out, ref[name], half * np.abs(ref[name]) + tol[name], name)
+    close(final, rf, tf, "final state")
+    close(dA, rA, sA, "dA_log")
+    if db is not None:
+        close(db, rb, sb, "ddt_bias")
+    if dinit is not None:
+        close(dinit, ri, ti, "dinitial_state")
+    assert (di is None) == (d["in_gate"] is None) and (db is None) == (d["dt_bias"] is None)
+
+
+CASES = [
+    # lengths, D, dtype, init, in_gate, bias, normalise, pad
+    ([1], 8, "bf16", True, True, True, True, 0),
+    ([1], 1, "f32", False, False, False, False, 0),
+    ([0, 1, 2, 3, 4, 5, 0, 37, 0], 64, "bf16", True, True, True, True, 0),
+    ([257], 130, "bf16", False, True, True, True, 2),
+    ([5, 300, 1, 0, 90], 65, "f32", True, True, True, True, 0),
+    ([130, 3, 70], 33, "bf16", True, False, True, False, 1),
+    ([64, 64, 128, 16], 200, "bf16", True, True, False, True, 0),
+    ([15, 1, 16, 17, 63, 65, 127, 129], 70, "f32", True, False, True, True, 3),
+    ([2] * 70 + [1] * 70, 24, "f32", True, True, True, False, 0),
+    ([1100, 30], 9, "bf16", True, True, True, True, 0),
+]
+
+
+@pytest.mark.parametrize("lengths,D,dtype,init,in_gate,bias,normalise,pad", CASES)
+@pytest.mark.parametrize("head,tail", [(0, 0), (3, 9), (0, 150)])
+def test_packed(lengths, D, dtype, init, in_gate, bias, normalise, pad, head, tail):
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    log(f"glr lengths={lengths[:8]} D={D} {dtype} head={head} tail={tail}")
+    _check(_make(lengths, D, dt, sum(lengths) + D, init, in_gate, bias, tail, head, pad), dt, normalise)
+
+
+@pytest.mark.parametrize("B,T,D,dtype", [(1, 1, 5, "f32"), (3, 40, 66, "bf16"), (2, 128, 128, "bf16"), (4, 100, 7, "f32"),
+                                         (1, 1025, 64, "bf16")])
+def test_dense(B, T, D, dtype):
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    _check(_make([T] * B, D, dt, B + T), dt, dense=True)
+
+
+@pytest.mark.parametrize("lengths", [[5000], [3000, 2500], [700, 1, 4000], [1024, 1024, 2048]])
+@pytest.mark.parametrize("dtype,D", [("bf16", 130), ("f32", 65)])
+def test_many_tiles(lengths, dtype, D):
+    """Sequences over many tiles and groups of them, with decays slow enough that states cross them."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    _check(_make(lengths, D, dt, len(lengths), rate=-5.0), dt)
+
+
+@pytest.mark.parametrize("lengths,D,dtype,in_gate", [([90, 0, 33], 64, "bf16", True), ([700], 32, "f32", True),
+                                                     ([1300, 20], 96, "bf16", False)])
+def test_backward_from_checkpoints(lengths, D, dtype, in_gate):
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    _check(_make(lengths, D, dt, D, in_gate=in_gate, tail=5), dt, packed=True)
+
+
+def test_empty_calls():
+    d = _make([0, 0], 16, torch.bfloat16, 1)
+    y, f = kda.kda_glr_fwd(d["x"], d["gate_x"], d["A_log"], d["dt_bias"], d["in_gate"], d["init"], d["cu"])
+    assert y.shape == (0, 16) and torch.equal(f, d["init"])
+    g = kda.kda_glr_bwd(d["x"], d["gate_x"], d["A_log"], d["dy"], d["dt_bias"], d["in_gate"], d["init"], d["dfinal"], d["cu"])
+    assert torch.equal(g[5], d["dfinal"]) and not g[3].any() and not g[4].any()
+    y, f = kda.kda_glr_fwd(d["x"].view(2, 0, 16), d["gate_x"].view(2, 0, 16), d["A_log"])
+    assert y.shape == (2, 0, 16) and not f.any()
+
+
+def test_rows_in_no_sequence_are_zero_or_left():
+    d = _make([20, 200], 40, torch.float32, 2, head=130, tail=70)
+    T, D = d["x"].shape
+    y, _ = kda.kda_glr_fwd(d["x"], d["gate_x"], d["A_log"], d["dt_bias"], None, None, d["cu"])
+    assert not y[:130].any() and not y[350:].any() and bool(y[130:350].all())
+    lib, mark, s = kda.library(), 2.0 ** 40, torch.cuda.current_stream().cuda_stream
+    n, m = lib.kda_glr_fwd_workspace_size(T, D), lib.kda_glr_bwd_workspace_size(T, D, 0)
+    ws = torch.empty(max(n, m), dtype=torch.uint8, device="cuda")
+    out, dx, dr = (torch.full((T, D), mark, device="cuda") for _ in range(3))
+    assert lib.kda_glr_fwd(d["x"].data_ptr(), D, d["gate_x"].data_ptr(), D, d["A_log"].data_ptr(), d["dt_bias"].data_ptr(), None,
+                           0, None, d["cu"].data_ptr(), 2, None, out.data_ptr(), None, T, D, 4, 0, ws.data_ptr(), n, s) == 0
+    assert lib.kda_glr_bwd(d["x"].data_ptr(), None, D, d["gate_x"].data_ptr(), None, D, d["A_log"].data_ptr(),
+                           d["dt_bias"].data_ptr(), None, None, 0, None, d["cu"].data_ptr(), 2, d["dy"].data_ptr(), D, None, None,
+                           dx.data_ptr(), dr.data_ptr(), None, None, None, None, T, D, 4, 0, ws.data_ptr(), m, s) == 0
+    assert torch.equal(out[130:350], y[130:350])
+    for t in (out, dx, dr):
+        assert bool((t[:130] == mark).all()) and bool((t[350:] == mark).all()) and not bool((t[130:350] == mark).any())
+
+
+def test_other_sequences_and_later_tokens_do_not_leak():
+    """Values that are not finite reach the outputs behind them in their sequence (in front of them,
+    for gradients), and no others."""
+    d = _make([300, 150, 260], 70, torch.bfloat16, 3)
+    call = lambda x, r, i, dy: (  # noqa: E731
+        kda.kda_glr_fwd(x, r, d["A_log"], d["dt_bias"], i, d["init"], d["cu"])[0],
+        *kda.kda_glr_bwd(x, r, d["A_log"], dy, d["dt_bias"], i, d["init"], d["dfinal"], d["cu"])[:3])
+    ref = call(d["x"], d["gate_x"], d["in_gate"], d["dy"])
+    for name in ("x", "gate_x", "in_gate", "dy"):
+        for bad in (float("nan"), float("inf"), float("-inf")):
+            t = dict(d, **{name: d[name].clone()})
+            t[name][390] = bad
+            got = call(t["x"], t["gate_x"], t["in_gate"], t["dy"])
+            for a, b in zip(got, ref):
+                assert torch.equal(a[:300], b[:300]) and torch.equal(a[450:], b[450:])
+            assert torch.equal(got[0][:390], ref[0][:390])
+            if name == "dy":
+                assert torch.equal(got[0], ref[0])
+                assert all(torch.equal(a[391:450], b[391:450]) for a, b in zip(got[1:], ref[1:]))
+    # a state that is not finite stays in its sequence
+    init = d["init"].clone()
+    init[1] = float("inf")
+    y, f = kda.kda_glr_fwd(d["x"], d["gate_x"], d["A_log"], d["dt_bias"], d["in_gate"], init, d["cu"])
+    assert torch.equal(y[:300], ref[0][:300]) and torch.equal(y[450:], ref[0][450:]) and not bool(torch.isfinite(y[300]).any())
+
+
+def test_extreme_gates():
+    """Gates at the ends of their range: decay 1 and input weight 0 (no NaN in gradients), decay 0 and
+    weight 1; rates past every float."""
+    T, D = 200, 66
+    torch.manual_seed(4)
+    x, dy = torch.randn(T, D, device="cuda"), torch.randn(T, D, device="cuda")
+    init = torch.randn(1, D, device="cuda")
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    for value, A in ((-200.0, 0.0), (float("-inf"), 0.0), (-200.0, 300.0), (float("-inf"), 300.0)):
+        r, A_log = torch.full((T, D), value, device="cuda"), torch.full((D,), A, device="cuda")
+        y, f = kda.kda_glr_fwd(x, r, A_log, None, None, init, cu)
+        assert torch.equal(f, init) and torch.equal(y, init.expand(T, D))  # nothing enters, nothing decays
+        g = kda.kda_glr_bwd(x, r, A_log, dy, None, None, init, init, cu)
+        assert all(bool(torch.isfinite(v).all()) for v in g if v is not None) and not g[0].any()
+    for value, A in ((1e30, 0.0), (float("inf"), 0.0), (5.0, 300.0), (5.0, float("inf"))):
+        r, A_log = torch.full((T, D), value, device="cuda"), torch.full((D,), A, device="cuda")
+        y, f = kda.kda_glr_fwd(x, r, A_log, None, None, init, cu)
+        assert torch.equal(y, x) and torch.equal(f[0], x[-1])
+        g = kda.kda_glr_bwd(x, r, A_log, dy, None, None, init, init, cu)
+        assert all(bool(torch.isfinite(v).all()) for v in g if v is not None)
+        assert torch.equal(g[0][:-1], dy[:-1]) and not g[1].any() and not g[5].any()
+
+
+@pytest.mark.parametrize("cu", [[0, 50, 20, 99], [-7, 5, 5, 1000], [9, 2, -3, 40], [400, 410, 410, 420], [0, 300, 10, 390]])
+def test_malformed_offsets_stay_in_bounds(cu):
+    """Offsets out of order or out of range are clamped: some result, in bounds, and it ends."""
+    d = _make([200, 100, 100], 16, torch.float32, 5)
+    off = torch.tensor(cu, dtype=torch.int32).cuda()
+    y, f = kda.kda_glr_fwd(d["x"], d["gate_x"], d["A_log"], d["dt_bias"], d["in_gate"], d["init"], off)
+    g = kda.kda_glr_bwd(d["x"], d["gate_x"], d["A_log"], d["dy"], d["dt_bias"], d["in_gate"], d["init"], d["dfinal"], off)
+    torch.cuda.synchronize()
+    assert y.shape == d["x"].shape and f.shape == d["init"].shape and g[0].shape == y.shape
+
+
+def test_large_offsets():
+    T, D, ld = 9, 8, 300_000_000
+    x = torch.empty(T * ld, dtype=torch.bfloat16, device="cuda").as_strided((T, D), (ld, 1))
+    x.copy_(torch.randn(T, D))
+    A, c = torch.randn(D, device="cuda"), x.contiguous()
+    cu = torch.tensor([0, 4, T], dtype=torch.int32, device="cuda")
+    assert torch.equal(kda.kda_glr_fwd(x, x, A, None, x, None, cu)[0], kda.kda_glr_fwd(c, c, A, None, c, None, cu)[0])
+    for a, b in zip(kda.kda_glr_bwd(x, x, A, x, None, x, None, None, cu), kda.kda_glr_bwd(c, c, A, c, None, c, None, None, cu)):
+        assert a is None or torch.equal(a, b)
+    assert torch.equal(kda.kda_glr_step(x, x, A, torch.ones(T, D, device="cuda")), kda.kda_glr_step(c, c, A, torch.ones(T, D, device="cuda")))
+
+
+@pytest.mark.parametrize("B,D,dtype,pad,in_gate,normalise", [(1, 1, "f32", 0, True, True), (5, 66, "bf16", 2, True, True),
+                                                             (3, 513, "bf16", 1, False, False), (64, 2048, "bf16", 0, True, False),
+                                                             (7, 300, "f32", 4, False, True)])
+def test_step(B, D, dtype, pad, in_gate, normalise):
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    d = _make([B], D, dt, B + D, in_gate=in_gate, pad=pad)
+    slots = torch.randperm(B + 3)[:B].to(torch.int32)
+    slots[B // 2] = -1 if B > 1 else slots[0]
+    if B > 2:
+        slots[0] = B + 3
+    pool = torch.randn(B + 3, D)
+    dev = pool.cuda()
+    y = kda.kda_glr_step(d["x"], d["gate_x"], d["A_log"], dev, d["dt_bias"], d["in_gate"], slots.cuda(), normalise)
+    h = {k: _value(v) for k, v in d.items()}
+    ref, tol, want, wtol = np.zeros((B, D)), np.zeros((B, D)), to64(pool).copy(), np.zeros((B + 3, D))
+    for n, s in enumerate(slots.tolist()):
+        if not 0 <= s < B + 3:
+            continue
+        one = slice(n, n + 1)
+        i = None if h["in_gate"] is None else h["in_gate"][one]
+        st = to64(pool)[s]
+        ref[n] = want[s] = glr(h["x"][one], h["gate_x"][one], h["A_log"], h["dt_bias"], i, st, normalise)[1]
+        tol[n] = wtol[s] = _bounds(h["x"][one], h["gate_x"][one], h["A_log"], h["dt_bias"], i, st, h["dy"][one], None, normalise)[1]
+    close(y, ref, HALF[dt] * np.abs(ref) + tol, "y")
+    close(dev, want, wtol, "pool")
+    # without slots request n uses slot n
+    a, b = pool.cuda(), pool.cuda()
+    ya = kda.kda_glr_step(d["x"], d["gate_x"], d["A_log"], a, d["dt_bias"], d["in_gate"], None, normalise)
+    yb = kda.kda_glr_step(d["x"], d["gate_x"], d["A_log"], b, d["dt_bias"], d["in_gate"],
+                          torch.arange(B, dtype=torch.int32, device="cuda"), normalise)
+    assert torch.equal(ya, yb) and torch.equal(a, b) and torch.equal(a[B:].cpu(), pool[B:])
+
+
+def test_repeats_bit_for_bit_on_a_side_stream_and_in_a_graph():
+    """Also two calls on two streams at once: each has a workspace of its own."""
+    d = _make([2700, 33, 1400], 300, torch.bfloat16, 6, rate=-4.0)
+
+    def run():
+        y, f, s = kda.kda_glr_fwd(d["x"], d["gate_x"], d["A_log"], d["dt_bias"], d["in_gate"], d["init"], d["cu"],
+                                  output_block_states=True)
+        return (y, f) + kda.kda_glr_bwd(d["x"], d["gate_x"], d["A_log"], d["dy"], d["dt_bias"], d["in_gate"], d["init"],
+                                        d["dfinal"], d["cu"], block_states=s)
+
+    ref = [t.clone() for t in run()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    both = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                both[i].append(run())
+    torch.cuda.synchronize()
+    for got in both[0] + both[1]:
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(3):
+        for t in got:
+            t.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        assert all(torch.equal(a, b) for a, b in zip(run(), ref))
