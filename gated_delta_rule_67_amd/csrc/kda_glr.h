@@ -46,22 +46,41 @@ hipError_t launch_glr_step(const GlrArgs& a, hipStream_t stream);
 
 namespace glr {
 
-// ---- Gates. Per channel: -exp(A_log) in units of log2 (an exp(A_log) above 2e38 counts as that, so
-// that the product is finite), and the bias.
+// ---- Gates. Per channel: -exp(A_log) (an exp(A_log) above 2e38 counts as that, so that products with
+// it and a constant are finite), and the bias in units of log2.
 struct Channel {
-  float neg_rate2, bias;
+  float neg_rate, bias2;
 };
+__device__ __forceinline__ Channel channel(float A_log, float dt_bias) {
+  const float rate = fast_exp2(A_log * kLog2e);
+  return {-(rate > 2.0e38f ? 2.0e38f : rate), dt_bias * kLog2e};
+}
 __device__ __forceinline__ Channel channel(const GlrArgs& a, int c) {
-  const float rate = expf(a.A_log[c]);
-  return {-(rate > 2.0e38f ? 2.0e38f : rate) * kLog2e, a.dt_bias ? a.dt_bias[c] : 0.f};
+  return channel(a.A_log[c], a.dt_bias ? a.dt_bias[c] : 0.f);
 }
 
-// log2 of the decay, g2 <= 0, for the gate's input; also what the softplus leaves for its slope, the
-// logistic of z. Held above -1e30, so that products with it stay finite (the decay is 0 long before).
+// log2 of the decay, g2 <= 0, for the gate's input; e = 2^-|z2| and u = fl(1 + e) are left for the
+// softplus' slope. With z2 = z log2 e, softplus(z) log2 e = max(z2, 0) + log2(1 + e), and the rounding d
+// of 1 + e is taken back at first order, log2(1 + e) = log2(u) - d log2 e (the factor 1 / u of that term
+// is left out: it is off by e d at most, under 2^-24 of the result), so that the value keeps its relative
+// accuracy however small e is.
+__device__ __forceinline__ float decay_log2(float x, const Channel& ch, float& z2, float& e, float& u) {
+  z2 = fmaf(x, kLog2e, ch.bias2);
+  e = fast_exp2(-fabsf(z2));
+  u = 1.f + e;
+  const float d = (u - 1.f) - e;
+  return ch.neg_rate * fmaf(d, -kLog2e, fmaxf(z2, 0.f) + __builtin_amdgcn_logf(u));
+}
+__device__ __forceinline__ float decay_log2(float x, const Channel& ch) {
+  float z2, e, u;
+  return decay_log2(x, ch, z2, e, u);
+}
+// The same held above -1e30, so that products with it stay finite (the decay is 0 long before), and the
+// slope of the softplus, logistic(z).
 __device__ __forceinline__ float decay_log2(float x, const Channel& ch, float& slope) {
-  float e, r;
-  const float z = x + ch.bias, g2 = ch.neg_rate2 * softplus_f32(z, e, r);
-  slope = logistic_from(z, e, r);
+  float z2, e, u;
+  const float g2 = decay_log2(x, ch, z2, e, u), r = __builtin_amdgcn_rcpf(u);
+  slope = z2 >= 0.f ? r : e * r;
   return g2 < -1e30f ? -1e30f : g2;
 }
 
@@ -70,13 +89,14 @@ __device__ __forceinline__ float sigmoid_fast(float z) {
   return __builtin_amdgcn_rcpf(1.f + fast_exp2(-z * kLog2e));
 }
 
-// sqrt(1 - a^2) for a = 2^g2. Near a = 1 the difference would cancel: there 1 - e^-v, v = -2 g ln 2,
-// by its series (relative error v^5 / 720 < 5e-8 at v = 1/8); elsewhere from a, whose last bit costs
+// sqrt(1 - a^2) for a = 2^g2. Near a = 1 the difference would cancel: there 1 - e^-v, v = -2 g2 ln 2, by
+// its series in g2 (relative error v^5 / 720 < 5e-8 at v = 1/8); elsewhere from a, whose last bit costs
 // 1e-6 at most.
 __device__ __forceinline__ float input_weight(float a, float g2) {
-  const float v = -2.f * kLn2 * g2;
-  const float p = v * fmaf(v, fmaf(v, fmaf(v, fmaf(v, 1.f / 120, -1.f / 24), 1.f / 6), -0.5f), 1.f);
-  return __builtin_amdgcn_sqrtf(v < 0.125f ? p : fmaf(-a, a, 1.f));
+  constexpr float k = -2.f * kLn2;
+  constexpr float c1 = k, c2 = -k * k / 2, c3 = k * k * k / 6, c4 = -k * k * k * k / 24, c5 = k * k * k * k * k / 120;
+  const float p = g2 * fmaf(g2, fmaf(g2, fmaf(g2, fmaf(g2, c5, c4), c3), c2), c1);
+  return __builtin_amdgcn_sqrtf(g2 > -0.125f / (2.f * kLn2) ? p : fmaf(-a, a, 1.f));
 }
 
 // ---- Work. A workgroup's tile is kWaves consecutive spans of tokens (one a wave) by 64 VEC channels
@@ -87,22 +107,26 @@ __device__ __forceinline__ float input_weight(float a, float g2) {
 // behind it as soon as it has them, the last tile of every kGroup leaves the state behind it, and a
 // tile gathers the state in front of it from the state behind the previous group and the (A, B) of its
 // own group's tiles in front of it, always folded in the same order: results do not depend on timing.
-// Workgroups take their tiles from a counter, in the order of q. So a tile waits only for tiles whose
-// workgroups have started before its own; (A, B) waits for nothing, and the state behind a group only
-// for those and for the state behind the group in front: every wait ends.
+// Workgroups take their tiles from a counter and work on them one after the other. A tile waits only for
+// tiles of its column that come before it in the counter's order, so the first one that is not finished
+// never waits for one that is not: every wait ends, however many workgroups run at a time.
 //
 // A word that is not there yet is all ones, which no value that is stored has (NaN is stored as
 // 0x7fc00000 where it could be mistaken): value and presence arrive together, in one relaxed atomic
 // access of the whole device (the XCDs' L2 caches are not coherent for plain ones).
+//
+// One more wave of the workgroup does this (the chain wave), while the others load their next tile: a wave's loads
+// return in order, so a wave with a tile's loads in flight would see an answer only after them.
 constexpr int kGroup = 8;
 constexpr unsigned kAbsent = 0xffffffffu;
-constexpr int kPolls = 1 << 22;  // of one word at most (seconds): then NaN, so that every wave ends
+constexpr int kPolls = 1 << 20;  // of the words in front of a tile at most (about a second): then NaN
 
 struct Chain {
   unsigned* ticket;    // counter
   uint64_t* map;       // [nq][D]: A in the upper, B in the lower half
   unsigned* state;     // [groups][D]
   int nq, ncol;        // tiles along the tokens, columns of tiles
+  int side, per;       // the order of tiles: `side` sequences of `per` tiles each side by side
 };
 
 inline int groups_of(int nq) { return (nq + kGroup - 1) / kGroup; }
@@ -111,9 +135,30 @@ inline size_t map_bytes(int nq, int D) { return round_up((size_t)nq * D * 8); }
 inline size_t chain_bytes(int nq, int D) {
   return nq <= 1 ? 0 : 256 + map_bytes(nq, D) + round_up((size_t)groups_of(nq) * D * 4);
 }
-// The chain in `workspace` (chain_bytes), and a launch that readies it.
-Chain make_chain(void* workspace, int nq, int ncol, int D);
-hipError_t launch_ready_chain(const Chain& c, int D, hipStream_t stream);
+// The chain in `workspace` (chain_bytes) over tiles of `tile` tokens.
+inline Chain make_chain(const GlrArgs& a, void* workspace, int tile, int width) {
+  Chain c{};
+  c.nq = (int)(((int64_t)a.T + tile - 1) / tile), c.ncol = (a.D + width - 1) / width;
+  c.side = 1, c.per = c.nq;
+  if (c.nq <= 1) return c;
+  // equal sequences of whole tiles do not depend on each other: side by side, each has the workgroups in
+  // flight reach less far, and waits less
+  if (!a.seqs.cu && a.seqs.len % tile == 0) c.side = a.N, c.per = c.nq / a.N;
+  unsigned char* p = static_cast<unsigned char*>(workspace);
+  c.ticket = reinterpret_cast<unsigned*>(p);
+  c.map = reinterpret_cast<uint64_t*>(p + 256);
+  c.state = reinterpret_cast<unsigned*>(p + 256 + map_bytes(c.nq, a.D));
+  return c;
+}
+// Readies the chain, and passes the states of sequences without tokens through (from: init or dfinal, or
+// null: zeros; to: final or dinit, or null).
+hipError_t launch_ready(const GlrArgs& a, const Chain& c, const float* from, float* to, hipStream_t stream);
+
+// Workgroups of a launch: `per_cu` of them, as many as run at a time, or one a tile if those are fewer.
+inline unsigned chain_blocks(const Chain& c, int per_cu) {
+  const int64_t tiles = (int64_t)c.nq * c.ncol;
+  return (unsigned)(c.nq <= 1 || tiles < per_cu * 256 ? tiles : per_cu * 256);
+}
 
 __device__ __forceinline__ unsigned stored_bits(float x) { return x != x ? 0x7fc00000u : __float_as_uint(x); }
 
@@ -124,47 +169,115 @@ __device__ __forceinline__ void put_map(const Chain& c, int q, int D, int col, f
 __device__ __forceinline__ void put_state(const Chain& c, int group, int D, int col, float h) {
   __hip_atomic_store(c.state + (size_t)group * D + col, stored_bits(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void wait_map(const Chain& c, int q, int D, int col, float& A, float& B) {
-  uint64_t w;
+
+// The state in front of tile q, whose sequence reaches back to tile q0 < q: its own tile (q0) when that is
+// in q's group, else the state behind the group in front; then the maps of the tiles between, in order.
+template <int VEC>
+__device__ __forceinline__ void wait_front(const Chain& c, int q, int q0, int D, int col, float (&front)[VEC]) {
+  const int group = q / kGroup, group0 = group * kGroup, from = max(q0, group0), count = q - from;
+  const bool far = q0 < group0;
+  uint64_t w[kGroup - 1][VEC];
+  unsigned s[VEC];
   for (int i = 0; i < kPolls; ++i) {
-    w = __hip_atomic_load(c.map + (size_t)q * D + col, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if ((unsigned)(w >> 32) != kAbsent) break;
+    bool here = true;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      s[e] = far ? __hip_atomic_load(c.state + (size_t)(group - 1) * D + col + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+#pragma unroll
+    for (int k = 0; k < kGroup - 1; ++k)
+      if (k < count) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          w[k][e] = __hip_atomic_load(c.map + (size_t)(from + k) * D + col + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) here = here && s[e] != kAbsent;
+#pragma unroll
+    for (int k = 0; k < kGroup - 1; ++k)
+      if (k < count) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) here = here && (unsigned)(w[k][e] >> 32) != kAbsent;
+      }
+    if (!wave_any(!here)) break;
     __builtin_amdgcn_s_sleep(1);
   }
-  A = __uint_as_float((unsigned)(w >> 32));  // still absent: all ones is a NaN
-  B = __uint_as_float((unsigned)w);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) front[e] = __uint_as_float(s[e]);  // still absent: all ones is a NaN
+#pragma unroll
+  for (int k = 0; k < kGroup - 1; ++k)
+    if (k < count) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float A = __uint_as_float((unsigned)(w[k][e] >> 32)), B = __uint_as_float((unsigned)w[k][e]);
+        // what was in front of the tile where the sequence began does not reach it
+        front[e] = k == 0 && !far ? B : fmaf(A, front[e], B);
+      }
+    }
 }
-__device__ __forceinline__ float wait_state(const Chain& c, int group, int D, int col) {
-  unsigned w;
-  for (int i = 0; i < kPolls; ++i) {
-    w = __hip_atomic_load(c.state + (size_t)group * D + col, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (w != kAbsent) break;
-    __builtin_amdgcn_s_sleep(1);
+
+// A tile as the chain wave finds it for the other waves: its place along the tokens, its column, and the
+// sequence [bos, eos] that its first (forward) or last (backward) token lies in (as `around`).
+struct Tile {
+  int q, column;  // q = nq: none is left
+  int bos, eos;
+};
+// The chain wave's next tile: by the counter where tiles wait for each other, else by its index.
+__device__ __forceinline__ int take(const Chain& c, bool first) {
+  if (c.nq <= 1) return first ? blockIdx.x : c.ncol;  // a workgroup a tile
+  int tile = 0;
+  if (__lane_id() == 0) tile = (int)__hip_atomic_fetch_add(c.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return __builtin_amdgcn_readfirstlane(tile);
+}
+// Place along the tokens (nq behind the last tile) and column of a tile.
+__device__ __forceinline__ void place_of(const Chain& c, int tile, int& q, int& column) {
+  const int i = tile / c.ncol;
+  column = tile - i * c.ncol;
+  q = i >= c.nq ? c.nq : c.side == 1 ? i : (i % c.side) * c.per + i / c.side;
+}
+// A tile through LDS, written by one lane.
+__device__ __forceinline__ void publish(Tile* s, const Tile& t) {
+  if (__lane_id() == 0) *s = t;
+}
+__device__ __forceinline__ Tile read(const Tile* s) {
+  return {__builtin_amdgcn_readfirstlane(s->q), __builtin_amdgcn_readfirstlane(s->column),
+          __builtin_amdgcn_readfirstlane(s->bos), __builtin_amdgcn_readfirstlane(s->eos)};
+}
+
+// VEC channels a lane in LDS.
+template <int VEC> struct Lanes {
+  typename RowVec<float, VEC>::type v[64];
+  __device__ __forceinline__ void get(int lane, float (&f)[VEC]) const {
+    const typename RowVec<float, VEC>::type t = v[lane];
+    if constexpr (VEC == 1) f[0] = t;
+    else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) f[e] = t[e];
+    }
   }
-  return __uint_as_float(w);
-}
-
-// This workgroup's tile: by the counter where tiles wait for each other, else by its index.
-__device__ __forceinline__ int take_tile(const Chain& c, int* shared) {
-  if (c.nq <= 1) return blockIdx.x;
-  if (threadIdx.x == 0) *shared = (int)__hip_atomic_fetch_add(c.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  block_barrier();
-  return __builtin_amdgcn_readfirstlane(*shared);
-}
-
-constexpr int kSeqs = 16;  // sequences a wave looks at for ones without tokens
+  __device__ __forceinline__ void set(int lane, const float (&f)[VEC]) {
+    typename RowVec<float, VEC>::type t;
+    if constexpr (VEC == 1) t = f[0];
+    else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) t[e] = f[e];
+    }
+    v[lane] = t;
+  }
+};
 
 // Which tokens of a wave's span begin or end a sequence, or lie in one: bit j is token t0 + j.
 struct Marks {
   unsigned start, end, valid;
-  int first;  // a sequence at or in front of the first one that is met in the span
+  int first;     // a sequence at or in front of the first one that is met in the span
+  int bos, eos;  // the first token of the sequence that the first token lies in (that token, if in none),
+                 // and the last token of the one that the last token lies in (that token, if in none)
 };
 __device__ __forceinline__ unsigned bits_between(int lo, int hi) {  // [lo, hi), hi - lo >= 1, hi <= 32
   return (0xffffffffu >> (32 - (hi - lo))) << lo;
 }
-// Every lane takes part. t0 < T.
+// Every lane takes part. 1 <= n <= 32 tokens from t0, in [0, T).
 __device__ __forceinline__ Marks marks_of(const Sequences& s, int t0, int n) {
-  Marks m{0, 0, 0, s.find(t0)};
+  Marks m{0, 0, 0, s.find(t0), t0, t0 + n - 1};
   for (int i = m.first; i < s.N; ++i) {
     const Span p = s.span(i);
     if (p.bos >= t0 + n) break;
@@ -173,8 +286,15 @@ __device__ __forceinline__ Marks marks_of(const Sequences& s, int t0, int n) {
     m.valid |= bits_between(lo - t0, hi - t0);
     if (p.bos >= t0) m.start |= 1u << (p.bos - t0);
     if (p.eos <= t0 + n) m.end |= 1u << (p.eos - 1 - t0);
+    if (lo == t0) m.bos = p.bos;
+    if (hi == t0 + n) m.eos = p.eos - 1;
   }
   return m;
+}
+// The sequence that token t lies in, as its first and last tokens; t itself where it lies in none.
+__device__ __forceinline__ Span around(const Sequences& s, int t) {
+  const Span p = s.span(s.find(t));
+  return p.bos <= t && p.eos > t ? Span{p.bos, p.eos - 1} : Span{t, t};
 }
 // The sequence at or behind `i` whose first (last) token is t; N where there is none.
 __device__ __forceinline__ int starting_at(const Sequences& s, int i, int t) {

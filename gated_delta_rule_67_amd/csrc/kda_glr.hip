@@ -5,10 +5,11 @@
 //
 // About 30 operations an element, six of them transcendental (16 cycles a wave each, the others 4), and
 // 8 bytes in bf16: the vector ALU needs about two thirds of the time that HBM does, so the gates are
-// computed once and every tensor moves once. A wave holds a span of tokens for 64 VEC channels in
-// registers: the states from zero, and the products of decays with which the state in front of the
-// span enters them. That state comes through the waves of the workgroup and the chain of tiles
-// (kda_glr.h).
+// computed once and every tensor moves once. A wave holds a span of tokens for 64 VEC channels: the states
+// from zero in registers, and in LDS the products of decays with which the state in front of the span
+// enters them. That state comes through the waves of the workgroup and the chain of tiles (kda_glr.h); the
+// chain's waiting is covered by the next tile, whose loads are under way and whose states from zero are
+// computed before the outputs of this one.
 #include <type_traits>
 
 #include "kda_glr.h"
@@ -18,102 +19,181 @@ namespace glr {
 
 constexpr int kReadyThreads = 256;
 
-__global__ __launch_bounds__(kReadyThreads) void ready_kernel(Chain c, int64_t words) {
-  const int64_t i = (int64_t)blockIdx.x * kReadyThreads + threadIdx.x;
-  if (i == 0) *c.ticket = 0;
-  // the maps and the states lie behind each other: 16 bytes a thread
+// A thread clears 16 bytes of the chain or copies a channel of a sequence without tokens.
+__global__ __launch_bounds__(kReadyThreads) void ready_kernel(GlrArgs a, Chain c, int64_t words, const float* from, float* to,
+                                                              int64_t channels) {
+  int64_t i = (int64_t)blockIdx.x * kReadyThreads + threadIdx.x;
+  if (c.nq > 1 && i == 0) *c.ticket = 0;
+  // the maps and the states lie behind each other
   if (i < words) reinterpret_cast<uint4*>(c.map)[i] = make_uint4(kAbsent, kAbsent, kAbsent, kAbsent);
+  if (i < channels) {
+    const int n = (int)(i / a.D);
+    int bos = 0, eos = 0;  // T = 0: none has tokens
+    if (a.seqs.cu) {
+      bos = min(max(a.seqs.cu[n], 0), a.T);
+      eos = min(max(a.seqs.cu[n + 1], bos), a.T);
+    }
+    if (eos == bos) to[i] = from ? from[i] : 0.f;
+  }
 }
 
-Chain make_chain(void* workspace, int nq, int ncol, int D) {
-  Chain c{};
-  c.nq = nq, c.ncol = ncol;
-  if (nq <= 1) return c;
-  unsigned char* p = static_cast<unsigned char*>(workspace);
-  c.ticket = reinterpret_cast<unsigned*>(p);
-  c.map = reinterpret_cast<uint64_t*>(p + 256);
-  c.state = reinterpret_cast<unsigned*>(p + 256 + map_bytes(nq, D));
-  return c;
-}
-
-hipError_t launch_ready_chain(const Chain& c, int D, hipStream_t stream) {
-  if (c.nq <= 1) return hipSuccess;
-  const int64_t words = (int64_t)(chain_bytes(c.nq, D) - 256) / 16;
-  hipLaunchKernelGGL(ready_kernel, dim3((unsigned)((words + kReadyThreads - 1) / kReadyThreads)),
-                     dim3(kReadyThreads), 0, stream, c, words);
+hipError_t launch_ready(const GlrArgs& a, const Chain& c, const float* from, float* to, hipStream_t stream) {
+  const int64_t words = c.nq <= 1 ? 0 : (int64_t)(chain_bytes(c.nq, a.D) - 256) / 16;
+  const int64_t channels = to && (a.seqs.cu || a.T == 0) ? (int64_t)a.N * a.D : 0;
+  const int64_t n = words > channels ? words : channels;
+  if (n == 0) return hipSuccess;
+  hipLaunchKernelGGL(ready_kernel, dim3((unsigned)((n + kReadyThreads - 1) / kReadyThreads)), dim3(kReadyThreads), 0,
+                     stream, a, c, words, from, to, channels);
   return hipGetLastError();
 }
 
-// Sequences without tokens: a chunk of kSeqs a wave.
-template <int VEC, int WAVES>
-__device__ __forceinline__ void empty_sequences(const GlrArgs& a, int chunk, int col, const float* from, float* to) {
-  const int wave = threadIdx.x / 64;
-  for (int i = 0; i < kSeqs; ++i) {
-    const int n = (chunk * kSeqs + i) * WAVES + wave;
-    if (n >= a.N) return;
-    const Span s = a.seqs.span(n);
-    if (s.eos > s.bos) continue;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      if (col + e < a.D) to[(int64_t)n * a.D + col + e] = from ? from[(int64_t)n * a.D + col + e] : 0.f;
-  }
-}
-
-constexpr int kFwdTokens = 16, kFwdWaves = 8;  // a wave's span, waves of a workgroup
+constexpr int kFwdTokens = 8, kFwdWaves = 15;  // a wave's span, spans of a tile
 constexpr int kFwdTile = kFwdTokens * kFwdWaves;
-static_assert(kGlrBlock % kFwdTokens == 0 && kFwdTile % kGlrBlock == 0, "a block's first token begins a span");
+static_assert(kGlrBlock % kFwdTokens == 0, "a block's first token begins a span");
 
 template <typename T, int VEC, bool CK, bool GATE, bool NORM>
-__global__ __launch_bounds__(64 * kFwdWaves, 4) void fwd_kernel(GlrArgs a, Chain chain, int ntiles) {
+__global__ __launch_bounds__(64 * (kFwdWaves + 1)) void fwd_kernel(GlrArgs a, Chain chain) {
   constexpr int NT = kFwdTokens, NW = kFwdWaves, C = 64 * VEC;
   constexpr unsigned kFull = 0xffffffffu >> (32 - NT);
   typedef typename KeptPiece<T, VEC, CK>::type piece;
-  __shared__ float s_wave[NW][2][C];       // a span's map
-  __shared__ float s_tile[kGroup][2][C];   // the maps of the group's tiles in front; slot kGroup - 1: the
-                                           // state in front of the group in its first row
-  __shared__ int s_index;
-  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  const int tile = take_tile(chain, &s_index);
-  const bool extra = tile >= ntiles;
-  const int index = extra ? tile - ntiles : tile;
-  const int q = index / chain.ncol, k0 = (index - q * chain.ncol) * C + lane * VEC;
-  if (extra) {
-    empty_sequences<VEC, NW>(a, q, k0, a.init, a.final);
+  // Of this turn's tile and of the one before: the spans' maps, which the chain wave replaces by the maps
+  // from the tile's front to each span's, and whether a sequence begins in them; the state in front of the
+  // tile; the products of decays (the last of a span in registers: two workgroups fit a CU's LDS).
+  __shared__ Lanes<VEC> s_map[2][NW][2], s_front[2], s_decay[2][NW][NT - 1];
+  __shared__ int s_begins[2][NW];
+  __shared__ Tile s_next[2];  // the tile of the turn after next; first, those of the first two
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, k0 = lane * VEC;
+
+  if (wave == NW) {  // the chain wave: one barrier a turn, as in the other waves' loop
+    auto find = [&](bool first) {
+      Tile t;
+      place_of(chain, take(chain, first), t.q, t.column);
+      const Span s = t.q < chain.nq ? around(a.seqs, t.q * kFwdTile) : Span{0, 0};
+      t.bos = s.bos, t.eos = s.eos;
+      return t;
+    };
+    Tile tile = find(true), next = find(false);
+    publish(&s_next[0], tile);
+    publish(&s_next[1], next);
+    lds_barrier();
+    if (tile.q >= chain.nq) return;  // every tile is taken
+    lds_barrier();                   // both have been read
+    for (int turn = 0;; turn ^= 1) {
+      const Tile later = find(false);
+      publish(&s_next[turn], later);
+      lds_barrier();
+      const int q = tile.q, tile0 = q * kFwdTile;
+      const bool there = tile.column * C + k0 < a.D;
+      const int col = there ? tile.column * C + k0 : a.D - VEC;
+      float A[VEC], B[VEC], front[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) A[e] = 1.f, B[e] = front[e] = 0.f;
+      bool begins = false;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        float p[VEC], h[VEC];
+        s_map[turn][i][0].get(lane, p);
+        s_map[turn][i][1].get(lane, h);
+        s_map[turn][i][0].set(lane, A);
+        s_map[turn][i][1].set(lane, B);
+        const bool here = s_begins[turn][i];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          B[e] = here ? h[e] : fmaf(p[e], B[e], h[e]);
+          A[e] *= p[e];
+        }
+        begins = begins || here;
+      }
+      if (chain.nq > 1) {
+        if (there && q + 1 < chain.nq) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) put_map(chain, q, a.D, col + e, A[e], B[e]);
+        }
+        if (tile.bos < tile0) wait_front<VEC>(chain, q, tile.bos / kFwdTile, a.D, col, front);
+        if (there && q + 1 < chain.nq && q % kGroup == kGroup - 1) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            put_state(chain, q / kGroup, a.D, col + e, begins ? B[e] : fmaf(A[e], front[e], B[e]));
+        }
+      }
+      s_front[turn].set(lane, front);
+      if (next.q >= chain.nq) break;
+      tile = next;
+      next = later;
+    }
+    lds_barrier();
     return;
   }
-  const bool active = k0 < a.D;            // D is a multiple of VEC
-  const int col = active ? k0 : a.D - VEC;
-  const int tile0 = q * kFwdTile, t0 = __builtin_amdgcn_readfirstlane(tile0 + wave * NT);
-  const int count = min(max(a.T - t0, 0), NT);
 
-  piece x[NT], r[NT], in[NT];
+  // This wave's part of a tile: first token, tokens, first channel (one that is there, for reading), the
+  // sequences in it.
+  struct Part {
+    int t0, count, col;
+    bool there;
+    Marks m;
+  };
+  auto part = [&](const Tile& t) {
+    Part p;
+    p.t0 = t.q * kFwdTile + wave * NT;
+    p.count = min(max(a.T - p.t0, 0), NT);
+    p.col = t.column * C + k0;
+    p.there = p.col < a.D;  // D is a multiple of VEC
+    if (!p.there) p.col = a.D - VEC;
+    const int tile0 = t.q * kFwdTile;
+    if (t.bos < tile0 && t.eos >= tile0 + kFwdTile) p.m = Marks{0, 0, kFull, 0, t.bos, t.eos};
+    else if (p.count > 0) p.m = marks_of(a.seqs, p.t0, p.count);
+    else p.m = Marks{};
+    return p;
+  };
+  // A part's inputs: two of these take turns, so that a tile's loads are under way while the one in front
+  // of it is worked on.
+  struct Raw {
+    piece x[NT], r[NT], in[NT];
+    float rate[VEC], bias[VEC];  // A_log and dt_bias
+    Part at;
+  };
+  auto fetch = [&](Raw& w, const Part& p) {
+    w.at = p;
+    // (loads without a condition: the wave does not wait for them here)
+    const float* bias = a.dt_bias ? a.dt_bias : a.A_log;
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t t = min(t0 + j, a.T - 1);
-    r[j].load(a.r, t * a.r.ld + col);
-    x[j].load(a.x, t * a.x.ld + col);
-    if constexpr (GATE) in[j].load(a.in, t * a.in.ld + col);
-  }
-  Channel ch[VEC];
+    for (int e = 0; e < VEC; ++e) {
+      w.rate[e] = a.A_log[p.col + e];
+      w.bias[e] = bias[p.col + e];
+    }
+    // rows that are there: the last one again behind the last token
+    const int rows = max(p.count, 1), t = min(p.t0, a.T - 1);
+    const Rows rx = piece::rows(a.x, t, rows, a.D), rr = piece::rows(a.r, t, rows, a.D);
+    const Rows ri = piece::rows(GATE ? a.in : a.x, t, rows, a.D);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) ch[e] = channel(a, col + e);
-  Marks m{0, 0, 0, 0};
-  if (count > 0) m = marks_of(a.seqs, t0, count);
-
-  float h[NT][VEC], p[NT][VEC];  // states from zero in front of the span; products of its decays
-  {
+    for (int j = 0; j < NT; ++j) {
+      const int row = min(j, rows - 1);
+      w.r[j].load(rr, row, p.col);
+      w.x[j].load(rx, row, p.col);
+      if constexpr (GATE) w.in[j].load(ri, row, p.col);
+    }
+  };
+  // A span's states from zero in front of it, the product of its decays, and where it lies.
+  struct Local {
+    float h[NT][VEC], decay[VEC];
+    Part at;
+  };
+  auto local = [&](const Raw& w, Local& l, int turn) {
+    l.at = w.at;
+    const Marks& m = l.at.m;
+    Channel ch[VEC];
     float hs[VEC], ps[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) hs[e] = 0.f, ps[e] = 1.f;
+    for (int e = 0; e < VEC; ++e) ch[e] = channel(w.rate[e], a.dt_bias ? w.bias[e] : 0.f), hs[e] = 0.f, ps[e] = 1.f;
     auto token = [&](int j, float (&av)[VEC], float (&bv)[VEC]) {
       float xv[VEC], rv[VEC], iv[VEC];
-      x[j].get(xv);
-      r[j].get(rv);
-      if constexpr (GATE) in[j].get(iv);
+      w.x[j].get(xv);
+      w.r[j].get(rv);
+      if constexpr (GATE) w.in[j].get(iv);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        float slope, b = xv[e];
-        const float g2 = decay_log2(rv[e], ch[e], slope);
+        float b = xv[e];
+        const float g2 = decay_log2(rv[e], ch[e]);
         av[e] = fast_exp2(g2);
         if constexpr (GATE) b *= sigmoid_fast(iv[e]);
         if constexpr (NORM) b *= input_weight(av[e], g2);
@@ -127,9 +207,10 @@ __global__ __launch_bounds__(64 * kFwdWaves, 4) void fwd_kernel(GlrArgs a, Chain
         token(j, av, bv);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          h[j][e] = hs[e] = fmaf(av[e], hs[e], bv[e]);
-          p[j][e] = ps[e] = ps[e] * av[e];
+          l.h[j][e] = hs[e] = fmaf(av[e], hs[e], bv[e]);
+          ps[e] *= av[e];
         }
+        if (j < NT - 1) s_decay[turn][wave][j].set(lane, ps);
       }
     } else {
       int n = m.first;
@@ -138,10 +219,10 @@ __global__ __launch_bounds__(64 * kFwdWaves, 4) void fwd_kernel(GlrArgs a, Chain
         float av[VEC], bv[VEC];
         token(j, av, bv);
         if (m.start >> j & 1) {
-          n = starting_at(a.seqs, n, t0 + j);
+          n = starting_at(a.seqs, n, l.at.t0 + j);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            const float first = a.init && n < a.N ? a.init[(int64_t)n * a.D + col + e] : 0.f;
+            const float first = a.init && n < a.N ? a.init[(int64_t)n * a.D + l.at.col + e] : 0.f;
             hs[e] = fmaf(av[e], first, bv[e]);
           }
         } else if (m.valid >> j & 1) {
@@ -152,173 +233,131 @@ __global__ __launch_bounds__(64 * kFwdWaves, 4) void fwd_kernel(GlrArgs a, Chain
           }
         }
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) h[j][e] = hs[e], p[j][e] = ps[e];
+        for (int e = 0; e < VEC; ++e) l.h[j][e] = hs[e];
+        if (j < NT - 1) s_decay[turn][wave][j].set(lane, ps);
       }
     }
+    s_map[turn][wave][0].set(lane, ps);
+    s_map[turn][wave][1].set(lane, hs);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      s_wave[wave][0][lane * VEC + e] = ps[e];
-      s_wave[wave][1][lane * VEC + e] = hs[e];
-    }
-  }
-  lds_barrier();
-  // The sequence that holds a token, if it began in front of it: where it began. Else the token.
-  auto began = [&](int t) {
-    const Span s = a.seqs.span(a.seqs.find(t));
-    return s.bos < t && s.eos > t ? s.bos : t;
+    for (int e = 0; e < VEC; ++e) l.decay[e] = ps[e];
+    if (lane == 0) s_begins[turn][wave] = m.start != 0;
   };
-  const bool whole = chain.nq > 1;
-  const int tile_bos = began(tile0);
-  // Folds the spans [from, to) of this tile behind the state c (to: wave-uniform).
-  auto fold = [&](float (&c)[VEC], int from, int to) {
-    for (int i = from; i < to; ++i)
+  // Outputs of a tile, once the chain wave knows what is in front of it.
+  auto finish = [&](Local& l, int turn) {
+    const Part& at = l.at;
+    const Marks& m = at.m;
+    if (at.count == 0 || !at.there) return;
+    float c[VEC], A[VEC], B[VEC];
+    s_front[turn].get(lane, c);
+    s_map[turn][wave][0].get(lane, A);
+    s_map[turn][wave][1].get(lane, B);
+    const bool inside = m.bos >= at.t0 - wave * NT;  // the sequence in front of the span began in this tile
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) c[e] = fmaf(s_wave[i][0][lane * VEC + e], c[e], s_wave[i][1][lane * VEC + e]);
-  };
-  // The state in front of this wave's span, given the tile's.
-  const int span_bos = count > 0 ? began(t0) : t0;
-  auto span_state = [&](float (&c)[VEC], const float (&front)[VEC]) {
-    if (span_bos >= t0) {
+    for (int e = 0; e < VEC; ++e) c[e] = m.bos >= at.t0 ? 0.f : inside ? B[e] : fmaf(A[e], c[e], B[e]);
+    if (a.states && at.t0 % kGlrBlock == 0) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) c[e] = 0.f;
-    } else if (span_bos >= tile0) {
-      const int i = (span_bos - tile0) / NT;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) c[e] = s_wave[i][1][lane * VEC + e];
-      fold(c, i + 1, wave);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) c[e] = front[e];
-      fold(c, 0, wave);
+      for (int e = 0; e < VEC; ++e) a.states[(int64_t)(at.t0 / kGlrBlock) * a.D + at.col + e] = c[e];
     }
-  };
-  // The last sequence that a token of this tile lies in: did it begin in the tile?
-  const int last = min(tile0 + kFwdTile, a.T) - 1, last_bos = began(last);
-  const bool resets = last_bos >= tile0;
-  const int last_wave = (last - tile0) / NT;
-  auto behind = [&](float (&c)[VEC], const float (&front)[VEC]) {  // the state behind the tile
-    if (resets) {
-      const int i = (last_bos - tile0) / NT;
+    auto decays = [&](int j, float (&p)[VEC]) {
+      if (j < NT - 1) s_decay[turn][wave][j].get(lane, p);
+      else
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) c[e] = s_wave[i][1][lane * VEC + e];
-      fold(c, i + 1, last_wave + 1);
-    } else {
+        for (int e = 0; e < VEC; ++e) p[e] = l.decay[e];
+    };
+    const Rows y = Piece<T, VEC>::rows(a.y, a.D, at.t0, at.count, a.D);
+    if (m.start == 0 && m.valid == kFull) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) c[e] = front[e];
-      fold(c, 0, last_wave + 1);
-    }
-  };
-  float front[VEC];
+      for (int j = 0; j < NT; ++j) {
+        float p[VEC];
+        decays(j, p);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) front[e] = 0.f;
-  const int group = q / kGroup, group0 = group * kGroup;
-  if (whole) {
-    if (wave == NW - 1 && active && q + 1 < chain.nq) {
-      float A[VEC], B[VEC];
+        for (int e = 0; e < VEC; ++e) l.h[j][e] = fmaf(p[e], c[e], l.h[j][e]);
+      }
+      if (a.y) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) A[e] = 1.f;
-      for (int i = 0; i <= last_wave; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) A[e] *= s_wave[i][0][lane * VEC + e];
-      behind(B, front);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) put_map(chain, q, a.D, col + e, A[e], B[e]);
-    }
-    if (tile_bos < tile0) {  // the state in front comes from other tiles
-      const int q0 = tile_bos / kFwdTile, from = max(q0, group0);
-      static_assert(NW >= kGroup, "a wave for every tile of a group");
-      if (wave < q - from) {
-        float A, B;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          wait_map(chain, from + wave, a.D, col + e, A, B);
-          s_tile[wave][0][lane * VEC + e] = A;
-          s_tile[wave][1][lane * VEC + e] = B;
+        for (int j = 0; j < NT; ++j) {
+          Piece<T, VEC> o;
+          o.set(l.h[j]);
+          o.store(y, j, at.col);
         }
-      } else if (wave == kGroup - 1 && q0 < group0) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          s_tile[kGroup - 1][0][lane * VEC + e] = wait_state(chain, group - 1, a.D, col + e);
       }
-      lds_barrier();
-      int i = 0;
-      if (q0 < group0) {
+    } else {
+      unsigned begun = 0;  // a sequence has begun in the span
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) front[e] = s_tile[kGroup - 1][0][lane * VEC + e];
-      } else {  // the sequence began in this tile: its state does not depend on what was in front
+      for (int j = 0; j < NT; ++j) {
+        begun |= m.start >> j & 1;
+        const bool lies = m.valid >> j & 1;
+        float p[VEC];
+        decays(j, p);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) front[e] = s_tile[0][1][lane * VEC + e];
-        i = 1;
+        for (int e = 0; e < VEC; ++e) l.h[j][e] = !lies ? 0.f : begun ? l.h[j][e] : fmaf(p[e], c[e], l.h[j][e]);
+        if (a.y && j < at.count && (lies || a.zero_rest)) {
+          Piece<T, VEC> o;
+          o.set(l.h[j]);
+          o.store(y, j, at.col);
+        }
       }
-      for (; i < q - from; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) front[e] = fmaf(s_tile[i][0][lane * VEC + e], front[e], s_tile[i][1][lane * VEC + e]);
     }
-    if (wave == NW - 1 && active && q + 1 < chain.nq && q - group0 == kGroup - 1) {
-      float c[VEC];
-      behind(c, front);
+    if (!a.final) return;
+    int n = m.first;
+    for (unsigned left = m.end; left; left &= left - 1) {
+      const int last = __builtin_ctz(left);
+      n = ending_at(a.seqs, n, at.t0 + last);
+      if (n >= a.N) break;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) put_state(chain, group, a.D, col + e, c[e]);
+      for (int j = 0; j < NT; ++j)
+        if (j == last) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) a.final[(int64_t)n * a.D + at.col + e] = l.h[j][e];
+        }
     }
-  }
-  if (count == 0 || !active) return;
-  float c[VEC];
-  span_state(c, front);
-  if (a.states && t0 % kGlrBlock == 0) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) a.states[(int64_t)(t0 / kGlrBlock) * a.D + col + e] = c[e];
-  }
-  T* y = static_cast<T*>(a.y) + (int64_t)t0 * a.D + col;
-  auto put = [&](int j, const float (&v)[VEC]) {
-    Piece<T, VEC> o;
-    o.set(v);
-    o.store(y, (int64_t)j * a.D);
   };
-  if (m.start == 0 && m.valid == kFull) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) h[j][e] = fmaf(p[j][e], c[e], h[j][e]);
-      if (a.y) put(j, h[j]);
-    }
-  } else {
-    unsigned begun = 0;  // a sequence has begun in the span
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      begun |= m.start >> j & 1;
-      const bool lies = m.valid >> j & 1;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) h[j][e] = !lies ? 0.f : begun ? h[j][e] : fmaf(p[j][e], c[e], h[j][e]);
-      if (a.y && j < count && (lies || a.zero_rest)) put(j, h[j]);
-    }
-  }
-  if (!a.final) return;
-  int n = m.first;
-  for (unsigned left = m.end; left; left &= left - 1) {
-    const int at = __builtin_ctz(left);
-    n = ending_at(a.seqs, n, t0 + at);
-    if (n >= a.N) break;
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      if (j == at) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) a.final[(int64_t)n * a.D + col + e] = h[j][e];
-      }
+  // A turn: the states of its tile from zero, then, behind the barrier, the outputs of the tile before and the loads
+  // of the tile after next. False where the next turn has no tile (this one's outputs are done then, too).
+  // Loads are issued where no tile is left, too (of row 0): a wave waits for its loads by counting the ones
+  // behind them, and where some might not be there it would wait for all.
+  Local before;
+  bool later = false;
+  auto fetch_tile = [&](Raw& w, const Tile& t) {
+    const bool left = t.q < chain.nq;
+    Part p;
+    p.t0 = 0, p.count = 1, p.col = min(k0, a.D - VEC), p.there = false, p.m = Marks{};
+    if (left) p = part(t);
+    fetch(w, p);
+    if (!left) w.at.count = -1;
+  };
+  auto step = [&](Raw& w, const Raw& next, int turn) {
+    Local now;
+    local(w, now, turn);
+    lds_barrier();
+    const Tile t = read(&s_next[turn]);
+    if (later) finish(before, turn ^ 1);
+    before = now;
+    later = true;
+    fetch_tile(w, t);
+    if (next.at.count >= 0) return true;
+    lds_barrier();
+    finish(before, turn);
+    return false;
+  };
+  lds_barrier();
+  const Tile t0 = read(&s_next[0]), t1 = read(&s_next[1]);
+  if (t0.q >= chain.nq) return;
+  lds_barrier();
+  Raw even, odd;
+  fetch_tile(even, t0);
+  fetch_tile(odd, t1);
+  while (step(even, odd, 0) && step(odd, even, 1)) {
   }
 }
 
 template <typename T, int VEC, bool CK, bool GATE, bool NORM>
 hipError_t run_fwd(const GlrArgs& a, void* workspace, hipStream_t stream) {
-  const int nq = (a.T + kFwdTile - 1) / kFwdTile, ncol = (a.D + 64 * VEC - 1) / (64 * VEC);
-  const Chain c = make_chain(workspace, nq, ncol, a.D);
-  hipError_t e = launch_ready_chain(c, a.D, stream);
-  if (e != hipSuccess) return e;
-  // sequences without tokens are looked for where there may be any
-  const int chunks = a.final && (a.seqs.cu || a.T == 0) ? (a.N + kSeqs * kFwdWaves - 1) / (kSeqs * kFwdWaves) : 0;
-  const int64_t blocks = (int64_t)(nq + chunks) * ncol;
-  if (blocks == 0) return hipSuccess;
-  hipLaunchKernelGGL((fwd_kernel<T, VEC, CK, GATE, NORM>), dim3((unsigned)blocks), dim3(64 * kFwdWaves), 0, stream, a, c,
-                     nq * ncol);
+  const Chain c = make_chain(a, workspace, kFwdTile, 64 * VEC);
+  const hipError_t e = launch_ready(a, c, a.init, a.final, stream);
+  if (e != hipSuccess || c.nq == 0) return e;
+  hipLaunchKernelGGL((fwd_kernel<T, VEC, CK, GATE, NORM>), dim3(chain_blocks(c, 1)), dim3(64 * (kFwdWaves + 1)), 0, stream, a, c);
   return hipGetLastError();
 }
 
@@ -348,8 +387,8 @@ __global__ __launch_bounds__(kStepThreads) void step_kernel(GlrArgs a, int ncol)
     if constexpr (GATE) in.get(iv);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      float slope, b = xv[e];
-      const float g2 = decay_log2(rv[e], channel(a, col + e), slope), av = fast_exp2(g2);
+      float b = xv[e];
+      const float g2 = decay_log2(rv[e], channel(a, col + e)), av = fast_exp2(g2);
       if constexpr (GATE) b *= sigmoid_fast(iv[e]);
       if constexpr (NORM) b *= input_weight(av, g2);
       y[e] = fmaf(av, h[e], b);

@@ -18,359 +18,385 @@ namespace kda {
 namespace glr {
 
 constexpr int kBwdTokens = 8, kBwdWaves = 8;
+constexpr int kAtOnce = 2;
 constexpr int kBwdTile = kBwdTokens * kBwdWaves;
 static_assert(kBwdTile == kGlrBlock, "a tile begins at a kept state");
 
 template <typename T, int VEC, bool CK, bool GATE, bool NORM>
-__global__ __launch_bounds__(64 * kBwdWaves) void bwd_kernel(GlrArgs a, Chain chain, int ntiles) {
+__global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Chain chain) {
   constexpr int NT = kBwdTokens, NW = kBwdWaves, C = 64 * VEC;
   constexpr unsigned kFull = 0xffffffffu >> (32 - NT);
   typedef typename KeptPiece<T, VEC, CK>::type kept;
   typedef Piece<T, VEC> piece;
-  __shared__ float s_wave[NW][3][C];      // a span's decays, its state and its gradient, each from zero
-  __shared__ float s_tile[kGroup][2][C];  // as in the forward kernel
-  __shared__ int s_index;
-  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  const int tile = take_tile(chain, &s_index);
-  const bool extra = tile >= ntiles;
-  const int index = extra ? tile - ntiles : tile;
-  const int q = index / chain.ncol, k0 = (index - q * chain.ncol) * C + lane * VEC;
-  if (extra) {  // sequences without tokens: the final state's gradient passes through
-    for (int i = 0; i < kSeqs; ++i) {
-      const int n = (q * kSeqs + i) * NW + wave;
-      if (n >= a.N) return;
-      const Span s = a.seqs.span(n);
-      if (s.eos > s.bos) continue;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (k0 + e < a.D) a.dinit[(int64_t)n * a.D + k0 + e] = a.dfinal ? a.dfinal[(int64_t)n * a.D + k0 + e] : 0.f;
-    }
-    return;
-  }
-  const bool active = k0 < a.D;
-  const int col = active ? k0 : a.D - VEC;
-  const int block = chain.nq - 1 - q;  // of tokens
-  const int tile0 = block * kBwdTile, t0 = __builtin_amdgcn_readfirstlane(tile0 + wave * NT);
-  const int count = min(max(a.T - t0, 0), NT);
+  // A span's decays, its state and its gradient, each from zero, and whether a sequence ends in it; the map
+  // (decays, gradient) from behind the tile to behind each span; the gradient that reaches the tile from
+  // behind; a span's sums of dA_log and ddt_bias.
+  __shared__ Lanes<VEC> s_map[NW][3], s_behind[NW][2], s_front, s_sum[NW][2];
+  __shared__ Lanes<VEC> s_held[NW][GATE ? 2 : 1][NT];  // what the outputs need and nothing in between (registers are scarce)
+  __shared__ int s_ends[NW];
+  __shared__ Tile s_next;  // the next turn's tile; first, this turn's
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, k0 = lane * VEC;
+  // tiles are counted against the tokens
+  auto first_token = [&](int q) { return (chain.nq - 1 - q) * kBwdTile; };
 
-  kept xk[NT], rk[NT], ik[NT];
-  piece gk[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t t = min(t0 + j, a.T - 1);
-    rk[j].load(a.r, t * a.r.ld + col);
-    xk[j].load(a.x, t * a.x.ld + col);
-    if constexpr (GATE) ik[j].load(a.in, t * a.in.ld + col);
-    gk[j].load(a.dy, t * a.dy.ld + col);
-  }
-  Channel ch[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) ch[e] = channel(a, col + e);
-  Marks m{0, 0, 0, 0};
-  if (count > 0) m = marks_of(a.seqs, t0, count);
-  const bool whole = m.valid == kFull && !m.start && !m.end;  // inside one sequence
-
-  // Per element: decay, its log2, input weight, input gate and one minus it, slope of the softplus
-  float av[NT][VEC], g2[NT][VEC], w[NT][VEC], s[NT][VEC], rest[NT][VEC], slope[NT][VEC];
-  float A[VEC], hs[VEC], rs[VEC];
-  auto input = [&](int j, float (&b)[VEC]) {  // w s x
-    xk[j].get(b);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      if constexpr (GATE) b[e] *= s[j][e];
-      if constexpr (NORM) b[e] *= w[j][e];
-    }
-  };
-  auto first_state = [&](int n, int e) { return a.init && n < a.N ? a.init[(int64_t)n * a.D + col + e] : 0.f; };
-  auto last_grad = [&](int n, int e) { return a.dfinal && n < a.N ? a.dfinal[(int64_t)n * a.D + col + e] : 0.f; };
-  // The states of the span behind hs, one token at a time: each(j) comes before token j.
-  auto states = [&](auto&& each) {
-    if (whole) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        each(j);
-        float b[VEC];
-        input(j, b);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) hs[e] = fmaf(av[j][e], hs[e], b[e]);
+  if (wave == NW) {  // the chain wave: two barriers a turn, as in the other waves' loop
+    auto find = [&](bool first) {
+      Tile t;
+      place_of(chain, take(chain, first), t.q, t.column);
+      t.bos = t.eos = 0;
+      if (t.q < chain.nq) {
+        const Span s = around(a.seqs, min(first_token(t.q) + kBwdTile, a.T) - 1);
+        t.bos = s.bos, t.eos = s.eos;
       }
-      return;
-    }
-    int n = m.first;
+      return t;
+    };
+    auto sums = [&](const Tile& t) {  // of a tile whose sums have been left, in order of the spans
+      const int col = t.column * C + k0;
+      float dA[VEC], db[VEC];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if (m.start >> j & 1) {
-        n = starting_at(a.seqs, n, t0 + j);
+      for (int e = 0; e < VEC; ++e) dA[e] = db[e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) hs[e] = first_state(n, e);
+      for (int i = 0; i < NW; ++i) {
+        float u[VEC], v[VEC];
+        s_sum[i][0].get(lane, u);
+        s_sum[i][1].get(lane, v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dA[e] += u[e], db[e] += v[e];
       }
-      each(j);
-      float b[VEC];
-      input(j, b);
-      if (m.valid >> j & 1) {
+      float* out = a.part + (size_t)(chain.nq - 1 - t.q) * 2 * a.D + col;
+      if (col < a.D) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) hs[e] = fmaf(av[j][e], hs[e], b[e]);
+        for (int e = 0; e < VEC; ++e) out[e] = dA[e] * kLn2, out[a.D + e] = db[e];
       }
-    }
-  };
-  // The sequences whose last tokens lie in the span, from the last one on: one at a time, against the tokens.
-  // (offsets do not decrease, so the walk begins at the span's first sequence each time)
-  auto grads = [&](auto&& each) {
+    };
+    Tile tile = find(true), before{};
+    publish(&s_next, tile);
+    lds_barrier();
+    if (tile.q >= chain.nq) return;  // every tile is taken
+    lds_barrier();
+    bool later = false;
+    for (;;) {
+      const Tile next = find(false);
+      publish(&s_next, next);
+      lds_barrier();
+      const int q = tile.q, last = min(first_token(q) + kBwdTile, a.T) - 1;
+      const bool there = tile.column * C + k0 < a.D;
+      const int col = there ? tile.column * C + k0 : a.D - VEC;
+      float A[VEC], B[VEC], front[VEC];
 #pragma unroll
-    for (int j = NT - 1; j >= 0; --j) {
-      if (!whole && (m.end >> j & 1)) {
-        const int n = ending_at(a.seqs, m.first, t0 + j);
+      for (int e = 0; e < VEC; ++e) A[e] = 1.f, B[e] = front[e] = 0.f;
+      bool ends = false;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) rs[e] = last_grad(n, e);
-      }
-      each(j);
-    }
-  };
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    float rv[VEC], iv[VEC];
-    rk[j].get(rv);
-    if constexpr (GATE) ik[j].get(iv);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      g2[j][e] = decay_log2(rv[e], ch[e], slope[j][e]);
-      av[j][e] = fast_exp2(g2[j][e]);
-      if constexpr (NORM) w[j][e] = input_weight(av[j][e], g2[j][e]);
-      if constexpr (GATE) logistic_pair(iv[e], s[j][e], rest[j][e]);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) A[e] = 1.f, hs[e] = rs[e] = 0.f;
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-    if (whole || (m.valid >> j & 1)) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) A[e] *= av[j][e];
-    }
-  states([](int) {});
-  grads([&](int j) {
-    if (whole || (m.valid >> j & 1)) {
-      float dy[VEC];
-      gk[j].get(dy);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) rs[e] = av[j][e] * (dy[e] + rs[e]);
-    }
-  });
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    s_wave[wave][0][lane * VEC + e] = A[e];
-    s_wave[wave][1][lane * VEC + e] = hs[e];
-    s_wave[wave][2][lane * VEC + e] = rs[e];
-  }
-  lds_barrier();
-  // Where the sequence that holds a token began, if in front of it, and its last token, if behind it;
-  // else the token itself.
-  auto around = [&](int t) {
-    const Span p = a.seqs.span(a.seqs.find(t));
-    return p.bos <= t && p.eos > t ? Span{p.bos, p.eos - 1} : Span{t, t};
-  };
-  const int last = min(tile0 + kBwdTile, a.T) - 1, last_wave = (last - tile0) / NT;
-  const Span at_first = around(tile0), at_last = around(last);
-  const int span_last = count > 0 ? t0 + count - 1 : t0;
-  const int span_bos = count > 0 ? around(t0).bos : t0, span_end = count > 0 ? around(span_last).eos : t0;
-  // ---- the state in front of the span
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) hs[e] = 0.f;
-  if (span_bos < t0) {
-    int i = 0;
-    if (span_bos >= tile0) {
-      i = (span_bos - tile0) / NT;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) hs[e] = s_wave[i][1][lane * VEC + e];
-      ++i;
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) hs[e] = a.states[(int64_t)block * a.D + col + e];
-    }
-    for (; i < wave; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) hs[e] = fmaf(s_wave[i][0][lane * VEC + e], hs[e], s_wave[i][1][lane * VEC + e]);
-  }
-  // ---- the gradient behind the tile, by the chain
-  auto fold = [&](float (&c)[VEC], int from, int to) {  // spans from, from - 1, ..., to
-    for (int i = from; i >= to; --i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) c[e] = fmaf(s_wave[i][0][lane * VEC + e], c[e], s_wave[i][2][lane * VEC + e]);
-  };
-  // From behind the last sequence that ends at token `end` of this tile, or from `front`, to span `to`.
-  auto gather = [&](float (&c)[VEC], int end, int to, const float (&front)[VEC]) {
-    int i = last_wave;
-    if (end <= last) {
-      i = (end - tile0) / NT;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) c[e] = s_wave[i][2][lane * VEC + e];
-      --i;
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) c[e] = front[e];
-    }
-    fold(c, i, to);
-  };
-  float front[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) front[e] = 0.f;
-  if (chain.nq > 1) {
-    const int group = q / kGroup, group0 = group * kGroup;
-    if (wave == NW - 1 && active && q + 1 < chain.nq) {
-      float P[VEC], B[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) P[e] = 1.f;
-      for (int i = 0; i <= last_wave; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) P[e] *= s_wave[i][0][lane * VEC + e];
-      gather(B, at_first.eos, 0, front);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) put_map(chain, q, a.D, col + e, P[e], B[e]);
-    }
-    if (at_last.eos > last) {
-      const int q0 = chain.nq - 1 - at_last.eos / kBwdTile, from = max(q0, group0);
-      static_assert(NW >= kGroup, "a wave for every tile of a group");
-      if (wave < q - from) {
-        float P, B;
+      for (int i = NW - 1; i >= 0; --i) {
+        float p[VEC], r[VEC];
+        s_map[i][0].get(lane, p);
+        s_map[i][2].get(lane, r);
+        s_behind[i][0].set(lane, A);
+        s_behind[i][1].set(lane, B);
+        const bool here = s_ends[i];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          wait_map(chain, from + wave, a.D, col + e, P, B);
-          s_tile[wave][0][lane * VEC + e] = P;
-          s_tile[wave][1][lane * VEC + e] = B;
+          B[e] = here ? r[e] : fmaf(p[e], B[e], r[e]);
+          A[e] *= p[e];
         }
-      } else if (wave == kGroup - 1 && q0 < group0) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          s_tile[kGroup - 1][0][lane * VEC + e] = wait_state(chain, group - 1, a.D, col + e);
+        ends = ends || here;
       }
+      if (chain.nq > 1) {
+        if (there && q + 1 < chain.nq) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) put_map(chain, q, a.D, col + e, A[e], B[e]);
+        }
+        if (tile.eos > last) wait_front<VEC>(chain, q, chain.nq - 1 - tile.eos / kBwdTile, a.D, col, front);
+        if (there && q + 1 < chain.nq && q % kGroup == kGroup - 1) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            put_state(chain, q / kGroup, a.D, col + e, ends ? B[e] : fmaf(A[e], front[e], B[e]));
+        }
+      }
+      s_front.set(lane, front);
+      if (a.part && later) sums(before);
       lds_barrier();
-      int i = 0;
-      if (q0 < group0) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) front[e] = s_tile[kGroup - 1][0][lane * VEC + e];
-      } else {  // the sequence ends in this tile
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) front[e] = s_tile[0][1][lane * VEC + e];
-        i = 1;
-      }
-      for (; i < q - from; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) front[e] = fmaf(s_tile[i][0][lane * VEC + e], front[e], s_tile[i][1][lane * VEC + e]);
+      before = tile;
+      later = true;
+      if (next.q >= chain.nq) break;
+      tile = next;
     }
-    if (wave == NW - 1 && active && q + 1 < chain.nq && q - group0 == kGroup - 1) {
-      float c[VEC];
-      gather(c, at_first.eos, 0, front);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) put_state(chain, group, a.D, col + e, c[e]);
-    }
+    lds_barrier();
+    if (a.part) sums(before);
+    return;
   }
-  if (span_end > span_last) gather(rs, span_end, wave + 1, front);
-  else {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) rs[e] = 0.f;
-  }
-  // ---- the span's gradients
-  float hp[NT][VEC], dA[VEC], db[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) dA[e] = db[e] = 0.f;
-  states([&](int j) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) hp[j][e] = hs[e];
-  });
-  grads([&](int j) {
-    if (!whole && !(m.valid >> j & 1)) return;
-    float x[VEC], dy[VEC], dx[VEC], dr[VEC], di[VEC];
-    xk[j].get(x);
-    gk[j].get(dy);
+
+  struct Part {
+    int t0, count, col;
+    bool there;
+    Marks m;
+  };
+  auto part = [&](const Tile& t) {
+    Part p;
+    const int tile0 = first_token(t.q);
+    p.t0 = tile0 + wave * NT;
+    p.count = min(max(a.T - p.t0, 0), NT);
+    p.col = t.column * C + k0;
+    p.there = p.col < a.D;
+    if (!p.there) p.col = a.D - VEC;
+    if (t.bos < tile0 && t.eos >= tile0 + kBwdTile) p.m = Marks{0, 0, kFull, 0, t.bos, t.eos};
+    else if (p.count > 0) p.m = marks_of(a.seqs, p.t0, p.count);
+    else p.m = Marks{};
+    return p;
+  };
+  kept xk[NT], rk[NT], ik[NT];
+  piece gk[NT];
+  float rate[VEC], bias[VEC];
+  Part at;
+  auto fetch = [&](const Part& p) {
+    at = p;
+    const float* db = a.dt_bias ? a.dt_bias : a.A_log;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const float G = dy[e] + rs[e], back = av[j][e] * G;
-      float gs = G, qx = x[e];  // G s, s x
-      if constexpr (GATE) gs *= s[j][e], qx *= s[j][e];
-      float dg = back * hp[j][e];
-      if constexpr (NORM) {
-        const float ratio = w[j][e] > 0.f ? av[j][e] * __builtin_amdgcn_rcpf(w[j][e]) : 0.f;
-        dg = fmaf(-back * qx, ratio, dg);
-        gs *= w[j][e];
-      }
-      dx[e] = gs;
-      if constexpr (GATE) di[e] = gs * x[e] * rest[j][e];
-      dr[e] = ch[e].neg_rate2 * kLn2 * slope[j][e] * dg;
-      dA[e] = fmaf(dg, g2[j][e], dA[e]);
-      db[e] += dr[e];
-      rs[e] = back;
+      rate[e] = a.A_log[p.col + e];
+      bias[e] = db[p.col + e];
     }
-    if (active) {
-      const int64_t off = (int64_t)(t0 + j) * a.D + col;
-      piece o;
-      o.set(dx);
-      o.store(a.dx, off);
-      o.set(dr);
-      o.store(a.dr, off);
-      if constexpr (GATE) {
-        o.set(di);
-        o.store(a.din, off);
-      }
-      if (a.dinit && (m.start >> j & 1)) {
-        const int n = starting_at(a.seqs, m.first, t0 + j);
-        if (n < a.N) {
+    const int rows = max(p.count, 1), t = min(p.t0, a.T - 1);
+    const Rows rx = kept::rows(a.x, t, rows, a.D), rr = kept::rows(a.r, t, rows, a.D);
+    const Rows ri = kept::rows(GATE ? a.in : a.x, t, rows, a.D), rg = piece::rows(a.dy, t, rows, a.D);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) a.dinit[(int64_t)n * a.D + col + e] = rs[e];
+    for (int j = 0; j < NT; ++j) {
+      const int row = min(j, rows - 1);
+      rk[j].load(rr, row, p.col);
+      xk[j].load(rx, row, p.col);
+      if constexpr (GATE) ik[j].load(ri, row, p.col);
+      gk[j].load(rg, row, p.col);
+    }
+  };
+  lds_barrier();
+  {
+    const Tile first = read(&s_next);
+    if (first.q >= chain.nq) return;
+    lds_barrier();
+    fetch(part(first));
+  }
+  for (;;) {
+    // Of every element: decay, and what makes the gradients from G, which the phases below complete:
+    // dx = cx G, din_gate = ci G, dgate_x = cr G, dA_log's term ca G.
+    float av[NT][VEC], cr[NT][VEC], ca[NT][VEC];
+    float hs[VEC], rs[VEC];
+    piece dy[NT];
+    const Part now = at;
+    const Marks& m = now.m;
+    const bool whole = m.valid == kFull && !m.start && !m.end;  // inside one sequence
+    // The state along the span, one token at a time: each(j) comes before token j, input(j) is w s x.
+    // (inside, here and below: the span lies inside one sequence, known when compiled: no branches then)
+    auto states = [&](auto inside, auto&& input, auto&& each) {
+      constexpr bool W = decltype(inside)::value;
+      int n = m.first;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (!W && (m.start >> j & 1)) {
+          n = starting_at(a.seqs, n, now.t0 + j);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) hs[e] = a.init && n < a.N ? a.init[(int64_t)n * a.D + now.col + e] : 0.f;
+        }
+        each(j);
+        if (W || (m.valid >> j & 1)) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) hs[e] = fmaf(av[j][e], hs[e], input(j, e));
         }
       }
-    }
-  });
-  if (a.zero_rest && !whole && active) {  // tokens in no sequence
-    piece o;
-    float zero[VEC];
+    };
+    // The gradient against the tokens: each(j) takes it over token j.
+    auto grads = [&](auto inside, auto&& each) {
+      constexpr bool W = decltype(inside)::value;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) zero[e] = 0.f;
-    o.set(zero);
-    for (int j = 0; j < count; ++j) {
-      if (m.valid >> j & 1) continue;
-      const int64_t off = (int64_t)(t0 + j) * a.D + col;
-      o.store(a.dx, off);
-      o.store(a.dr, off);
-      if constexpr (GATE) o.store(a.din, off);
-    }
-  }
-  if (!a.part) return;
-  // ---- the tile's sums, spans in order
-  lds_barrier();  // the spans' maps have been read
+      for (int j = NT - 1; j >= 0; --j) {
+        if (!W && (m.end >> j & 1)) {  // the walk begins at the span's first sequence each time
+          const int n = ending_at(a.seqs, m.first, now.t0 + j);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    s_wave[wave][0][lane * VEC + e] = dA[e] * kLn2;
-    s_wave[wave][1][lane * VEC + e] = db[e];
+          for (int e = 0; e < VEC; ++e) rs[e] = a.dfinal && n < a.N ? a.dfinal[(int64_t)n * a.D + now.col + e] : 0.f;
+        }
+        if (W || (m.valid >> j & 1)) each(j);
+      }
+    };
+    // ---- the span's maps; ca holds log2 of the decay, cr the gate's slope, and:
+    float b[NT][VEC], tw[NT][VEC];  // w s x; s x a / w
+    auto gates = [&](auto inside) {
+      constexpr bool W = decltype(inside)::value;
+      Channel ch[VEC];
+      float A[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) ch[e] = channel(rate[e], a.dt_bias ? bias[e] : 0.f), A[e] = 1.f, hs[e] = rs[e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float rv[VEC], iv[VEC], xv[VEC], cx[VEC], ci[VEC];
+        dy[j] = gk[j];
+        rk[j].get(rv);
+        xk[j].get(xv);
+        if constexpr (GATE) ik[j].get(iv);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float slope, s = 1.f, rest = 0.f;
+          const float g2 = decay_log2(rv[e], ch[e], slope), d = fast_exp2(g2);
+          if constexpr (GATE) logistic_pair(iv[e], s, rest);
+          float q = s * xv[e], w = 1.f;
+          if constexpr (NORM) {
+            w = input_weight(d, g2);
+            tw[j][e] = w > 0.f ? q * d * __builtin_amdgcn_rcpf(w) : 0.f;
+          }
+          cx[e] = s * w;
+          b[j][e] = q * w;
+          ci[e] = b[j][e] * rest;
+          cr[j][e] = ch[e].neg_rate * slope;
+          ca[j][e] = g2;
+          av[j][e] = d;
+        }
+        if constexpr (GATE || NORM) s_held[wave][0][j].set(lane, cx);
+        if constexpr (GATE) s_held[wave][1][j].set(lane, ci);
+        if (W || (m.valid >> j & 1)) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) A[e] *= av[j][e];
+        }
+        // a few elements at a time: the gates of all at once would need registers that are not there
+        if (j % kAtOnce == kAtOnce - 1) __builtin_amdgcn_sched_barrier(0);
+      }
+      states(inside, [&](int j, int e) { return b[j][e]; }, [](int) {});
+      grads(inside, [&](int j) {
+        float d[VEC];
+        dy[j].get(d);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) rs[e] = av[j][e] * (d[e] + rs[e]);
+      });
+      s_map[wave][0].set(lane, A);
+      s_map[wave][1].set(lane, hs);
+      s_map[wave][2].set(lane, rs);
+      if (lane == 0) s_ends[wave] = m.end != 0;
+    };
+    whole ? gates(std::true_type{}) : gates(std::false_type{});
+    lds_barrier();
+    const Tile next = read(&s_next);
+    // ---- the states in front of the tokens, while the chain wave waits: dg = G a (h_{t-1} - s x a / w)
+    const int tile0 = now.t0 - wave * NT;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) hs[e] = 0.f;
+    if (now.count > 0 && m.bos < now.t0) {
+      const bool inside = m.bos >= tile0;
+      int i = inside ? (m.bos - tile0) / NT : 0;
+      if (inside) s_map[i][1].get(lane, hs);
+      else
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) hs[e] = a.states[(int64_t)(tile0 / kBwdTile) * a.D + now.col + e];
+      for (i += inside; i < wave; ++i) {
+        float p[VEC], h[VEC];
+        s_map[i][0].get(lane, p);
+        s_map[i][1].get(lane, h);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) hs[e] = fmaf(p[e], hs[e], h[e]);
+      }
+    }
+    auto slopes = [&](auto inside) {
+      states(inside, [&](int j, int e) { return b[j][e]; }, [&](int j) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float d = hs[e];
+          if constexpr (NORM) d -= tw[j][e];
+          d *= av[j][e];
+          cr[j][e] *= d;
+          ca[j][e] *= d;
+        }
+      });
+    };
+    whole ? slopes(std::true_type{}) : slopes(std::false_type{});
+    __builtin_amdgcn_sched_barrier(0);
+    // (row 0 where no tile is left: the registers are then not the old values' any more)
+    const bool more = next.q < chain.nq;
+    Part p;
+    p.t0 = 0, p.count = 1, p.col = min(k0, a.D - VEC), p.there = false, p.m = Marks{};
+    if (more) p = part(next);
+    fetch(p);
+    lds_barrier();
+    // ---- gradients
+    float dA[VEC], db[VEC];
+    {
+      float A[VEC], B[VEC], front[VEC];
+      s_front.get(lane, front);
+      s_behind[wave][0].get(lane, A);
+      s_behind[wave][1].get(lane, B);
+      const int span_last = now.t0 + now.count - 1, last = min(tile0 + kBwdTile, a.T) - 1;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        rs[e] = now.count == 0 || m.eos <= span_last ? 0.f : m.eos <= last ? B[e] : fmaf(A[e], front[e], B[e]);
+        dA[e] = db[e] = 0.f;
+      }
+    }
+    const Rows ox = piece::rows(a.dx, a.D, now.t0, now.count, a.D), orr = piece::rows(a.dr, a.D, now.t0, now.count, a.D);
+    const Rows oi = piece::rows(GATE ? a.din : a.dx, a.D, now.t0, now.count, a.D);
+    auto outputs = [&](auto inside) {
+     grads(inside, [&](int j) {
+      float d[VEC], dx[VEC], dr[VEC], di[VEC], cx[VEC], ci[VEC];
+      dy[j].get(d);
+      if constexpr (GATE || NORM) s_held[wave][0][j].get(lane, cx);
+      if constexpr (GATE) s_held[wave][1][j].get(lane, ci);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float G = d[e] + rs[e];
+        dx[e] = GATE || NORM ? cx[e] * G : G;
+        if constexpr (GATE) di[e] = ci[e] * G;
+        dr[e] = cr[j][e] * G;
+        dA[e] = fmaf(ca[j][e], G, dA[e]);
+        db[e] += dr[e];
+        rs[e] = av[j][e] * G;
+      }
+      if (now.there) {
+        piece o;
+        o.set(dx);
+        o.store(ox, j, now.col);
+        o.set(dr);
+        o.store(orr, j, now.col);
+        if constexpr (GATE) {
+          o.set(di);
+          o.store(oi, j, now.col);
+        }
+        if (!decltype(inside)::value && a.dinit && (m.start >> j & 1)) {
+          const int n = starting_at(a.seqs, m.first, now.t0 + j);
+          if (n < a.N) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) a.dinit[(int64_t)n * a.D + now.col + e] = rs[e];
+          }
+        }
+      }
+     });
+    };
+    whole ? outputs(std::true_type{}) : outputs(std::false_type{});
+    if (a.zero_rest && !whole && now.there) {  // tokens in no sequence
+      piece o;
+      float zero[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) zero[e] = 0.f;
+      o.set(zero);
+      for (int j = 0; j < now.count; ++j) {
+        if (m.valid >> j & 1) continue;
+        o.store(ox, j, now.col);
+        o.store(orr, j, now.col);
+        if constexpr (GATE) o.store(oi, j, now.col);
+      }
+    }
+    s_sum[wave][0].set(lane, dA);
+    s_sum[wave][1].set(lane, db);
+    if (!more) break;
   }
   lds_barrier();
-  if (wave < 2 && active) {
-    float* part = a.part + ((size_t)block * 2 + wave) * a.D + col;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < NW; ++i) sum += s_wave[i][wave][lane * VEC + e];
-      part[e] = sum;
-    }
-  }
 }
 
 template <typename T, int VEC, bool CK, bool GATE, bool NORM>
 hipError_t run_bwd(const GlrArgs& a, void* workspace, hipStream_t stream) {
-  const int nq = (a.T + kBwdTile - 1) / kBwdTile, ncol = (a.D + 64 * VEC - 1) / (64 * VEC);
-  const Chain c = make_chain(workspace, nq, ncol, a.D);
-  hipError_t e = launch_ready_chain(c, a.D, stream);
+  const Chain c = make_chain(a, workspace, kBwdTile, 64 * VEC);
+  hipError_t e = launch_ready(a, c, a.dfinal, a.dinit, stream);
   if (e != hipSuccess) return e;
-  const int chunks = a.dinit && (a.seqs.cu || a.T == 0) ? (a.N + kSeqs * kBwdWaves - 1) / (kSeqs * kBwdWaves) : 0;
-  const int64_t blocks = (int64_t)(nq + chunks) * ncol;
-  if (blocks > 0) {
-    hipLaunchKernelGGL((bwd_kernel<T, VEC, CK, GATE, NORM>), dim3((unsigned)blocks), dim3(64 * kBwdWaves), 0, stream, a,
-                       c, nq * ncol);
+  if (c.nq > 0) {
+    hipLaunchKernelGGL((bwd_kernel<T, VEC, CK, GATE, NORM>), dim3(chain_blocks(c, 1)), dim3(64 * (kBwdWaves + 1)), 0, stream,
+                       a, c);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (!a.part && nq > 0) return e;
   if (!a.dA_log && !a.ddt_bias) return e;
-  return launch_column_sums({a.part, {a.dA_log, a.ddt_bias}, nq, 2, a.D}, stream);
+  return launch_column_sums({a.part, {a.dA_log, a.ddt_bias}, c.nq, 2, a.D}, stream);
 }
 
 }  // namespace glr

@@ -15,6 +15,17 @@ struct Source {
 
 constexpr int kScaleBlock = 32;  // neighbours that share a scale
 
+// Rows of a Source from some token on, for buffer accesses: a row's offset is scalar, a lane's column the
+// vector part. Offsets stay below 2^31: no more rows than that are asked for.
+struct Rows {
+  __amdgpu_buffer_rsrc_t p, scales;
+  int ld, ld_scales;  // bytes between rows
+};
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const void* p, int64_t first, int64_t bytes) {
+  char* q = const_cast<char*>(static_cast<const char*>(p)) + first;
+  return __builtin_amdgcn_make_buffer_rsrc(q, 0, (int)bytes, 0x00020000);
+}
+
 // 2^(byte - 127), the scale that a checkpoint's byte stands for (byte <= 254; 0 is 2^-127).
 __device__ __forceinline__ float scale_of(unsigned byte) {
   return __uint_as_float(byte ? byte << 23 : 1u << 22);
@@ -33,6 +44,25 @@ template <typename T, int VEC> struct Piece {
     raw = *reinterpret_cast<const typename RowVec<T, VEC>::type*>(static_cast<const T*>(p) + off);
   }
   __device__ __forceinline__ void load(const Source& s, int64_t off) { load(s.p, off); }
+  // `rows` rows of D columns from `token` on, and a lane's piece of one (row uniform over the wave).
+  static __device__ __forceinline__ Rows rows(const void* p, int64_t ld, int64_t token, int rows, int D) {
+    const int64_t step = ld * (int64_t)sizeof(T);
+    Rows r;
+    r.p = rows_at(p, token * step, (rows - 1) * step + D * (int64_t)sizeof(T));
+    r.ld = (int)step;
+    return r;
+  }
+  static __device__ __forceinline__ Rows rows(const Source& s, int64_t token, int n, int D) { return rows(s.p, s.ld, token, n, D); }
+  __device__ __forceinline__ void load(const Rows& r, int row, int col) {
+    const int off = col * (int)sizeof(T);
+    if constexpr (sizeof(raw) == 4) raw = __builtin_bit_cast(decltype(raw), __builtin_amdgcn_raw_buffer_load_b32(r.p, off, row * r.ld, 0));
+    else raw = __builtin_bit_cast(decltype(raw), __builtin_amdgcn_raw_buffer_load_b16(r.p, off, row * r.ld, 0));
+  }
+  __device__ __forceinline__ void store(const Rows& r, int row, int col) const {
+    const int off = col * (int)sizeof(T);
+    if constexpr (sizeof(raw) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, raw), r.p, off, row * r.ld, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, raw), r.p, off, row * r.ld, 0);
+  }
   __device__ __forceinline__ void get(float (&v)[VEC]) const {
     if constexpr (VEC == 1) v[0] = to_f32(raw);
     else {
@@ -49,9 +79,6 @@ template <typename T, int VEC> struct Piece {
   }
   __device__ __forceinline__ void store(void* p, int64_t off) const {
     *reinterpret_cast<typename RowVec<T, VEC>::type*>(static_cast<T*>(p) + off) = raw;
-  }
-  __device__ __forceinline__ void store_stream(void* p, int64_t off) const {
-    __builtin_nontemporal_store(raw, reinterpret_cast<typename RowVec<T, VEC>::type*>(static_cast<T*>(p) + off));
   }
 };
 
@@ -70,6 +97,20 @@ template <int VEC> struct PackedPiece {
     else if constexpr (VEC == 2) word[0] = *reinterpret_cast<const unsigned short*>(c);
     else word[0] = *c;
     byte = s.scales[off / kScaleBlock];
+  }
+  static __device__ __forceinline__ Rows rows(const Source& s, int64_t token, int n, int D) {
+    const int64_t few = s.ld / kScaleBlock;
+    Rows r;
+    r.p = rows_at(s.p, token * s.ld, (n - 1) * s.ld + D);
+    r.scales = rows_at(s.scales, token * few, n * few);
+    r.ld = (int)s.ld, r.ld_scales = (int)few;
+    return r;
+  }
+  __device__ __forceinline__ void load(const Rows& r, int row, int col) {
+    static_assert(VEC <= 2, "the recurrence reads one or two channels a lane");
+    if constexpr (VEC == 2) word[0] = __builtin_amdgcn_raw_buffer_load_b16(r.p, col, row * r.ld, 0);
+    else word[0] = __builtin_amdgcn_raw_buffer_load_b8(r.p, col, row * r.ld, 0);
+    byte = __builtin_amdgcn_raw_buffer_load_b8(r.scales, col / kScaleBlock, row * r.ld_scales, 0);
   }
   __device__ __forceinline__ void get(float (&v)[VEC]) const {
     const float f = scale_of(byte);
