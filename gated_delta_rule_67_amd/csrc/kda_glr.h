@@ -178,28 +178,40 @@ __device__ __forceinline__ void wait_front(const Chain& c, int q, int q0, int D,
   const bool far = q0 < group0;
   uint64_t w[kGroup - 1][VEC];
   unsigned s[VEC];
-  for (int i = 0; i < kPolls; ++i) {
-    bool here = true;
+  // bit k: map k is awaited; bit kGroup - 1: the state is. Uniform over the wave.
+  unsigned open = (1u << count) - 1 | (far ? 1u << (kGroup - 1) : 0u);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      s[e] = far ? __hip_atomic_load(c.state + (size_t)(group - 1) * D + col + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+  for (int e = 0; e < VEC; ++e) s[e] = 0;
+  for (int i = 0; i < kPolls && open; ++i) {
+    if (open >> (kGroup - 1)) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        s[e] = __hip_atomic_load(c.state + (size_t)(group - 1) * D + col + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
 #pragma unroll
     for (int k = 0; k < kGroup - 1; ++k)
-      if (k < count) {
+      if (open >> k & 1) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
           w[k][e] = __hip_atomic_load(c.map + (size_t)(from + k) * D + col + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
+    unsigned left = 0;
+    if (open >> (kGroup - 1)) {
+      bool here = true;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) here = here && s[e] != kAbsent;
+      for (int e = 0; e < VEC; ++e) here = here && s[e] != kAbsent;
+      if (wave_any(!here)) left |= 1u << (kGroup - 1);
+    }
 #pragma unroll
     for (int k = 0; k < kGroup - 1; ++k)
-      if (k < count) {
+      if (open >> k & 1) {
+        bool here = true;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) here = here && (unsigned)(w[k][e] >> 32) != kAbsent;
+        if (wave_any(!here)) left |= 1u << k;
       }
-    if (!wave_any(!here)) break;
-    __builtin_amdgcn_s_sleep(1);
+    open = left;
+    if (open) __builtin_amdgcn_s_sleep(1);
   }
 #pragma unroll
   for (int e = 0; e < VEC; ++e) front[e] = __uint_as_float(s[e]);  // still absent: all ones is a NaN
@@ -221,13 +233,13 @@ struct Tile {
   int q, column;  // q = nq: none is left
   int bos, eos;
 };
-// The chain wave's next tile: by the counter where tiles wait for each other, else by its index.
-__device__ __forceinline__ int take(const Chain& c, bool first) {
+// The chain wave's next tile: by the counter where tiles wait for each other, else by its index. ask() sends
+// for it, and told() is uniform.
+__device__ __forceinline__ int ask(const Chain& c, bool first) {
   if (c.nq <= 1) return first ? blockIdx.x : c.ncol;  // a workgroup a tile
-  int tile = 0;
-  if (__lane_id() == 0) tile = (int)__hip_atomic_fetch_add(c.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return __builtin_amdgcn_readfirstlane(tile);
+  return __lane_id() == 0 ? (int)__hip_atomic_fetch_add(c.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
 }
+__device__ __forceinline__ int told(int answer) { return __builtin_amdgcn_readfirstlane(answer); }
 // Place along the tokens (nq behind the last tile) and column of a tile.
 __device__ __forceinline__ void place_of(const Chain& c, int tile, int& q, int& column) {
   const int i = tile / c.ncol;

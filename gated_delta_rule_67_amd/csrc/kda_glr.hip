@@ -47,13 +47,15 @@ hipError_t launch_ready(const GlrArgs& a, const Chain& c, const float* from, flo
   return hipGetLastError();
 }
 
-constexpr int kFwdTokens = 8, kFwdWaves = 15;  // a wave's span, spans of a tile
-constexpr int kFwdTile = kFwdTokens * kFwdWaves;
-static_assert(kGlrBlock % kFwdTokens == 0, "a block's first token begins a span");
+// A wave's span and the spans of a tile.
+template <int VEC> struct FwdTile {
+  static constexpr int kTokens = VEC == 4 ? 4 : 8, kWaves = 15, kTile = kTokens * kWaves;
+  static_assert(kGlrBlock % kTokens == 0, "a block's first token begins a span");
+};
 
 template <typename T, int VEC, bool CK, bool GATE, bool NORM>
-__global__ __launch_bounds__(64 * (kFwdWaves + 1)) void fwd_kernel(GlrArgs a, Chain chain) {
-  constexpr int NT = kFwdTokens, NW = kFwdWaves, C = 64 * VEC;
+__global__ __launch_bounds__(64 * (FwdTile<VEC>::kWaves + 1)) void fwd_kernel(GlrArgs a, Chain chain) {
+  constexpr int NT = FwdTile<VEC>::kTokens, NW = FwdTile<VEC>::kWaves, kFwdTile = NT * NW, C = 64 * VEC;
   constexpr unsigned kFull = 0xffffffffu >> (32 - NT);
   typedef typename KeptPiece<T, VEC, CK>::type piece;
   // Of this turn's tile and of the one before: the spans' maps, which the chain wave replaces by the maps
@@ -64,86 +66,88 @@ __global__ __launch_bounds__(64 * (kFwdWaves + 1)) void fwd_kernel(GlrArgs a, Ch
   __shared__ Tile s_next[2];  // the tile of the turn after next; first, those of the first two
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, k0 = lane * VEC;
 
-  if (wave == NW) {  // the chain wave: one barrier a turn, as in the other waves' loop
-    auto find = [&](bool first) {
+  if (wave == NW) {  // the chain wave: one barrier a turn, an even number of turns, as in the other waves' loop
+    auto find = [&](int answer) {
       Tile t;
-      place_of(chain, take(chain, first), t.q, t.column);
+      place_of(chain, told(answer), t.q, t.column);
       const Span s = t.q < chain.nq ? around(a.seqs, t.q * kFwdTile) : Span{0, 0};
       t.bos = s.bos, t.eos = s.eos;
       return t;
     };
-    Tile tile = find(true), next = find(false);
+    Tile tile = find(ask(chain, true)), next = find(ask(chain, false)), later = find(ask(chain, false));
     publish(&s_next[0], tile);
     publish(&s_next[1], next);
     lds_barrier();
     if (tile.q >= chain.nq) return;  // every tile is taken
     lds_barrier();                   // both have been read
     for (int turn = 0;; turn ^= 1) {
-      const Tile later = find(false);
       publish(&s_next[turn], later);
       lds_barrier();
-      const int q = tile.q, tile0 = q * kFwdTile;
-      const bool there = tile.column * C + k0 < a.D;
-      const int col = there ? tile.column * C + k0 : a.D - VEC;
-      float A[VEC], B[VEC], front[VEC];
+      Tile after{chain.nq, 0, 0, 0};
+      if (tile.q < chain.nq) {
+        const int answer = ask(chain, false);
+        const int q = tile.q, tile0 = q * kFwdTile;
+        const bool there = tile.column * C + k0 < a.D;
+        const int col = there ? tile.column * C + k0 : a.D - VEC;
+        float A[VEC], B[VEC], front[VEC];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) A[e] = 1.f, B[e] = front[e] = 0.f;
-      bool begins = false;
+        for (int e = 0; e < VEC; ++e) A[e] = 1.f, B[e] = front[e] = 0.f;
+        bool begins = false;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        float p[VEC], h[VEC];
-        s_map[turn][i][0].get(lane, p);
-        s_map[turn][i][1].get(lane, h);
-        s_map[turn][i][0].set(lane, A);
-        s_map[turn][i][1].set(lane, B);
-        const bool here = s_begins[turn][i];
+        for (int i = 0; i < NW; ++i) {
+          float p[VEC], h[VEC];
+          s_map[turn][i][0].get(lane, p);
+          s_map[turn][i][1].get(lane, h);
+          s_map[turn][i][0].set(lane, A);
+          s_map[turn][i][1].set(lane, B);
+          const bool here = s_begins[turn][i];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          B[e] = here ? h[e] : fmaf(p[e], B[e], h[e]);
-          A[e] *= p[e];
+          for (int e = 0; e < VEC; ++e) {
+            B[e] = here ? h[e] : fmaf(p[e], B[e], h[e]);
+            A[e] *= p[e];
+          }
+          begins = begins || here;
         }
-        begins = begins || here;
+        if (chain.nq > 1) {
+          if (there && q + 1 < chain.nq) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) put_map(chain, q, a.D, col + e, A[e], B[e]);
+          }
+          after = find(answer);  // while the other workgroups' maps are on their way
+          if (tile.bos < tile0) wait_front<VEC>(chain, q, tile.bos / kFwdTile, a.D, col, front);
+          if (there && q + 1 < chain.nq && q % kGroup == kGroup - 1) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+              put_state(chain, q / kGroup, a.D, col + e, begins ? B[e] : fmaf(A[e], front[e], B[e]));
+          }
+        }
+        s_front[turn].set(lane, front);
       }
-      if (chain.nq > 1) {
-        if (there && q + 1 < chain.nq) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) put_map(chain, q, a.D, col + e, A[e], B[e]);
-        }
-        if (tile.bos < tile0) wait_front<VEC>(chain, q, tile.bos / kFwdTile, a.D, col, front);
-        if (there && q + 1 < chain.nq && q % kGroup == kGroup - 1) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            put_state(chain, q / kGroup, a.D, col + e, begins ? B[e] : fmaf(A[e], front[e], B[e]));
-        }
-      }
-      s_front[turn].set(lane, front);
-      if (next.q >= chain.nq) break;
+      if (turn && next.q >= chain.nq) break;
       tile = next;
       next = later;
+      later = after;
     }
     lds_barrier();
     return;
   }
 
-  // This wave's part of a tile: first token, tokens, first channel (one that is there, for reading), the
-  // sequences in it.
+  // This wave's part of a tile: first token (-1: no tile), column, and whether the tile lies inside one sequence
+  // that begins in front of it and ends behind it. The rest follows where it is needed: scalar registers are scarce.
   struct Part {
-    int t0, count, col;
-    bool there;
-    Marks m;
+    int t0, column;
+    bool whole;
   };
   auto part = [&](const Tile& t) {
-    Part p;
-    p.t0 = t.q * kFwdTile + wave * NT;
-    p.count = min(max(a.T - p.t0, 0), NT);
-    p.col = t.column * C + k0;
-    p.there = p.col < a.D;  // D is a multiple of VEC
-    if (!p.there) p.col = a.D - VEC;
     const int tile0 = t.q * kFwdTile;
-    if (t.bos < tile0 && t.eos >= tile0 + kFwdTile) p.m = Marks{0, 0, kFull, 0, t.bos, t.eos};
-    else if (p.count > 0) p.m = marks_of(a.seqs, p.t0, p.count);
-    else p.m = Marks{};
-    return p;
+    if (t.q >= chain.nq) return Part{-1, 0, true};
+    return Part{tile0 + wave * NT, t.column, t.bos < tile0 && t.eos >= tile0 + kFwdTile};
+  };
+  auto tokens = [&](const Part& p) { return min(max(a.T - p.t0, 0), NT); };
+  auto channel_of = [&](const Part& p) { return p.column * C + k0; };  // D and more: none (D is a multiple of VEC)
+  auto marks = [&](const Part& p) {  // of a part that is not whole
+    const int n = p.t0 < 0 ? 0 : tokens(p);
+    return n > 0 ? marks_of(a.seqs, p.t0, n) : Marks{};
   };
   // A part's inputs: two of these take turns, so that a tile's loads are under way while the one in front
   // of it is worked on.
@@ -152,25 +156,27 @@ __global__ __launch_bounds__(64 * (kFwdWaves + 1)) void fwd_kernel(GlrArgs a, Ch
     float rate[VEC], bias[VEC];  // A_log and dt_bias
     Part at;
   };
+  // Loads are issued where no tile is left, too (of row 0): a wave waits for its loads by counting the ones behind
+  // them, and where some might not be there, on any way through its loop, it would wait for all.
   auto fetch = [&](Raw& w, const Part& p) {
     w.at = p;
-    // (loads without a condition: the wave does not wait for them here)
+    const int col = min(channel_of(p), a.D - VEC);
     const float* bias = a.dt_bias ? a.dt_bias : a.A_log;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      w.rate[e] = a.A_log[p.col + e];
-      w.bias[e] = bias[p.col + e];
+      w.rate[e] = a.A_log[col + e];
+      w.bias[e] = bias[col + e];
     }
     // rows that are there: the last one again behind the last token
-    const int rows = max(p.count, 1), t = min(p.t0, a.T - 1);
+    const int t = min(max(p.t0, 0), a.T - 1), rows = min(a.T - t, NT);
     const Rows rx = piece::rows(a.x, t, rows, a.D), rr = piece::rows(a.r, t, rows, a.D);
     const Rows ri = piece::rows(GATE ? a.in : a.x, t, rows, a.D);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int row = min(j, rows - 1);
-      w.r[j].load(rr, row, p.col);
-      w.x[j].load(rx, row, p.col);
-      if constexpr (GATE) w.in[j].load(ri, row, p.col);
+      w.r[j].load(rr, row, col);
+      w.x[j].load(rx, row, col);
+      if constexpr (GATE) w.in[j].load(ri, row, col);
     }
   };
   // A span's states from zero in front of it, the product of its decays, and where it lies.
@@ -180,7 +186,7 @@ __global__ __launch_bounds__(64 * (kFwdWaves + 1)) void fwd_kernel(GlrArgs a, Ch
   };
   auto local = [&](const Raw& w, Local& l, int turn) {
     l.at = w.at;
-    const Marks& m = l.at.m;
+    bool begins = false;
     Channel ch[VEC];
     float hs[VEC], ps[VEC];
 #pragma unroll
@@ -200,7 +206,7 @@ __global__ __launch_bounds__(64 * (kFwdWaves + 1)) void fwd_kernel(GlrArgs a, Ch
         bv[e] = b;
       }
     };
-    if (m.start == 0 && m.valid == kFull) {
+    if (l.at.whole) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float av[VEC], bv[VEC];
@@ -213,6 +219,9 @@ __global__ __launch_bounds__(64 * (kFwdWaves + 1)) void fwd_kernel(GlrArgs a, Ch
         if (j < NT - 1) s_decay[turn][wave][j].set(lane, ps);
       }
     } else {
+      const Marks m = marks(l.at);
+      const int col = min(channel_of(l.at), a.D - VEC);
+      begins = m.start != 0;
       int n = m.first;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
@@ -222,7 +231,7 @@ __global__ __launch_bounds__(64 * (kFwdWaves + 1)) void fwd_kernel(GlrArgs a, Ch
           n = starting_at(a.seqs, n, l.at.t0 + j);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            const float first = a.init && n < a.N ? a.init[(int64_t)n * a.D + l.at.col + e] : 0.f;
+            const float first = a.init && n < a.N ? a.init[(int64_t)n * a.D + col + e] : 0.f;
             hs[e] = fmaf(av[e], first, bv[e]);
           }
         } else if (m.valid >> j & 1) {
@@ -241,32 +250,34 @@ __global__ __launch_bounds__(64 * (kFwdWaves + 1)) void fwd_kernel(GlrArgs a, Ch
     s_map[turn][wave][1].set(lane, hs);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) l.decay[e] = ps[e];
-    if (lane == 0) s_begins[turn][wave] = m.start != 0;
+    if (lane == 0) s_begins[turn][wave] = begins;
   };
   // Outputs of a tile, once the chain wave knows what is in front of it.
   auto finish = [&](Local& l, int turn) {
     const Part& at = l.at;
-    const Marks& m = at.m;
-    if (at.count == 0 || !at.there) return;
+    const int col = channel_of(at);
+    if (at.t0 < 0 || at.t0 >= a.T || col >= a.D) return;
     float c[VEC], A[VEC], B[VEC];
     s_front[turn].get(lane, c);
     s_map[turn][wave][0].get(lane, A);
     s_map[turn][wave][1].get(lane, B);
-    const bool inside = m.bos >= at.t0 - wave * NT;  // the sequence in front of the span began in this tile
+    const Rows y = Piece<T, VEC>::rows(a.y, a.D, at.t0, tokens(at), a.D);
+    auto keep = [&] {
+      if (a.states && at.t0 % kGlrBlock == 0) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) c[e] = m.bos >= at.t0 ? 0.f : inside ? B[e] : fmaf(A[e], c[e], B[e]);
-    if (a.states && at.t0 % kGlrBlock == 0) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) a.states[(int64_t)(at.t0 / kGlrBlock) * a.D + at.col + e] = c[e];
-    }
+        for (int e = 0; e < VEC; ++e) a.states[(int64_t)(at.t0 / kGlrBlock) * a.D + col + e] = c[e];
+      }
+    };
     auto decays = [&](int j, float (&p)[VEC]) {
       if (j < NT - 1) s_decay[turn][wave][j].get(lane, p);
       else
 #pragma unroll
         for (int e = 0; e < VEC; ++e) p[e] = l.decay[e];
     };
-    const Rows y = Piece<T, VEC>::rows(a.y, a.D, at.t0, at.count, a.D);
-    if (m.start == 0 && m.valid == kFull) {
+    if (at.whole) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) c[e] = fmaf(A[e], c[e], B[e]);
+      keep();
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float p[VEC];
@@ -279,24 +290,30 @@ __global__ __launch_bounds__(64 * (kFwdWaves + 1)) void fwd_kernel(GlrArgs a, Ch
         for (int j = 0; j < NT; ++j) {
           Piece<T, VEC> o;
           o.set(l.h[j]);
-          o.store(y, j, at.col);
+          o.store(y, j, col);
         }
       }
-    } else {
-      unsigned begun = 0;  // a sequence has begun in the span
+      return;
+    }
+    const Marks m = marks(at);
+    const bool inside = m.bos >= at.t0 - wave * NT;  // the sequence in front of the span began in this tile
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        begun |= m.start >> j & 1;
-        const bool lies = m.valid >> j & 1;
-        float p[VEC];
-        decays(j, p);
+    for (int e = 0; e < VEC; ++e) c[e] = m.bos >= at.t0 ? 0.f : inside ? B[e] : fmaf(A[e], c[e], B[e]);
+    keep();
+    const int count = tokens(at);
+    unsigned begun = 0;  // a sequence has begun in the span
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) l.h[j][e] = !lies ? 0.f : begun ? l.h[j][e] : fmaf(p[e], c[e], l.h[j][e]);
-        if (a.y && j < at.count && (lies || a.zero_rest)) {
-          Piece<T, VEC> o;
-          o.set(l.h[j]);
-          o.store(y, j, at.col);
-        }
+    for (int j = 0; j < NT; ++j) {
+      begun |= m.start >> j & 1;
+      const bool lies = m.valid >> j & 1;
+      float p[VEC];
+      decays(j, p);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) l.h[j][e] = !lies ? 0.f : begun ? l.h[j][e] : fmaf(p[e], c[e], l.h[j][e]);
+      if (a.y && j < count && (lies || a.zero_rest)) {
+        Piece<T, VEC> o;
+        o.set(l.h[j]);
+        o.store(y, j, col);
       }
     }
     if (!a.final) return;
@@ -309,55 +326,44 @@ __global__ __launch_bounds__(64 * (kFwdWaves + 1)) void fwd_kernel(GlrArgs a, Ch
       for (int j = 0; j < NT; ++j)
         if (j == last) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) a.final[(int64_t)n * a.D + at.col + e] = l.h[j][e];
+          for (int e = 0; e < VEC; ++e) a.final[(int64_t)n * a.D + col + e] = l.h[j][e];
         }
     }
   };
   // A turn: the states of its tile from zero, then, behind the barrier, the outputs of the tile before and the loads
-  // of the tile after next. False where the next turn has no tile (this one's outputs are done then, too).
-  // Loads are issued where no tile is left, too (of row 0): a wave waits for its loads by counting the ones
-  // behind them, and where some might not be there it would wait for all.
+  // of the tile after next. Turns come in pairs (see fetch).
   Local before;
-  bool later = false;
-  auto fetch_tile = [&](Raw& w, const Tile& t) {
-    const bool left = t.q < chain.nq;
-    Part p;
-    p.t0 = 0, p.count = 1, p.col = min(k0, a.D - VEC), p.there = false, p.m = Marks{};
-    if (left) p = part(t);
-    fetch(w, p);
-    if (!left) w.at.count = -1;
-  };
-  auto step = [&](Raw& w, const Raw& next, int turn) {
+  before.at.t0 = -1;
+  auto step = [&](Raw& w, int turn) {
     Local now;
     local(w, now, turn);
     lds_barrier();
     const Tile t = read(&s_next[turn]);
-    if (later) finish(before, turn ^ 1);
+    finish(before, turn ^ 1);
     before = now;
-    later = true;
-    fetch_tile(w, t);
-    if (next.at.count >= 0) return true;
-    lds_barrier();
-    finish(before, turn);
-    return false;
+    fetch(w, part(t));
   };
   lds_barrier();
   const Tile t0 = read(&s_next[0]), t1 = read(&s_next[1]);
   if (t0.q >= chain.nq) return;
   lds_barrier();
   Raw even, odd;
-  fetch_tile(even, t0);
-  fetch_tile(odd, t1);
-  while (step(even, odd, 0) && step(odd, even, 1)) {
-  }
+  fetch(even, part(t0));
+  fetch(odd, part(t1));
+  do {
+    step(even, 0);
+    step(odd, 1);
+  } while (even.at.t0 >= 0);
+  lds_barrier();
+  finish(before, 1);
 }
 
 template <typename T, int VEC, bool CK, bool GATE, bool NORM>
 hipError_t run_fwd(const GlrArgs& a, void* workspace, hipStream_t stream) {
-  const Chain c = make_chain(a, workspace, kFwdTile, 64 * VEC);
+  const Chain c = make_chain(a, workspace, FwdTile<VEC>::kTile, 64 * VEC);
   const hipError_t e = launch_ready(a, c, a.init, a.final, stream);
   if (e != hipSuccess || c.nq == 0) return e;
-  hipLaunchKernelGGL((fwd_kernel<T, VEC, CK, GATE, NORM>), dim3(chain_blocks(c, 1)), dim3(64 * (kFwdWaves + 1)), 0, stream, a, c);
+  hipLaunchKernelGGL((fwd_kernel<T, VEC, CK, GATE, NORM>), dim3(chain_blocks(c, 1)), dim3(64 * (FwdTile<VEC>::kWaves + 1)), 0, stream, a, c);
   return hipGetLastError();
 }
 
@@ -409,8 +415,10 @@ hipError_t run_step(const GlrArgs& a, hipStream_t stream) {
 
 }  // namespace glr
 
-size_t glr_fwd_workspace_bytes(int T, int D) {
-  return glr::chain_bytes((int)(((int64_t)T + glr::kFwdTile - 1) / glr::kFwdTile), D);
+size_t glr_fwd_workspace_bytes(int T, int D) {  // for the shortest tiles
+  constexpr int tile = glr::FwdTile<4>::kTile;
+  static_assert(tile <= glr::FwdTile<2>::kTile && tile <= glr::FwdTile<1>::kTile, "the shortest tiles");
+  return glr::chain_bytes((int)(((int64_t)T + tile - 1) / tile), D);
 }
 
 hipError_t launch_glr_fwd(GlrArgs a, void* workspace, hipStream_t stream) {
@@ -418,7 +426,7 @@ hipError_t launch_glr_fwd(GlrArgs a, void* workspace, hipStream_t stream) {
   return glr::with_gates(a, [&](auto gate, auto norm) {
     constexpr bool G = decltype(gate)::value, M = decltype(norm)::value;
     if (a.packed) {  // states in front of the blocks of a checkpointed call: no outputs of type T
-      if (vector_width(2, 1, a.D, ptrs, 3) == 2) return glr::run_fwd<bf16, 2, true, G, M>(a, workspace, stream);
+      if (vector_width(4, 1, a.D, ptrs, 3) == 4) return glr::run_fwd<bf16, 4, true, G, M>(a, workspace, stream);
       return glr::run_fwd<bf16, 1, true, G, M>(a, workspace, stream);
     }
     if (!a.bf) return glr::run_fwd<float, 1, false, G, M>(a, workspace, stream);

@@ -30,8 +30,8 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
   typedef Piece<T, VEC> piece;
   // A span's decays, its state and its gradient, each from zero, and whether a sequence ends in it; the map
   // (decays, gradient) from behind the tile to behind each span; the gradient that reaches the tile from
-  // behind; a span's sums of dA_log and ddt_bias.
-  __shared__ Lanes<VEC> s_map[NW][3], s_behind[NW][2], s_front, s_sum[NW][2];
+  // behind; a span's sums of dA_log and ddt_bias, of this turn and the one before.
+  __shared__ Lanes<VEC> s_map[NW][3], s_behind[NW][2], s_front, s_sum[2][NW][2];
   __shared__ Lanes<VEC> s_held[NW][GATE ? 2 : 1][NT];  // what the outputs need and nothing in between (registers are scarce)
   __shared__ int s_ends[NW];
   __shared__ Tile s_next;  // the next turn's tile; first, this turn's
@@ -40,9 +40,9 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
   auto first_token = [&](int q) { return (chain.nq - 1 - q) * kBwdTile; };
 
   if (wave == NW) {  // the chain wave: two barriers a turn, as in the other waves' loop
-    auto find = [&](bool first) {
+    auto find = [&](int answer) {
       Tile t;
-      place_of(chain, take(chain, first), t.q, t.column);
+      place_of(chain, told(answer), t.q, t.column);
       t.bos = t.eos = 0;
       if (t.q < chain.nq) {
         const Span s = around(a.seqs, min(first_token(t.q) + kBwdTile, a.T) - 1);
@@ -50,7 +50,7 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
       }
       return t;
     };
-    auto sums = [&](const Tile& t) {  // of a tile whose sums have been left, in order of the spans
+    auto sums = [&](const Tile& t, int turn) {  // of a tile whose sums have been left, in order of the spans
       const int col = t.column * C + k0;
       float dA[VEC], db[VEC];
 #pragma unroll
@@ -58,8 +58,8 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
         float u[VEC], v[VEC];
-        s_sum[i][0].get(lane, u);
-        s_sum[i][1].get(lane, v);
+        s_sum[turn][i][0].get(lane, u);
+        s_sum[turn][i][1].get(lane, v);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) dA[e] += u[e], db[e] += v[e];
       }
@@ -69,16 +69,17 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
         for (int e = 0; e < VEC; ++e) out[e] = dA[e] * kLn2, out[a.D + e] = db[e];
       }
     };
-    Tile tile = find(true), before{};
+    Tile tile = find(ask(chain, true)), next = find(ask(chain, false)), before{};
     publish(&s_next, tile);
     lds_barrier();
     if (tile.q >= chain.nq) return;  // every tile is taken
     lds_barrier();
     bool later = false;
-    for (;;) {
-      const Tile next = find(false);
+    for (int turn = 0;; turn ^= 1) {
       publish(&s_next, next);
       lds_barrier();
+      const int answer = ask(chain, false);
+      Tile after{chain.nq, 0, 0, 0};
       const int q = tile.q, last = min(first_token(q) + kBwdTile, a.T) - 1;
       const bool there = tile.column * C + k0 < a.D;
       const int col = there ? tile.column * C + k0 : a.D - VEC;
@@ -106,6 +107,7 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
 #pragma unroll
           for (int e = 0; e < VEC; ++e) put_map(chain, q, a.D, col + e, A[e], B[e]);
         }
+        after = find(answer);  // while the other workgroups' maps are on their way
         if (tile.eos > last) wait_front<VEC>(chain, q, chain.nq - 1 - tile.eos / kBwdTile, a.D, col, front);
         if (there && q + 1 < chain.nq && q % kGroup == kGroup - 1) {
 #pragma unroll
@@ -114,16 +116,18 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
         }
       }
       s_front.set(lane, front);
-      if (a.part && later) sums(before);
       lds_barrier();
+      if (a.part && later) sums(before, turn ^ 1);
       before = tile;
       later = true;
-      if (next.q >= chain.nq) break;
+      if (next.q >= chain.nq) {
+        lds_barrier();
+        if (a.part) sums(before, turn);
+        return;
+      }
       tile = next;
+      next = after;
     }
-    lds_barrier();
-    if (a.part) sums(before);
-    return;
   }
 
   struct Part {
@@ -175,7 +179,7 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
     lds_barrier();
     fetch(part(first));
   }
-  for (;;) {
+  for (int turn = 0;; turn ^= 1) {
     // Of every element: decay, and what makes the gradients from G, which the phases below complete:
     // dx = cx G, din_gate = ci G, dgate_x = cr G, dA_log's term ca G.
     float av[NT][VEC], cr[NT][VEC], ca[NT][VEC];
@@ -378,8 +382,8 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
         if constexpr (GATE) o.store(oi, j, now.col);
       }
     }
-    s_sum[wave][0].set(lane, dA);
-    s_sum[wave][1].set(lane, db);
+    s_sum[turn][wave][0].set(lane, dA);
+    s_sum[turn][wave][1].set(lane, db);
     if (!more) break;
   }
   lds_barrier();

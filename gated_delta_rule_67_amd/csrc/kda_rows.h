@@ -55,12 +55,15 @@ template <typename T, int VEC> struct Piece {
   static __device__ __forceinline__ Rows rows(const Source& s, int64_t token, int n, int D) { return rows(s.p, s.ld, token, n, D); }
   __device__ __forceinline__ void load(const Rows& r, int row, int col) {
     const int off = col * (int)sizeof(T);
-    if constexpr (sizeof(raw) == 4) raw = __builtin_bit_cast(decltype(raw), __builtin_amdgcn_raw_buffer_load_b32(r.p, off, row * r.ld, 0));
+    if constexpr (sizeof(raw) == 8) raw = __builtin_bit_cast(decltype(raw), __builtin_amdgcn_raw_buffer_load_b64(r.p, off, row * r.ld, 0));
+    else if constexpr (sizeof(raw) == 4) raw = __builtin_bit_cast(decltype(raw), __builtin_amdgcn_raw_buffer_load_b32(r.p, off, row * r.ld, 0));
     else raw = __builtin_bit_cast(decltype(raw), __builtin_amdgcn_raw_buffer_load_b16(r.p, off, row * r.ld, 0));
   }
   __device__ __forceinline__ void store(const Rows& r, int row, int col) const {
     const int off = col * (int)sizeof(T);
-    if constexpr (sizeof(raw) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, raw), r.p, off, row * r.ld, 0);
+    typedef unsigned two __attribute__((ext_vector_type(2)));
+    if constexpr (sizeof(raw) == 8) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(two, raw), r.p, off, row * r.ld, 0);
+    else if constexpr (sizeof(raw) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, raw), r.p, off, row * r.ld, 0);
     else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, raw), r.p, off, row * r.ld, 0);
   }
   __device__ __forceinline__ void get(float (&v)[VEC]) const {
@@ -107,8 +110,9 @@ template <int VEC> struct PackedPiece {
     return r;
   }
   __device__ __forceinline__ void load(const Rows& r, int row, int col) {
-    static_assert(VEC <= 2, "the recurrence reads one or two channels a lane");
-    if constexpr (VEC == 2) word[0] = __builtin_amdgcn_raw_buffer_load_b16(r.p, col, row * r.ld, 0);
+    static_assert(VEC <= 4, "a word of codes a lane");
+    if constexpr (VEC == 4) word[0] = __builtin_amdgcn_raw_buffer_load_b32(r.p, col, row * r.ld, 0);
+    else if constexpr (VEC == 2) word[0] = __builtin_amdgcn_raw_buffer_load_b16(r.p, col, row * r.ld, 0);
     else word[0] = __builtin_amdgcn_raw_buffer_load_b8(r.p, col, row * r.ld, 0);
     byte = __builtin_amdgcn_raw_buffer_load_b8(r.scales, col / kScaleBlock, row * r.ld_scales, 0);
   }
