@@ -92,11 +92,21 @@ __device__ __forceinline__ float sigmoid_fast(float z) {
 // sqrt(1 - a^2) for a = 2^g2. Near a = 1 the difference would cancel: there 1 - e^-v, v = -2 g2 ln 2, by
 // its series in g2 (relative error v^5 / 720 < 5e-8 at v = 1/8); elsewhere from a, whose last bit costs
 // 1e-6 at most.
-__device__ __forceinline__ float input_weight(float a, float g2) {
+__device__ __forceinline__ float input_weight_squared(float a, float g2) {
   constexpr float k = -2.f * kLn2;
   constexpr float c1 = k, c2 = -k * k / 2, c3 = k * k * k / 6, c4 = -k * k * k * k / 24, c5 = k * k * k * k * k / 120;
   const float p = g2 * fmaf(g2, fmaf(g2, fmaf(g2, fmaf(g2, c5, c4), c3), c2), c1);
-  return __builtin_amdgcn_sqrtf(g2 > -0.125f / (2.f * kLn2) ? p : fmaf(-a, a, 1.f));
+  return g2 > -0.125f / (2.f * kLn2) ? p : fmaf(-a, a, 1.f);
+}
+__device__ __forceinline__ float input_weight(float a, float g2) {
+  return __builtin_amdgcn_sqrtf(input_weight_squared(a, g2));
+}
+// The same and its reciprocal, which is held below 2^63: it is multiplied by the softplus' slope, which is as
+// small as the weight's square, so that a weight of 0 has no part in a gradient.
+__device__ __forceinline__ float input_weight(float a, float g2, float& inv) {
+  const float v = input_weight_squared(a, g2);
+  inv = __builtin_amdgcn_rsqf(v < 0x1p-126f ? 0x1p-126f : v);
+  return v * inv;
 }
 
 // ---- Work. A workgroup's tile is kWaves consecutive spans of tokens (one a wave) by 64 VEC channels

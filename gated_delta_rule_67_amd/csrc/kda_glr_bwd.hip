@@ -32,7 +32,7 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
   // (decays, gradient) from behind the tile to behind each span; the gradient that reaches the tile from
   // behind; a span's sums of dA_log and ddt_bias, of this turn and the one before.
   __shared__ Lanes<VEC> s_map[NW][3], s_behind[NW][2], s_front, s_sum[2][NW][2];
-  __shared__ Lanes<VEC> s_held[NW][GATE ? 2 : 1][NT];  // what the outputs need and nothing in between (registers are scarce)
+  __shared__ Lanes<VEC> s_held[NW][3][NT];  // what the outputs need and nothing in between (registers are scarce)
   __shared__ int s_ends[NW];
   __shared__ Tile s_next;  // the next turn's tile; first, this turn's
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, k0 = lane * VEC;
@@ -79,7 +79,6 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
       publish(&s_next, next);
       lds_barrier();
       const int answer = ask(chain, false);
-      Tile after{chain.nq, 0, 0, 0};
       const int q = tile.q, last = min(first_token(q) + kBwdTile, a.T) - 1;
       const bool there = tile.column * C + k0 < a.D;
       const int col = there ? tile.column * C + k0 : a.D - VEC;
@@ -107,7 +106,6 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
 #pragma unroll
           for (int e = 0; e < VEC; ++e) put_map(chain, q, a.D, col + e, A[e], B[e]);
         }
-        after = find(answer);  // while the other workgroups' maps are on their way
         if (tile.eos > last) wait_front<VEC>(chain, q, chain.nq - 1 - tile.eos / kBwdTile, a.D, col, front);
         if (there && q + 1 < chain.nq && q % kGroup == kGroup - 1) {
 #pragma unroll
@@ -117,6 +115,7 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
       }
       s_front.set(lane, front);
       lds_barrier();
+      const Tile after = find(answer);
       if (a.part && later) sums(before, turn ^ 1);
       before = tile;
       later = true;
@@ -230,7 +229,7 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
       for (int e = 0; e < VEC; ++e) ch[e] = channel(rate[e], a.dt_bias ? bias[e] : 0.f), A[e] = 1.f, hs[e] = rs[e] = 0.f;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        float rv[VEC], iv[VEC], xv[VEC], cx[VEC], ci[VEC];
+        float rv[VEC], iv[VEC], xv[VEC], cx[VEC], ci[VEC], lg[VEC];
         dy[j] = gk[j];
         rk[j].get(rv);
         xk[j].get(xv);
@@ -242,16 +241,18 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
           if constexpr (GATE) logistic_pair(iv[e], s, rest);
           float q = s * xv[e], w = 1.f;
           if constexpr (NORM) {
-            w = input_weight(d, g2);
-            tw[j][e] = w > 0.f ? q * d * __builtin_amdgcn_rcpf(w) : 0.f;
+            float inv;
+            w = input_weight(d, g2, inv);
+            tw[j][e] = q * d * inv;
           }
           cx[e] = s * w;
           b[j][e] = q * w;
           ci[e] = b[j][e] * rest;
           cr[j][e] = ch[e].neg_rate * slope;
-          ca[j][e] = g2;
+          lg[e] = g2;
           av[j][e] = d;
         }
+        s_held[wave][2][j].set(lane, lg);
         if constexpr (GATE || NORM) s_held[wave][0][j].set(lane, cx);
         if constexpr (GATE) s_held[wave][1][j].set(lane, ci);
         if (W || (m.valid >> j & 1)) {
@@ -297,13 +298,15 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
     }
     auto slopes = [&](auto inside) {
       states(inside, [&](int j, int e) { return b[j][e]; }, [&](int j) {
+        float lg[VEC];
+        s_held[wave][2][j].get(lane, lg);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           float d = hs[e];
           if constexpr (NORM) d -= tw[j][e];
           d *= av[j][e];
           cr[j][e] *= d;
-          ca[j][e] *= d;
+          ca[j][e] = lg[e] * d;
         }
       });
     };
