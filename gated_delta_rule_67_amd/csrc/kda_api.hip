@@ -855,9 +855,15 @@ static int check_glr(int64_t N, int T, int D, unsigned flags, int dtype) {
   if (flags & ~(unsigned)(KDA_ZERO_REST | KDA_GLR_NORMALISE)) return KDA_ERR_INVALID;
   if (N < 1 || T < 0 || !positive(D) || !valid_dtype(dtype)) return KDA_ERR_INVALID;
   if (D > (1 << 20) || N > (1 << 17) || T > kMaxTokens) return KDA_ERR_UNSUPPORTED;
-  // workgroups of 512 threads, 64 tokens or 128 sequences by 64 channels at least: under 2^32 threads a launch
-  const int64_t tiles = ((int64_t)T / kda::kGlrBlock + 1 + N / 128 + 1) * (D / 64 + 1);
-  return tiles >= (1 << 23) ? KDA_ERR_UNSUPPORTED : KDA_OK;
+  // tiles are counted in 32 bits, and a thread a state is launched
+  if ((int64_t)T * D >= (int64_t)1 << 35 || N * D > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+// Token tensors of the recurrence: buffer offsets inside a tile stay below 2^31.
+static int glr_source(kda::Source* s, const void* p, const void* scales, int64_t stride, int64_t T, int64_t D) {
+  if (!source(s, p, scales, stride, T, D)) return KDA_ERR_INVALID;
+  return s->ld > (1 << 24) ? KDA_ERR_UNSUPPORTED : KDA_OK;
 }
 
 size_t kda_glr_fwd_workspace_size(int T, int D) {
@@ -876,13 +882,13 @@ int kda_glr_fwd(const void* x, int64_t x_stride, const void* gate_x, int64_t gat
                 const float* dt_bias, const void* in_gate, int64_t in_gate_stride, const float* initial_state,
                 const int* cu_seqlens, int N, float* final_state, void* y, float* block_states, int T, int D,
                 unsigned flags, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
-  const int rc = check_glr(N, T, D, flags, dtype);
+  int rc = check_glr(N, T, D, flags, dtype);
   if (rc != KDA_OK) return rc;
   if (!valid_sequences(N, T, cu_seqlens) || !A_log || (T > 0 && (!x || !gate_x || !y))) return KDA_ERR_INVALID;
   kda::GlrArgs a{};
-  if (!source(&a.x, x, nullptr, x_stride, T, D) || !source(&a.r, gate_x, nullptr, gate_x_stride, T, D) ||
-      !source(&a.in, in_gate, nullptr, in_gate_stride, T, D))
-    return KDA_ERR_INVALID;
+  if ((rc = glr_source(&a.x, x, nullptr, x_stride, T, D)) != KDA_OK) return rc;
+  if ((rc = glr_source(&a.r, gate_x, nullptr, gate_x_stride, T, D)) != KDA_OK) return rc;
+  if ((rc = glr_source(&a.in, in_gate, nullptr, in_gate_stride, T, D)) != KDA_OK) return rc;
   if (!valid_workspace(workspace, workspace_bytes, kda_glr_fwd_workspace_size(T, D))) return KDA_ERR_INVALID;
   a.A_log = A_log, a.dt_bias = dt_bias, a.init = initial_state, a.seqs = kda::make_sequences(cu_seqlens, N, T);
   a.N = N, a.T = T, a.D = D, a.states = block_states, a.final = final_state, a.y = y;
@@ -897,14 +903,15 @@ int kda_glr_bwd(const void* x, const void* x_scales, int64_t x_stride, const voi
                 int N, const void* dy, int64_t dy_stride, const float* dfinal_state, const float* block_states,
                 void* dx, void* dgate_x, void* din_gate, float* dA_log, float* ddt_bias, float* dinitial_state, int T,
                 int D, unsigned flags, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
-  const int rc = check_glr(N, T, D, flags, dtype);
+  int rc = check_glr(N, T, D, flags, dtype);
   if (rc != KDA_OK) return rc;
   if (!valid_sequences(N, T, cu_seqlens) || !A_log) return KDA_ERR_INVALID;
   if (T > 0 && (!x || !gate_x || !dy || !dx || !dgate_x || (in_gate && !din_gate))) return KDA_ERR_INVALID;
   kda::GlrArgs a{};
-  if (!source(&a.x, x, x_scales, x_stride, T, D) || !source(&a.r, gate_x, gate_x_scales, gate_x_stride, T, D) ||
-      !source(&a.in, in_gate, in_gate_scales, in_gate_stride, T, D) || !source(&a.dy, dy, nullptr, dy_stride, T, D))
-    return KDA_ERR_INVALID;
+  if ((rc = glr_source(&a.x, x, x_scales, x_stride, T, D)) != KDA_OK) return rc;
+  if ((rc = glr_source(&a.r, gate_x, gate_x_scales, gate_x_stride, T, D)) != KDA_OK) return rc;
+  if ((rc = glr_source(&a.in, in_gate, in_gate_scales, in_gate_stride, T, D)) != KDA_OK) return rc;
+  if ((rc = glr_source(&a.dy, dy, nullptr, dy_stride, T, D)) != KDA_OK) return rc;
   if (!same_kind(a.x, a.r) || !same_kind(a.x, a.in)) return KDA_ERR_INVALID;
   a.packed = a.x.scales != nullptr;
   if (a.packed && D % kda::kScaleBlock != 0) return KDA_ERR_UNSUPPORTED;

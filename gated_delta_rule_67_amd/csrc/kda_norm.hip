@@ -140,7 +140,7 @@ template <typename T, int VEC, bool BEHIND>
 hipError_t run_fwd(const NormArgs& a, hipStream_t stream) {
   return with_tile<VEC>(a.D, [&](auto tile) {
     typedef decltype(tile) TILE;
-    constexpr int ROWS = TILE::NC >= 4 ? 1 : TILE::NC == 2 ? 2 : 4;
+    constexpr int ROWS = TILE::NC > 2 ? 1 : TILE::NC == 2 ? 2 : 4;
     const int64_t need = (a.rows + TILE::SIDE * ROWS - 1) / (TILE::SIDE * ROWS);
     const int64_t most = kFwdThreads / TILE::BLOCK;
     hipLaunchKernelGGL((fwd_kernel<T, TILE, ROWS, BEHIND>), dim3((unsigned)(need < most ? need : most)),

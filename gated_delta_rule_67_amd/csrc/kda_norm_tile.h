@@ -67,8 +67,9 @@ template <int VEC, class F> inline hipError_t with_tile(int D, F&& go) {
   }
   if (D <= 64 * VEC) return go(Tile<VEC, 64, 1>{});
   if (D <= 256 * VEC) return go(Tile<VEC, 256, 1>{});
-  if constexpr (VEC >= 4) {
-    if (D <= 512 * VEC) return go(Tile<VEC, 256, 2>{});
+  if (D <= 512 * VEC) return go(Tile<VEC, 256, 2>{});
+  if constexpr (VEC < 4) {
+    if (D <= 768 * VEC) return go(Tile<VEC, 256, 3>{});
   }
   if (D <= 1024 * VEC) return go(Tile<VEC, 256, 4>{});
   if constexpr (VEC < 8) return go(Tile<VEC, 1024, kNormMaxDim / (1024 * VEC)>{});

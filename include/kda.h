@@ -694,7 +694,8 @@ int kda_checkpoint_unpack(const void* codes, const void* scales, void* x, int64_
  *     h_t = a_t h_{t-1} + w_t logistic(in_gate_t) x_t,   y_t = h_t
  * with w_t = sqrt(1 - a_t^2) with KDA_GLR_NORMALISE, else 1.
  *
- *   x, gate_x, in_gate  [T, D]  dtype, *_stride elements between tokens (>= D); in_gate may be NULL: factor 1
+ *   x, gate_x, in_gate  [T, D]  dtype, *_stride elements between tokens (>= D, <= 2^24); in_gate may be NULL:
+ *                               factor 1
  *   A_log, dt_bias      [D]     float32 (an exp(A_log) above 2e38 counts as 2e38); dt_bias may be NULL
  *   initial_state       [N, D]  float32, or NULL: zeros
  *   cu_seqlens          as for kda_conv_fwd (NULL: N sequences of T / N tokens each)
@@ -709,7 +710,7 @@ int kda_checkpoint_unpack(const void* codes, const void* scales, void* x, int64_
  * The token axis is scanned in one pass of the data; results are bitwise reproducible. Tokens of other
  * sequences, and tokens behind, do not reach an output, finite or not; behind a state that is not finite,
  * NaN may stand for an infinity. The softplus, decays and weights have a relative error of about 1e-6.
- * N >= 1, T >= 0, D >= 1 (else KDA_ERR_INVALID); N <= 2^17, D <= 2^20, T <= 2^30, T D under about 2^35 (else
+ * N >= 1, T >= 0, D >= 1 (else KDA_ERR_INVALID); N <= 2^17, D <= 2^20, T <= 2^30, T D < 2^35, N D < 2^31 (else
  * KDA_ERR_UNSUPPORTED). No alignment is required. Nothing is allocated.
  */
 size_t kda_glr_fwd_workspace_size(int T, int D);
@@ -745,7 +746,8 @@ int kda_glr_bwd(const void* x, const void* x_scales, int64_t x_stride, const voi
  * One token of kda_glr_fwd per request, on slot slots[n] of state_pool [num_slots, D] (float32, updated in
  * place): x, gate_x, in_gate (or NULL) and y [B, D]. slots NULL: request n uses slot n (num_slots >= B). A
  * request whose slot is outside [0, num_slots) gets y = 0 and changes no state; valid slots of one call must
- * be distinct. flags: 0 or KDA_GLR_NORMALISE. B ceil(D / 256) < 2^23, otherwise as kda_glr_fwd.
+ * be distinct. flags: 0 or KDA_GLR_NORMALISE. B ceil(D / 256) < 2^23, otherwise as kda_glr_fwd, without its
+ * limits on strides.
  */
 int kda_glr_step(const void* x, int64_t x_stride, const void* gate_x, int64_t gate_x_stride,
                  const float* A_log, const float* dt_bias, const void* in_gate,

@@ -150,6 +150,8 @@ CASES = [
     ([15, 1, 16, 17, 63, 65, 127, 129], 70, "f32", True, False, True, True, 3),
     ([2] * 70 + [1] * 70, 24, "f32", True, True, True, False, 0),
     ([1100, 30], 9, "bf16", True, True, True, True, 0),
+    ([119, 1, 120, 121, 240, 7], 258, "bf16", True, True, True, True, 0),
+    ([59, 61, 60, 1, 500], 256, "bf16", False, False, True, True, 0),
 ]
 
 
@@ -177,7 +179,8 @@ def test_many_tiles(lengths, dtype, D):
 
 
 @pytest.mark.parametrize("lengths,D,dtype,in_gate", [([90, 0, 33], 64, "bf16", True), ([700], 32, "f32", True),
-                                                     ([1300, 20], 96, "bf16", False)])
+                                                     ([1300, 20], 96, "bf16", False), ([59, 61, 60, 1, 900], 288, "bf16", True),
+                                                     ([4000], 64, "bf16", True)])
 def test_backward_from_checkpoints(lengths, D, dtype, in_gate):
     dt = torch.bfloat16 if dtype == "bf16" else torch.float32
     _check(_make(lengths, D, dt, D, in_gate=in_gate, tail=5), dt, packed=True)
@@ -273,11 +276,12 @@ def test_malformed_offsets_stay_in_bounds(cu):
 
 
 def test_large_offsets():
-    T, D, ld = 9, 8, 300_000_000
+    """Tokens at the largest stride, whose element offsets pass 32 bits."""
+    T, D, ld = 300, 8, 1 << 24
     x = torch.empty(T * ld, dtype=torch.bfloat16, device="cuda").as_strided((T, D), (ld, 1))
     x.copy_(torch.randn(T, D))
     A, c = torch.randn(D, device="cuda"), x.contiguous()
-    cu = torch.tensor([0, 4, T], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 4, 260, T], dtype=torch.int32, device="cuda")
     assert torch.equal(kda.kda_glr_fwd(x, x, A, None, x, None, cu)[0], kda.kda_glr_fwd(c, c, A, None, c, None, cu)[0])
     for a, b in zip(kda.kda_glr_bwd(x, x, A, x, None, x, None, None, cu), kda.kda_glr_bwd(c, c, A, c, None, c, None, None, cu)):
         assert a is None or torch.equal(a, b)

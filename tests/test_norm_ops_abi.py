@@ -93,7 +93,8 @@ GLR_BAD = [
     (dict(x=None), INV), (dict(r=None), INV), (dict(A=None), INV), (dict(N=0), INV), (dict(T=-1), INV), (dict(T=65), INV),
     (dict(D=0), INV), (dict(sx=63), INV), (dict(sr=63), INV), (dict(i=FAKE, si=3), INV), (dict(flags=1), INV), (dict(flags=8), INV),
     (dict(dtype=2), INV), (dict(N=1 << 18, T=1 << 18), UNS), (dict(D=(1 << 20) + 1), UNS), (dict(T=(1 << 30) + 2), UNS),
-    (dict(T=1 << 30, D=64), UNS), (dict(T=4096, ws=None), INV), (dict(T=4096, ws_bytes=8), INV),
+    (dict(T=1 << 30, D=64), UNS), (dict(N=1 << 17, T=0, D=1 << 14, sx=1 << 14, sr=1 << 14, sdy=1 << 14), UNS),
+    (dict(sx=(1 << 24) + 1), UNS), (dict(i=FAKE, si=(1 << 24) + 1), UNS), (dict(T=4096, ws=None), INV), (dict(T=4096, ws_bytes=8), INV),
     (dict(ws=ctypes.c_void_p(0x1010)), INV),
 ]
 
@@ -107,7 +108,7 @@ def test_glr_fwd_refuses(lib, bad, rc):
 
 
 @pytest.mark.parametrize("bad,rc", GLR_BAD + [
-    (dict(dy=None), INV), (dict(sdy=3), INV), (dict(dx=None), INV), (dict(dr=None), INV), (dict(i=FAKE, di=None), INV),
+    (dict(dy=None), INV), (dict(sdy=3), INV), (dict(sdy=1 << 25), UNS), (dict(dx=None), INV), (dict(dr=None), INV), (dict(i=FAKE, di=None), INV),
     (dict(xs=FAKE), INV), (dict(xs=FAKE, rs=FAKE, i=FAKE), INV), (dict(rs=FAKE), INV),
     (dict(xs=FAKE, rs=FAKE, D=48, sdy=48), UNS)])
 def test_glr_bwd_refuses(lib, bad, rc):
@@ -134,7 +135,7 @@ def test_workspaces(lib):
     fwd, bwd, norm = lib.kda_glr_fwd_workspace_size, lib.kda_glr_bwd_workspace_size, lib.kda_norm_bwd_workspace_size
     assert fwd(0, 64) == 0 and fwd(1, 64) == 0 and fwd(1, 0) == 0 and fwd(-1, 64) == 0
     assert fwd(8192, 64) >= 8192 // 128 * 64 * 8 and fwd(8192, 65) % 256 == 0
-    assert bwd(64, 64, 1) == 2 * 64 * 4 and bwd(64, 64, 0) == 3 * 64 * 4  # one tile: partial sums (and a state)
+    assert bwd(32, 64, 1) == 2 * 64 * 4 and bwd(32, 64, 0) == 3 * 64 * 4  # one tile: partial sums (and a state)
     assert bwd(8192, 64, 0) >= bwd(8192, 64, 1) + 8192 // 64 * 64 * 4
     assert norm(0, 1, 64) == 0 and norm(1, 1, 64) == 512 and norm(1 << 20, 16, 128) <= 2048 * 2 * 128 * 4
     assert norm(4, 1, 8193) == 0
