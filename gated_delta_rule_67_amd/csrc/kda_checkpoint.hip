@@ -23,11 +23,11 @@ constexpr int kPieces = 4;                  // of a thread
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 // 8 elements at p[off], as vectors of VEC (8: 16 bytes of bf16 or twice 16 of float32; or one by one).
-template <typename T, int VEC> __device__ __forceinline__ void read8(const T* p, float (&v)[kVec]) {
+template <typename T, int VEC, bool ONCE> __device__ __forceinline__ void read8(const T* p, float (&v)[kVec]) {
 #pragma unroll
   for (int i = 0; i < kVec; i += VEC) {
     Piece<T, VEC> q;
-    q.load(p, i);
+    q.template load<ONCE>(p, i);
     float f[VEC];
     q.get(f);
 #pragma unroll
@@ -47,7 +47,7 @@ __device__ __forceinline__ Place place(int64_t i, int per) {
   return {(int64_t)row, (int)(block - row * blocks) * kScaleBlock + (int)(i % (kScaleBlock / kVec)) * kVec};
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool ONCE>
 __global__ __launch_bounds__(kThreads) void pack_kernel(const T* __restrict__ x, int64_t ldx, uint8_t* __restrict__ codes,
                                                         uint8_t* __restrict__ scales, int64_t pieces, int per) {
   const int64_t first = (int64_t)blockIdx.x * (kThreads * kPieces) + threadIdx.x;
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const T* __restrict__ x,
 #pragma unroll
   for (int u = 0; u < kPieces; ++u) {
     const Place at = place(min(first + u * kThreads, pieces - 1), per);
-    read8<T, VEC>(x + at.row * ldx + at.col, v[u]);
+    read8<T, VEC, ONCE>(x + at.row * ldx + at.col, v[u]);
   }
 #pragma unroll
   for (int u = 0; u < kPieces; ++u) {
@@ -127,15 +127,16 @@ hipError_t launch_checkpoint_pack(const void* x, int64_t ldx, uint8_t* codes, ui
   if (pieces == 0) return hipSuccess;
   const dim3 grid(blocks_of(pieces)), block(kThreads);
   const int vec = vector_width(bf ? 8 : 4, bf ? 2 : 4, ldx, &x, 1);
+  const bool once = rows * D * (bf ? 3 : 5) > kCached;
   auto go = [&](auto kernel, auto* p) {
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, p, ldx, codes, scales, pieces, D / kVec);
   };
   if (bf) {
     const bf16* p = static_cast<const bf16*>(x);
-    vec == 8 ? go(pack_kernel<bf16, 8>, p) : go(pack_kernel<bf16, 1>, p);
+    vec < 8 ? go(pack_kernel<bf16, 1, false>, p) : once ? go(pack_kernel<bf16, 8, true>, p) : go(pack_kernel<bf16, 8, false>, p);
   } else {
     const float* p = static_cast<const float*>(x);
-    vec == 4 ? go(pack_kernel<float, 4>, p) : go(pack_kernel<float, 1>, p);
+    vec < 4 ? go(pack_kernel<float, 1, false>, p) : once ? go(pack_kernel<float, 4, true>, p) : go(pack_kernel<float, 4, false>, p);
   }
   return hipGetLastError();
 }

@@ -354,12 +354,12 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
       if (now.there) {
         piece o;
         o.set(dx);
-        o.store(ox, j, now.col);
+        o.template store<true>(ox, j, now.col);
         o.set(dr);
-        o.store(orr, j, now.col);
+        o.template store<true>(orr, j, now.col);
         if constexpr (GATE) {
           o.set(di);
-          o.store(oi, j, now.col);
+          o.template store<true>(oi, j, now.col);
         }
         if (!decltype(inside)::value && a.dinit && (m.start >> j & 1)) {
           const int n = starting_at(a.seqs, m.first, now.t0 + j);
@@ -380,9 +380,9 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
       o.set(zero);
       for (int j = 0; j < now.count; ++j) {
         if (m.valid >> j & 1) continue;
-        o.store(ox, j, now.col);
-        o.store(orr, j, now.col);
-        if constexpr (GATE) o.store(oi, j, now.col);
+        o.template store<true>(ox, j, now.col);
+        o.template store<true>(orr, j, now.col);
+        if constexpr (GATE) o.template store<true>(oi, j, now.col);
       }
     }
     s_sum[turn][wave][0].set(lane, dA);

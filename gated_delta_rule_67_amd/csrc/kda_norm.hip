@@ -17,7 +17,7 @@
 namespace kda {
 namespace norm {
 
-template <typename T, class TILE, int ROWS, bool BEHIND>
+template <typename T, class TILE, int ROWS, bool BEHIND, bool ONCE>
 __global__ __launch_bounds__(TILE::BLOCK) void fwd_kernel(NormArgs a) {
   constexpr int VEC = TILE::VEC, NC = TILE::NC;
   typedef Piece<T, VEC> piece;
@@ -48,16 +48,16 @@ __global__ __launch_bounds__(TILE::BLOCK) void fwd_kernel(NormArgs a) {
       const int64_t row = min(first + u * TILE::SIDE + side, a.rows - 1);
       const int64_t off = row_offset(a, a.v, row);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) v[u][c].load(a.v, off + col[c]);
+      for (int c = 0; c < NC; ++c) v[u][c].template load<ONCE>(a.v, off + col[c]);
       if (added) {
         const int64_t o = row_offset(a, a.other, row);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) r[u][c].load(a.other, o + col[c]);
+        for (int c = 0; c < NC; ++c) r[u][c].template load<ONCE>(a.other, o + col[c]);
       }
       if (gated) {
         const int64_t o = row_offset(a, a.gate, row);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) z[u][c].load(a.gate, o + col[c]);
+        for (int c = 0; c < NC; ++c) z[u][c].template load<ONCE>(a.gate, o + col[c]);
       }
     }
     float x[ROWS][NC][VEC], sq[ROWS];
@@ -136,14 +136,14 @@ __global__ __launch_bounds__(TILE::BLOCK) void fwd_kernel(NormArgs a) {
 
 constexpr int kFwdThreads = 256 * 2048;  // threads of a launch: every CU full
 
-template <typename T, int VEC, bool BEHIND>
+template <typename T, int VEC, bool BEHIND, bool ONCE>
 hipError_t run_fwd(const NormArgs& a, hipStream_t stream) {
   return with_tile<VEC>(a.D, [&](auto tile) {
     typedef decltype(tile) TILE;
     constexpr int ROWS = TILE::NC > 2 ? 1 : TILE::NC == 2 ? 2 : 4;
     const int64_t need = (a.rows + TILE::SIDE * ROWS - 1) / (TILE::SIDE * ROWS);
     const int64_t most = kFwdThreads / TILE::BLOCK;
-    hipLaunchKernelGGL((fwd_kernel<T, TILE, ROWS, BEHIND>), dim3((unsigned)(need < most ? need : most)),
+    hipLaunchKernelGGL((fwd_kernel<T, TILE, ROWS, BEHIND, ONCE>), dim3((unsigned)(need < most ? need : most)),
                        dim3(TILE::BLOCK), 0, stream, a);
     return hipGetLastError();
   });
@@ -192,14 +192,16 @@ hipError_t launch_norm_fwd(const NormArgs& a, bool behind, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
   const void* ptrs[] = {a.v.p, a.gate.p, a.other.p, a.y, a.extra};
   const int vec = vector_width(a.bf ? 8 : 4, a.bf ? 2 : 4, a.D | a.v.ld | a.gate.ld | a.other.ld, ptrs, 5);
+  const int tensors = 2 + (a.gate.p != nullptr) + (a.other.p != nullptr) + (a.extra != nullptr);
+  const bool once = a.rows * a.D * (a.bf ? 2 : 4) * tensors > kCached;
   auto go = [&](auto b) {
     constexpr bool B = decltype(b)::value;
     if (a.bf) {
-      if (vec == 8) return norm::run_fwd<bf16, 8, B>(a, stream);
-      return vec >= 2 ? norm::run_fwd<bf16, 2, B>(a, stream) : norm::run_fwd<bf16, 1, B>(a, stream);
+      if (vec == 8) return once ? norm::run_fwd<bf16, 8, B, true>(a, stream) : norm::run_fwd<bf16, 8, B, false>(a, stream);
+      return vec >= 2 ? norm::run_fwd<bf16, 2, B, false>(a, stream) : norm::run_fwd<bf16, 1, B, false>(a, stream);
     }
-    if (vec == 4) return norm::run_fwd<float, 4, B>(a, stream);
-    return vec == 2 ? norm::run_fwd<float, 2, B>(a, stream) : norm::run_fwd<float, 1, B>(a, stream);
+    if (vec == 4) return once ? norm::run_fwd<float, 4, B, true>(a, stream) : norm::run_fwd<float, 4, B, false>(a, stream);
+    return vec == 2 ? norm::run_fwd<float, 2, B, false>(a, stream) : norm::run_fwd<float, 1, B, false>(a, stream);
   };
   return behind ? go(std::true_type{}) : go(std::false_type{});
 }

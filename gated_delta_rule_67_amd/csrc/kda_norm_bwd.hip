@@ -20,7 +20,7 @@
 namespace kda {
 namespace norm {
 
-template <typename T, class TILE, int ROWS, bool BEHIND, bool CK>
+template <typename T, class TILE, int ROWS, bool BEHIND, bool CK, bool ONCE>
 __global__ __launch_bounds__(TILE::BLOCK) void bwd_kernel(NormArgs a) {
   constexpr int VEC = TILE::VEC, NC = TILE::NC;
   typedef Piece<T, VEC> piece;
@@ -56,19 +56,19 @@ __global__ __launch_bounds__(TILE::BLOCK) void bwd_kernel(NormArgs a) {
       const int64_t ov = row_offset(a, a.v, row), og = row_offset(a, a.dy, row);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        v[u][c].load(a.v, ov + col[c]);
-        g[u][c].load(a.dy, og + col[c]);
+        v[u][c].template load<ONCE>(a.v, ov + col[c]);
+        g[u][c].template load<ONCE>(a.dy, og + col[c]);
       }
       if (BEHIND ? gated : scaled) {
         const Source& s = BEHIND ? a.gate : a.other;
         const int64_t o = row_offset(a, s, row);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) k[u][c].load(s, o + col[c]);
+        for (int c = 0; c < NC; ++c) k[u][c].template load<ONCE>(s, o + col[c]);
       }
       if (joined) {
         const int64_t o = row_offset(a, a.dh, row);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) r[u][c].load(a.dh, o + col[c]);
+        for (int c = 0; c < NC; ++c) r[u][c].template load<ONCE>(a.dh, o + col[c]);
       }
     }
     // act(gate) of an element (its slope too): computed where it is needed, twice
@@ -194,13 +194,13 @@ inline int bwd_blocks(int64_t rows, int batch) {
   return (int)(need < kBwdBlocks ? need : kBwdBlocks);
 }
 
-template <typename T, int VEC, bool BEHIND, bool CK>
+template <typename T, int VEC, bool BEHIND, bool CK, bool ONCE>
 hipError_t run_bwd(const NormArgs& a, hipStream_t stream) {
   return with_tile<VEC>(a.D, [&](auto tile) {
     typedef decltype(tile) TILE;
     constexpr int ROWS = TILE::NC > 1 ? 1 : 2;
     const int nb = bwd_blocks(a.rows, TILE::SIDE * ROWS);
-    hipLaunchKernelGGL((bwd_kernel<T, TILE, ROWS, BEHIND, CK>), dim3(nb), dim3(TILE::BLOCK), 0, stream, a);
+    hipLaunchKernelGGL((bwd_kernel<T, TILE, ROWS, BEHIND, CK, ONCE>), dim3(nb), dim3(TILE::BLOCK), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
     return launch_column_sums({a.part, {a.dweight, a.dscale}, nb, 2, a.D}, stream);
@@ -226,14 +226,16 @@ hipError_t launch_norm_bwd(const NormArgs& a, bool behind, hipStream_t stream) {
     const int most = vector_width(a.bf ? 8 : 4, 1, 0, codes, 3);
     vec = most < vec ? most : vec;
   }
+  const int tensors = 3 + (a.gate.p != nullptr) + (a.other.p != nullptr) + (a.dh.p != nullptr) + (a.extra != nullptr);
+  const bool once = a.rows * a.D * (a.bf ? 2 : 4) * tensors > kCached;
   auto go = [&](auto b, auto k) {
     constexpr bool B = decltype(b)::value, K = decltype(k)::value;
     if (a.bf) {
-      if (vec == 8) return norm::run_bwd<bf16, 8, B, K>(a, stream);
-      return vec >= 2 ? norm::run_bwd<bf16, 2, B, K>(a, stream) : norm::run_bwd<bf16, 1, B, K>(a, stream);
+      if (vec == 8) return once ? norm::run_bwd<bf16, 8, B, K, true>(a, stream) : norm::run_bwd<bf16, 8, B, K, false>(a, stream);
+      return vec >= 2 ? norm::run_bwd<bf16, 2, B, K, false>(a, stream) : norm::run_bwd<bf16, 1, B, K, false>(a, stream);
     }
-    if (vec == 4) return norm::run_bwd<float, 4, B, K>(a, stream);
-    return vec == 2 ? norm::run_bwd<float, 2, B, K>(a, stream) : norm::run_bwd<float, 1, B, K>(a, stream);
+    if (vec == 4) return once ? norm::run_bwd<float, 4, B, K, true>(a, stream) : norm::run_bwd<float, 4, B, K, false>(a, stream);
+    return vec == 2 ? norm::run_bwd<float, 2, B, K, false>(a, stream) : norm::run_bwd<float, 1, B, K, false>(a, stream);
   };
   if (behind) return a.packed ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
   return a.packed ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
