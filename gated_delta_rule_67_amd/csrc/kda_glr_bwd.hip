@@ -18,7 +18,6 @@ namespace kda {
 namespace glr {
 
 constexpr int kBwdTokens = 8, kBwdWaves = 8;
-constexpr int kAtOnce = 2;
 constexpr int kBwdTile = kBwdTokens * kBwdWaves;
 static_assert(kBwdTile == kGlrBlock, "a tile begins at a kept state");
 
@@ -259,8 +258,6 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
 #pragma unroll
           for (int e = 0; e < VEC; ++e) A[e] *= av[j][e];
         }
-        // a few elements at a time: the gates of all at once would need registers that are not there
-        if (j % kAtOnce == kAtOnce - 1) __builtin_amdgcn_sched_barrier(0);
       }
       states(inside, [&](int j, int e) { return b[j][e]; }, [](int) {});
       grads(inside, [&](int j) {
@@ -311,7 +308,6 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
       });
     };
     whole ? slopes(std::true_type{}) : slopes(std::false_type{});
-    __builtin_amdgcn_sched_barrier(0);
     // (row 0 where no tile is left: the registers are then not the old values' any more)
     const bool more = next.q < chain.nq;
     Part p;
