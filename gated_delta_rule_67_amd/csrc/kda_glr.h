@@ -287,6 +287,36 @@ template <int VEC> struct Lanes {
   }
 };
 
+// What a lane holds of a tensor over its wave's span of NT tokens.
+template <typename T, int VEC, int NT, bool CK> struct Held {
+  Piece<T, VEC> at[NT];
+  static __device__ __forceinline__ Rows rows(const Source& s, int64_t t, int n, int D) { return Piece<T, VEC>::rows(s, t, n, D); }
+  __device__ __forceinline__ void begin(const Rows&, int, int, int) {}
+  __device__ __forceinline__ void load(const Rows& r, int j, int row, int col) { at[j].load(r, row, col); }
+  __device__ __forceinline__ void get(int j, float (&v)[VEC]) const { at[j].get(v); }
+};
+// A checkpoint's: a span has 2 VEC scales a token, one load brings a scale to a lane, and they are passed
+// between lanes where they are used (every lane takes part).
+template <typename T, int VEC, int NT> struct Held<T, VEC, NT, true> {
+  static constexpr int kScales = 64 * VEC / kScaleBlock;
+  static_assert(kScales * NT <= 64, "a scale a lane");
+  unsigned word[NT], scale;
+  static __device__ __forceinline__ Rows rows(const Source& s, int64_t t, int n, int D) { return PackedPiece<VEC>::rows(s, t, n, D); }
+  // c0: the wave's first channel
+  __device__ __forceinline__ void begin(const Rows& r, int n, int c0, int D) {
+    const int lane = __lane_id(), j = min(lane / kScales, n - 1);
+    const int block = min(c0 / kScaleBlock + lane % kScales, D / kScaleBlock - 1);
+    scale = __builtin_amdgcn_raw_buffer_load_b8(r.scales, j * r.ld_scales + block, 0, 0);
+  }
+  __device__ __forceinline__ void load(const Rows& r, int j, int row, int col) { word[j] = PackedPiece<VEC>::codes(r, row, col); }
+  __device__ __forceinline__ void get(int j, float (&v)[VEC]) const {
+    PackedPiece<VEC> p;
+    p.word[0] = word[j];
+    p.byte = __builtin_amdgcn_ds_bpermute((j * kScales + (int)__lane_id() * VEC / kScaleBlock) * 4, scale);
+    p.get(v);
+  }
+};
+
 // Which tokens of a wave's span begin or end a sequence, or lie in one: bit j is token t0 + j.
 struct Marks {
   unsigned start, end, valid;

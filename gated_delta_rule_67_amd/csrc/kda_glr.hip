@@ -57,7 +57,7 @@ template <typename T, int VEC, bool CK, bool GATE, bool NORM>
 __global__ __launch_bounds__(64 * (FwdTile<VEC>::kWaves + 1)) void fwd_kernel(GlrArgs a, Chain chain) {
   constexpr int NT = FwdTile<VEC>::kTokens, NW = FwdTile<VEC>::kWaves, kFwdTile = NT * NW, C = 64 * VEC;
   constexpr unsigned kFull = 0xffffffffu >> (32 - NT);
-  typedef typename KeptPiece<T, VEC, CK>::type piece;
+  typedef Held<T, VEC, FwdTile<VEC>::kTokens, CK> held;
   // Of this turn's tile and of the one before: the spans' maps, which the chain wave replaces by the maps
   // from the tile's front to each span's, and whether a sequence begins in them; the state in front of the
   // tile; the products of decays (the last of a span in registers: two workgroups fit a CU's LDS).
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(64 * (FwdTile<VEC>::kWaves + 1)) void fwd_kernel(Gl
   // A part's inputs: two of these take turns, so that a tile's loads are under way while the one in front
   // of it is worked on.
   struct Raw {
-    piece x[NT], r[NT], in[NT];
+    held x, r, in;
     float rate[VEC], bias[VEC];  // A_log and dt_bias
     Part at;
   };
@@ -169,14 +169,17 @@ __global__ __launch_bounds__(64 * (FwdTile<VEC>::kWaves + 1)) void fwd_kernel(Gl
     }
     // rows that are there: the last one again behind the last token
     const int t = min(max(p.t0, 0), a.T - 1), rows = min(a.T - t, NT);
-    const Rows rx = piece::rows(a.x, t, rows, a.D), rr = piece::rows(a.r, t, rows, a.D);
-    const Rows ri = piece::rows(GATE ? a.in : a.x, t, rows, a.D);
+    const Rows rx = held::rows(a.x, t, rows, a.D), rr = held::rows(a.r, t, rows, a.D);
+    const Rows ri = held::rows(GATE ? a.in : a.x, t, rows, a.D);
+    w.r.begin(rr, rows, p.column * C, a.D);
+    w.x.begin(rx, rows, p.column * C, a.D);
+    if constexpr (GATE) w.in.begin(ri, rows, p.column * C, a.D);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int row = min(j, rows - 1);
-      w.r[j].load(rr, row, col);
-      w.x[j].load(rx, row, col);
-      if constexpr (GATE) w.in[j].load(ri, row, col);
+      w.r.load(rr, j, row, col);
+      w.x.load(rx, j, row, col);
+      if constexpr (GATE) w.in.load(ri, j, row, col);
     }
   };
   // A span's states from zero in front of it, the product of its decays, and where it lies.
@@ -193,9 +196,9 @@ __global__ __launch_bounds__(64 * (FwdTile<VEC>::kWaves + 1)) void fwd_kernel(Gl
     for (int e = 0; e < VEC; ++e) ch[e] = channel(w.rate[e], a.dt_bias ? w.bias[e] : 0.f), hs[e] = 0.f, ps[e] = 1.f;
     auto token = [&](int j, float (&av)[VEC], float (&bv)[VEC]) {
       float xv[VEC], rv[VEC], iv[VEC];
-      w.x[j].get(xv);
-      w.r[j].get(rv);
-      if constexpr (GATE) w.in[j].get(iv);
+      w.x.get(j, xv);
+      w.r.get(j, rv);
+      if constexpr (GATE) w.in.get(j, iv);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         float b = xv[e];

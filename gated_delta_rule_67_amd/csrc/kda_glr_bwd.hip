@@ -25,7 +25,7 @@ template <typename T, int VEC, bool CK, bool GATE, bool NORM>
 __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Chain chain) {
   constexpr int NT = kBwdTokens, NW = kBwdWaves, C = 64 * VEC;
   constexpr unsigned kFull = 0xffffffffu >> (32 - NT);
-  typedef typename KeptPiece<T, VEC, CK>::type kept;
+  typedef Held<T, VEC, NT, CK> held;
   typedef Piece<T, VEC> piece;
   // A span's decays, its state and its gradient, each from zero, and whether a sequence ends in it; the map
   // (decays, gradient) from behind the tile to behind each span; the gradient that reaches the tile from
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
   }
 
   struct Part {
-    int t0, count, col;
+    int t0, count, c0, col;  // c0: the wave's first channel
     bool there;
     Marks m;
   };
@@ -138,7 +138,8 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
     const int tile0 = first_token(t.q);
     p.t0 = tile0 + wave * NT;
     p.count = min(max(a.T - p.t0, 0), NT);
-    p.col = t.column * C + k0;
+    p.c0 = t.column * C;
+    p.col = p.c0 + k0;
     p.there = p.col < a.D;
     if (!p.there) p.col = a.D - VEC;
     if (t.bos < tile0 && t.eos >= tile0 + kBwdTile) p.m = Marks{0, 0, kFull, 0, t.bos, t.eos};
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
     else p.m = Marks{};
     return p;
   };
-  kept xk[NT], rk[NT], ik[NT];
+  held xk, rk, ik;
   piece gk[NT];
   float rate[VEC], bias[VEC];
   Part at;
@@ -159,14 +160,17 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
       bias[e] = db[p.col + e];
     }
     const int rows = max(p.count, 1), t = min(p.t0, a.T - 1);
-    const Rows rx = kept::rows(a.x, t, rows, a.D), rr = kept::rows(a.r, t, rows, a.D);
-    const Rows ri = kept::rows(GATE ? a.in : a.x, t, rows, a.D), rg = piece::rows(a.dy, t, rows, a.D);
+    const Rows rx = held::rows(a.x, t, rows, a.D), rr = held::rows(a.r, t, rows, a.D);
+    const Rows ri = held::rows(GATE ? a.in : a.x, t, rows, a.D), rg = piece::rows(a.dy, t, rows, a.D);
+    rk.begin(rr, rows, p.c0, a.D);
+    xk.begin(rx, rows, p.c0, a.D);
+    if constexpr (GATE) ik.begin(ri, rows, p.c0, a.D);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int row = min(j, rows - 1);
-      rk[j].load(rr, row, p.col);
-      xk[j].load(rx, row, p.col);
-      if constexpr (GATE) ik[j].load(ri, row, p.col);
+      rk.load(rr, j, row, p.col);
+      xk.load(rx, j, row, p.col);
+      if constexpr (GATE) ik.load(ri, j, row, p.col);
       gk[j].load(rg, row, p.col);
     }
   };
@@ -230,9 +234,9 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
       for (int j = 0; j < NT; ++j) {
         float rv[VEC], iv[VEC], xv[VEC], cx[VEC], ci[VEC], lg[VEC];
         dy[j] = gk[j];
-        rk[j].get(rv);
-        xk[j].get(xv);
-        if constexpr (GATE) ik[j].get(iv);
+        rk.get(j, rv);
+        xk.get(j, xv);
+        if constexpr (GATE) ik.get(j, iv);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           float slope, s = 1.f, rest = 0.f;
@@ -311,7 +315,7 @@ __global__ __launch_bounds__(64 * (kBwdWaves + 1)) void bwd_kernel(GlrArgs a, Ch
     // (row 0 where no tile is left: the registers are then not the old values' any more)
     const bool more = next.q < chain.nq;
     Part p;
-    p.t0 = 0, p.count = 1, p.col = min(k0, a.D - VEC), p.there = false, p.m = Marks{};
+    p.t0 = 0, p.count = 1, p.c0 = 0, p.col = min(k0, a.D - VEC), p.there = false, p.m = Marks{};
     if (more) p = part(next);
     fetch(p);
     lds_barrier();

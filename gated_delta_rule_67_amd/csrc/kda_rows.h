@@ -113,12 +113,11 @@ template <int VEC> struct PackedPiece {
     r.ld = (int)s.ld, r.ld_scales = (int)few;
     return r;
   }
-  __device__ __forceinline__ void load(const Rows& r, int row, int col) {
+  static __device__ __forceinline__ unsigned codes(const Rows& r, int row, int col) {
     static_assert(VEC <= 4, "a word of codes a lane");
-    if constexpr (VEC == 4) word[0] = __builtin_amdgcn_raw_buffer_load_b32(r.p, col, row * r.ld, 0);
-    else if constexpr (VEC == 2) word[0] = __builtin_amdgcn_raw_buffer_load_b16(r.p, col, row * r.ld, 0);
-    else word[0] = __builtin_amdgcn_raw_buffer_load_b8(r.p, col, row * r.ld, 0);
-    byte = __builtin_amdgcn_raw_buffer_load_b8(r.scales, col / kScaleBlock, row * r.ld_scales, 0);
+    if constexpr (VEC == 4) return __builtin_amdgcn_raw_buffer_load_b32(r.p, col, row * r.ld, 0);
+    else if constexpr (VEC == 2) return __builtin_amdgcn_raw_buffer_load_b16(r.p, col, row * r.ld, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b8(r.p, col, row * r.ld, 0);
   }
   __device__ __forceinline__ void get(float (&v)[VEC]) const {
     const float f = scale_of(byte);
@@ -160,8 +159,8 @@ struct ColumnSums {
 };
 hipError_t launch_column_sums(const ColumnSums& a, hipStream_t stream);
 
-// The largest vector, of at most `most` elements (4 bytes or 16 of them, or one), that the widths and
-// strides (or-ed together) and the addresses allow.
+// The largest vector, of `most` elements or a half, a quarter ... of them, that the widths and strides
+// (or-ed together) and the addresses allow.
 inline int vector_width(int most, int esize, int64_t widths, const void* const* ptrs, int n) {
   uintptr_t bits = 0;
   for (int i = 0; i < n; ++i) bits |= reinterpret_cast<uintptr_t>(ptrs[i]);
