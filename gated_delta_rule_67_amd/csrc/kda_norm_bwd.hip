@@ -11,6 +11,9 @@
 // that every tensor moves once and HBM bounds the kernel. A thread keeps its columns over all of its
 // rows and adds dweight and dscale up in registers; workgroups leave partial sums, which a second
 // kernel adds in a fixed order.
+// Measured: behind, 524288 rows of 128 in bf16 under a gate 139 us (671 MB, 4.8 TB/s: the gate's activation is
+// computed twice, since registers for both uses cost more; 1, 2, 3 and 4 rows at a time 149, 148, 168 and
+// 170 us before loads went past the caches); in front, 5003 rows of 1030 in float32 28.5 us (124 MB).
 // v (and the gate, and x in front) may be 8-bit checkpoints: the gradients are those at the values
 // that these stand for, and the tensor moves 33 bytes for every 32 elements.
 #include <type_traits>
@@ -186,7 +189,8 @@ __global__ __launch_bounds__(TILE::BLOCK) void bwd_kernel(NormArgs a) {
 }
 
 // Workgroups of a launch at most: three of 256 threads a CU in one round (their partial sums are
-// written and read once more, 8 bytes a column each).
+// written and read once more, 8 bytes a column each). 2, 3, 4, 6 and 8 a CU: 28.5, 28.5, 29.7, 33 and
+// 34.6 us for 5003 rows of 1030.
 constexpr int kBwdBlocks = 3 * 256;
 
 inline int bwd_blocks(int64_t rows, int batch) {

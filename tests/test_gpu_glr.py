@@ -178,6 +178,15 @@ def test_many_tiles(lengths, dtype, D):
     _check(_make(lengths, D, dt, len(lengths), rate=-5.0), dt)
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 10), ("f32", 3)])
+def test_many_empty_sequences(dtype, D):
+    """Empty sequences by the hundreds, in front, inside a span of tokens, between spans and at the end."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    lengths = [0] * 70 + [3] + [0] * 700 + [1, 1, 1] + [0] * 65 + [2, 0, 130] + [0] * 900 + [64] + [0] * 300 + [49] + [0] * 200
+    _check(_make(lengths, D, dt, D), dt)
+    _check(_make(lengths, D, dt, D, head=4, tail=9), dt)
+
+
 @pytest.mark.parametrize("lengths,D,dtype,in_gate", [([90, 0, 33], 64, "bf16", True), ([700], 32, "f32", True),
                                                      ([1300, 20], 96, "bf16", False), ([59, 61, 60, 1, 900], 288, "bf16", True),
                                                      ([4000], 64, "bf16", True)])
