@@ -3,8 +3,8 @@
 //   g_t = -exp(A_log) softplus(gate_x_t + dt_bias),  a_t = exp(g_t)       (the standard decay gate)
 //   h_t = a_t h_{t-1} + w_t logistic(in_gate_t) x_t,  w_t = sqrt(1 - a_t^2) or 1;   y_t = h_t
 //
-// 39 instructions of the vector ALU an element, six of them transcendental (which take twice the others'
-// time), and 8 bytes in bf16: the vector ALU is busy 62% of the time, HBM moves 4.2 TB/s, so the gates are
+// 38 instructions of the vector ALU an element, six of them transcendental (which take twice the others'
+// time), and 8 bytes in bf16: the vector ALU is busy 64% of the time, HBM and the last-level cache bring 4.2 TB/s, so the gates are
 // computed once and every tensor moves once. A wave holds a span of tokens for 64 VEC channels: the states
 // from zero in registers, and in LDS the products of decays with which the state in front of the span
 // enters them. That state comes through the waves of the workgroup and the chain of tiles (kda_glr.h); the

@@ -58,7 +58,8 @@ __device__ __forceinline__ int64_t row_offset(const NormArgs& a, const Source& s
   return token * s.ld + (row - token * a.G) * a.D;
 }
 
-// The tile of the fewest threads whose vectors hold a row, out of a list; go.template operator()<Tile>().
+// The tile of the fewest threads whose vectors hold a row, out of a list. Three vectors a thread for 1030
+// columns of float32 (the backward pass 28.5 us over 5003 rows; with four, of which the last is empty, 34).
 template <int VEC, class F> inline hipError_t with_tile(int D, F&& go) {
   if constexpr (VEC >= 4) {
     if (D <= 8 * VEC) return go(Tile<VEC, 8, 1>{});
