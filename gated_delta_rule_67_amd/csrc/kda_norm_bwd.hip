@@ -11,8 +11,8 @@
 // that every tensor moves once and HBM bounds the kernel. A thread keeps its columns over all of its
 // rows and adds dweight and dscale up in registers; workgroups leave partial sums, which a second
 // kernel adds in a fixed order.
-// Measured: behind, 524288 rows of 128 in bf16 under a gate 139 us (671 MB, 4.8 TB/s: the gate's activation is
-// computed twice, since registers for both uses cost more; 1, 2, 3 and 4 rows at a time 149, 148, 168 and
+// Measured: behind, 524288 rows of 128 in bf16 under a gate 139 us (671 MB, 4.8 TB/s; the gate's activation is
+// computed twice: kept in registers between its uses, 145 us; 1, 2, 3 and 4 rows at a time 149, 148, 168 and
 // 170 us before loads went past the caches); in front, 5003 rows of 1030 in float32 28.5 us (124 MB).
 // v (and the gate, and x in front) may be 8-bit checkpoints: the gradients are those at the values
 // that these stand for, and the tensor moves 33 bytes for every 32 elements.
