@@ -77,18 +77,28 @@ def _bounds(x, r, A, b, i, h0, dy, df, normalise):
     return Ey, E, Edx, Edr, Edi, F + U * G, (dg * np.abs(g)).sum(0), EdA, (rate * l * dg).sum(0), Edr.sum(0)
 
 
+def _at_odd_address(codes):
+    there = torch.empty(codes.numel() + 1, dtype=torch.uint8, device="cuda")[1:].view(codes.dtype).view(codes.shape)
+    there.copy_(codes)
+    assert there.data_ptr() % 2 == 1 and there.is_contiguous()
+    return there
+
+
 def _value(t):
     if isinstance(t, tuple):
         return to64(kda.kda_checkpoint_unpack(t[0], t[1], torch.float32))
     return None if t is None else to64(t)
 
 
-def _check(d, dtype, normalise=True, packed=False, dense=False, states=True):
+def _check(d, dtype, normalise=True, packed=False, dense=False, states=True, odd=False):
     half, cu = HALF[dtype], d["cu"].cpu().numpy()
     N, T = len(cu) - 1, d["x"].shape[0]
     kept = {k: d[k] for k in ("x", "gate_x", "in_gate")}
     if packed:
         kept = {k: None if v is None else kda.kda_checkpoint_pack(v) for k, v in kept.items()}
+        hk = {k: _value(v) for k, v in kept.items()}  # kda_checkpoint_unpack takes aligned codes only
+        if odd:
+            kept = {k: None if v is None else (_at_odd_address(v[0]), v[1]) for k, v in kept.items()}
     shaped = lambda v: v if v is None or not dense else (  # noqa: E731
         tuple(shaped(u) for u in v) if isinstance(v, tuple) else v.unflatten(0, (N, -1)))
     off = None if dense else d["cu"]
@@ -102,7 +112,7 @@ def _check(d, dtype, normalise=True, packed=False, dense=False, states=True):
             assert (a is None and b is None) or torch.equal(a, b)
     torch.cuda.synchronize()
     h = {k: _value(v) for k, v in d.items()}
-    hk = {k: _value(v) for k, v in kept.items()}
+    hk = hk if packed else {k: _value(v) for k, v in kept.items()}
     flat = lambda v: None if v is None else v.reshape(d["dy"].shape)  # noqa: E731
     y, (dx, dr, di, dA, db, dinit) = flat(y), (flat(got[0]), flat(got[1]), flat(got[2])) + got[3:]
     sA = sb = rA = rb = 0.0
@@ -193,6 +203,12 @@ def test_many_empty_sequences(dtype, D):
 def test_backward_from_checkpoints(lengths, D, dtype, in_gate):
     dt = torch.bfloat16 if dtype == "bf16" else torch.float32
     _check(_make(lengths, D, dt, D, in_gate=in_gate, tail=5), dt, packed=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_backward_from_checkpoints_at_odd_addresses(dtype):
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    _check(_make([90, 0, 333], 96, dt, 5, tail=5), dt, packed=True, odd=True)
 
 
 def test_empty_calls():
