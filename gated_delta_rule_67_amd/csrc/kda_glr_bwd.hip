@@ -10,7 +10,7 @@
 // comes from the states in front of blocks that the forward pass kept (or, without them, from its
 // kernel run for the states only), so every tensor moves once: 14 bytes an element in bf16. The gates
 // are computed once; what the outputs need of them and nothing in between waits in LDS, the rest in
-// registers, of which a span of 8 tokens takes 159.
+// registers, of which a span of 8 tokens takes 156 (163 from checkpoints).
 //
 // Measured: 270 us at 4 x 8192 tokens of 2048 channels, bf16, with both gates (940 MB, 3.5 TB/s); without any
 // waiting for the chain 10 us less. Bound by the gates' and gradients' instructions: 4 tokens x 14 waves 310 us,
