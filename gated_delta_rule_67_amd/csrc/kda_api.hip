@@ -938,7 +938,7 @@ int kda_glr_step(const void* x, int64_t x_stride, const void* gate_x, int64_t ga
   if (!source(&a.x, x, nullptr, x_stride, B, D) || !source(&a.r, gate_x, nullptr, gate_x_stride, B, D) ||
       !source(&a.in, in_gate, nullptr, in_gate_stride, B, D))
     return KDA_ERR_INVALID;
-  if ((int64_t)B * (D / 256 + 1) >= (1 << 23)) return KDA_ERR_UNSUPPORTED;
+  if ((int64_t)B * ((D + 255) / 256) >= (1 << 23)) return KDA_ERR_UNSUPPORTED;
   a.A_log = A_log, a.dt_bias = dt_bias, a.pool = state_pool, a.slots = slots, a.nslots = num_slots, a.B = B, a.D = D;
   a.y = y, a.normalise = (flags & KDA_GLR_NORMALISE) != 0, a.bf = dtype == KDA_DTYPE_BF16;
   return norm_status(kda::launch_glr_step(a, static_cast<hipStream_t>(stream)));
