@@ -682,6 +682,11 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _require_ints(what, *sizes):
+    """Sizes that the C ABI takes as ints (ctypes would pass on their low 32 bits)."""
+    _require(max(sizes) < 1 << 31, f"{what} must be fewer than 2^31")
+
+
 def _fresh(t):
     """An uninitialised contiguous tensor shaped and typed like t."""
     return torch.empty_like(t, memory_format=torch.contiguous_format)
@@ -727,6 +732,7 @@ def _sequences(x, cu_seqlens, dims, index):
         _require(x.dim() == dims, "x must be a batch [B, T, ...] (packed sequences: give cu_seqlens)")
         N, T = x.shape[0], x.shape[0] * x.shape[1]
         _require(N >= 1 and T < 1 << 31, "x must have at least one sequence and fewer than 2^31 tokens")
+        _require_ints("sequences", N)
         return 2, N, T
     _require(cu_seqlens.get_device() == index and cu_seqlens.dtype is torch.int32
              and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous() and cu_seqlens.numel() >= 2,
@@ -735,6 +741,7 @@ def _sequences(x, cu_seqlens, dims, index):
     _require(lead == 1 or (lead == 2 and x.shape[0] == 1), "packed x must be [T, ...] or [1, T, ...]")
     T = x.shape[lead - 1]
     _require(T < 1 << 31, "x must have fewer than 2^31 tokens")
+    _require_ints("sequences", cu_seqlens.numel() - 1)
     return lead, cu_seqlens.numel() - 1, T
 
 
@@ -809,6 +816,7 @@ def kda_conv_bwd(x, weight, dy, bias=None, initial_state=None, dfinal_state=None
 
 
 def _slots(slots, B, num_slots, index):
+    _require_ints("requests and slots", B, num_slots)
     if slots is None:
         _require(num_slots >= B, "without slots the pool needs a state per request")
         return None
@@ -898,6 +906,7 @@ def _pools(pools):
     n = len(pools)
     _require(n > 0, "at least one pool is needed")
     index, num_slots = pools[0].get_device(), pools[0].shape[0] if pools[0].dim() else 0
+    _require_ints("slots", num_slots)
     _require(index >= 0, "pools must be on a GPU")
     base, size = [], []
     for p in pools:
@@ -981,6 +990,7 @@ def _row_layout(like, named):
         if lead < 2:
             raise
         G = shape[-2]
+        _require_ints("rows of a token", G)
         return rows // G, G, {n: _token_stride(n, t, lead - 1, G * D) for n, t in given}
 
 
@@ -988,6 +998,7 @@ def _norm_args(x, weight, scale):
     index, code = _gpu(x)
     _require(x.dim() >= 1 and x.shape[-1] >= 1, "x must have at least one column")
     D = x.shape[-1]
+    _require_ints("columns", D)
     _dense("weight", weight, (D,), torch.float32, index)
     _dense("scale", scale, (D,), torch.float32, index)
     return index, code, D
@@ -1083,6 +1094,7 @@ def kda_checkpoint_pack(x):
     index, code = _gpu(x)
     _require(x.dim() >= 1 and x.shape[-1] % 32 == 0 and x.shape[-1] > 0, "x must have a multiple of 32 channels")
     T, G, ld = _row_layout(x, (("x", x),))
+    _require_ints("channels of a token", G * x.shape[-1])
     codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     scales = torch.empty(x.shape[:-1] + (x.shape[-1] // 32,), dtype=torch.uint8, device=x.device)
     _call(index, library().kda_checkpoint_pack, x.data_ptr(), ld["x"], codes.data_ptr(), scales.data_ptr(), T,
@@ -1095,6 +1107,7 @@ def kda_checkpoint_unpack(codes, scales, dtype=torch.bfloat16):
     index = codes.get_device()
     _require(index >= 0, "inputs must be on a GPU")
     _require(codes.dim() >= 1 and codes.shape[-1] > 0, "codes must have at least one channel")
+    _require_ints("channels", codes.shape[-1])
     _require(dtype in _DTYPE, f"unsupported dtype {dtype}")
     _checkpoint("checkpoint", (codes, scales), codes.shape, index)
     x = torch.empty(codes.shape, dtype=dtype, device=codes.device)
@@ -1106,6 +1119,7 @@ def kda_checkpoint_unpack(codes, scales, dtype=torch.bfloat16):
 
 def _glr_params(D, A_log, dt_bias, index):
     _require(D >= 1, "x must have at least one channel")
+    _require_ints("channels", D)
     _dense("A_log", A_log, (D,), torch.float32, index)
     _dense("dt_bias", dt_bias, (D,), torch.float32, index)
 

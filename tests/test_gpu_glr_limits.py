@@ -1,4 +1,4 @@
-"""Calls at the limits that the recurrence's documentation names."""
+"""Calls at and past the limits that the recurrence's documentation names, and sizes past 32 bits."""
 
 import pytest
 import torch
@@ -32,3 +32,31 @@ def test_step_of_as_many_requests_as_are_allowed(D, B):
 def test_step_of_more_requests_is_refused(D, B):
     assert kda.library().kda_glr_step(FAKE, D, FAKE, D, FAKE, None, None, 0, FAKE, FAKE, 8, FAKE, B, D, 0, 1, None) \
         == kda.KDA_ERR_UNSUPPORTED
+
+
+BIG = 1 << 32
+
+
+def test_sizes_past_32_bits_are_refused_by_the_checks():
+    """ctypes passes on an int's low 32 bits: such a size must not reach it."""
+    huge = torch.empty(BIG + 1, 0, 8, device="meta")
+    for call in (lambda: kda._sequences(huge, None, 3, -1), lambda: kda._slots(None, 3, BIG + 5, -1),
+                 lambda: kda._sequences(torch.empty(5, 8, device="meta"), torch.empty(BIG + 2, dtype=torch.int32, device="meta"), 3, -1),
+                 lambda: kda._glr_params(BIG + 64, None, None, -1)):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.gpu
+def test_sizes_past_32_bits_are_refused():
+    flat = torch.empty(BIG + 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        kda.kda_checkpoint_pack(flat)
+    with pytest.raises(ValueError):
+        kda.kda_checkpoint_unpack(flat[:BIG // 2 + 32].view(torch.float8_e4m3fn), flat[:BIG // 64 + 1].view(torch.uint8))
+    del flat
+    one, pool = torch.ones(1, 1, device="cuda"), torch.empty(BIG + 5, 1, device="cuda")
+    with pytest.raises(ValueError):
+        kda.kda_glr_step(one, one, one[0], pool, slots=torch.tensor([7], dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        kda.kda_glr_fwd(torch.empty(BIG + 1, 0, 1, device="cuda"), torch.empty(BIG + 1, 0, 1, device="cuda"), one[0])
