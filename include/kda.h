@@ -709,7 +709,8 @@ int kda_checkpoint_unpack(const void* codes, const void* scales, void* x, int64_
  *
  * The token axis is scanned in one pass of the data; results are bitwise reproducible. Tokens of other
  * sequences, and tokens behind, do not reach an output, finite or not; behind a state that is not finite,
- * NaN may stand for an infinity. The softplus, decays and weights have a relative error of about 1e-6.
+ * NaN may stand for an infinity. The softplus and the log decay have a relative error of about 1e-6 +
+ * 2.3 2^-24 |gate_x + dt_bias| (the sum is rounded to float32 once, however large its terms).
  * N >= 1, T >= 0, D >= 1 (else KDA_ERR_INVALID); N <= 2^17, D <= 2^20, T <= 2^30, T D < 2^35, N D < 2^31 (else
  * KDA_ERR_UNSUPPORTED). No alignment is required. Nothing is allocated.
  */
