@@ -62,7 +62,7 @@ __device__ __forceinline__ Channel channel(const GlrArgs& a, int c) {
 // log2 of the decay, g2 <= 0, for the gate's input; e = 2^-|z2| and u = fl(1 + e) are left for the
 // softplus' slope. z = x + bias is rounded before it is scaled: x log2 e + (bias log2 e) in one instruction
 // carries the second product's rounding, which stays where a large bias cancels (softplus off by 6e-6 at 100;
-// the instruction more costs the backward pass 6 of 270 us, the forward pass nothing). With z2 = z log2 e,
+// the instruction more costs the backward pass 2 of 267 us, the forward pass nothing). With z2 = z log2 e,
 // softplus(z) log2 e = max(z2, 0) + log2(1 + e), and the rounding d of 1 + e is taken back at first order,
 // log2(1 + e) = log2(u) - d log2 e (the factor 1 / u of that term is left out: it is off by e d at most, under
 // 2^-24 of the result), so that the value keeps its relative accuracy however small e is.
@@ -134,10 +134,11 @@ __device__ __forceinline__ float input_weight(float a, float g2, float& inv) {
 // 8192 x 2048, 200, 203 and 229 (all before later steps).
 constexpr int kGroup = 8;
 constexpr unsigned kAbsent = 0xffffffffu;
-constexpr int kPolls = 1 << 20;  // of the words in front of a tile at most (about half a second): then NaN
+constexpr int kPolls = 1 << 20;  // looks at the words in front of a tile at most (about half a second): then NaN
+constexpr unsigned kGaveUp = 1;  // left behind the ticket by a wait that ran out of them
 
 struct Chain {
-  unsigned* ticket;    // counter
+  unsigned* ticket;    // counter; behind it, kGaveUp once a wait has given up (no kernel clears it)
   uint64_t* map;       // [nq][D]: A in the upper, B in the lower half
   unsigned* state;     // [groups][D]
   int nq, ncol;        // tiles along the tokens, columns of tiles
@@ -228,6 +229,7 @@ __device__ __forceinline__ void wait_front(const Chain& c, int q, int q0, int D,
     open = left;
     if (open) __builtin_amdgcn_s_sleep(1);
   }
+  if (open && __lane_id() == 0) __hip_atomic_store(c.ticket + 1, kGaveUp, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
   for (int e = 0; e < VEC; ++e) front[e] = __uint_as_float(s[e]);  // still absent: all ones is a NaN
 #pragma unroll

@@ -711,6 +711,12 @@ int kda_checkpoint_unpack(const void* codes, const void* scales, void* x, int64_
  * sequences, and tokens behind, do not reach an output, finite or not; behind a state that is not finite,
  * NaN may stand for an infinity. The softplus and the log decay have a relative error of about 1e-6 +
  * 2.3 2^-24 |gate_x + dt_bias| (the sum is rounded to float32 once, however large its terms).
+ * A tile of tokens waits for those in front of it, on work that is already running only, and a bounded time all
+ * the same (2^20 looks, about half a second). A wait that gives up, which no input is known to cause, leaves NaN in
+ * the states from there on to the sequence's end (backward: in the gradients, to its beginning), which nothing
+ * else tells from NaN of the data; the call has returned KDA_OK. It also sets the second 32-bit word of the workspace
+ * to 1. Calls of more than 64 tokens, forward or backward, leave that word as it was otherwise: who wants to know
+ * clears it once and looks at it later.
  * N >= 1, T >= 0, D >= 1 (else KDA_ERR_INVALID); N <= 2^17, D <= 2^20, T <= 2^30, T D < 2^35, N D < 2^31 (else
  * KDA_ERR_UNSUPPORTED). No alignment is required. Nothing is allocated.
  */

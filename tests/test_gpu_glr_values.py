@@ -43,3 +43,33 @@ def test_far_negative_gates(bias):
     zz, _, _, w, _ = glr_gates(to64(r), to64(A), to64(b))
     close(y, w, np.abs(w) * ((17 + 2.3 * np.abs(zz)) / 2 + 20) * U, "y")
     assert torch.equal(y, pool)
+
+
+@pytest.mark.parametrize("lengths,D,dtype,packed", [([65], 64, "bf16", False), ([121, 200], 65, "f32", False),
+                                                    ([5000, 3192], 2048, "bf16", False), ([65], 64, "bf16", True),
+                                                    ([3000, 1000], 256, "bf16", True)])
+def test_no_wait_gives_up(lengths, D, dtype, packed):
+    """The second word of a workspace tells of waits that gave up: every call leaves it as it was, whatever the rest
+    of the workspace held."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    d, lib, s = _make(lengths, D, dt, D), kda.library(), torch.cuda.current_stream().cuda_stream
+    T, N = sum(lengths), len(lengths)
+    n, m, k = lib.kda_glr_fwd_workspace_size(T, D), lib.kda_glr_bwd_workspace_size(T, D, 0), lib.kda_glr_bwd_workspace_size(T, D, 1)
+    y, dx, dr, di = (torch.empty_like(d["x"]) for _ in range(4))
+    states, dA = torch.empty((T + 63) // 64, D, device="cuda"), torch.empty(D, device="cuda")
+    p = lambda t: t.data_ptr()  # noqa: E731
+    held = [kda.kda_checkpoint_pack(d[v]) if packed else (d[v], None) for v in ("x", "gate_x", "in_gate")]
+    kept = [(p(a), None if b is None else p(b), D) for a, b in held]
+    for fill in (0, 0xff, 0x5a):
+        ws = torch.full((max(n, m, k) // 4,), fill * 0x01010101 - (1 << 32 if fill > 127 else 0), dtype=torch.int32, device="cuda")
+        for clear in (0, 7):
+            ws[1] = clear
+            assert lib.kda_glr_fwd(p(d["x"]), D, p(d["gate_x"]), D, p(d["A_log"]), p(d["dt_bias"]), p(d["in_gate"]), D, p(d["init"]),
+                                   p(d["cu"]), N, None, p(y), p(states), T, D, 4, int(dt is torch.bfloat16), p(ws), n, s) == 0
+            assert int(ws[1]) == clear
+            for have, size in ((None, m),) if packed else ((None, m), (p(states), k)):
+                assert lib.kda_glr_bwd(*kept[0], *kept[1], p(d["A_log"]), p(d["dt_bias"]), *kept[2], p(d["init"]), p(d["cu"]), N,
+                                       p(d["dy"]), D, None, have, p(dx), p(dr), p(di), p(dA), None, None, T, D, 4,
+                                       int(dt is torch.bfloat16), p(ws), size, s) == 0
+                assert int(ws[1]) == clear
+    assert bool(torch.isfinite(dA).all())
