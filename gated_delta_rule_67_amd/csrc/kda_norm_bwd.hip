@@ -230,8 +230,11 @@ hipError_t launch_norm_bwd(const NormArgs& a, bool behind, hipStream_t stream) {
     const int most = vector_width(a.bf ? 8 : 4, 1, 0, codes, 3);
     vec = most < vec ? most : vec;
   }
-  const int tensors = 3 + (a.gate.p != nullptr) + (a.other.p != nullptr) + (a.dh.p != nullptr) + (a.extra != nullptr);
-  const bool once = a.rows * a.D * (a.bf ? 2 : 4) * tensors > kCached;
+  // 32 elements of a tensor move 32 elements' bytes, of a checkpoint 33
+  const int whole = 32 * (a.bf ? 2 : 4), kept = a.packed ? kScaleBlock + 1 : whole;
+  const int tensors = 2 + (a.dh.p != nullptr) + (a.extra != nullptr);
+  const int read = 1 + (a.gate.p != nullptr) + (a.other.p != nullptr);
+  const bool once = a.rows * a.D / 32 * (whole * tensors + kept * read) > kCached;
   auto go = [&](auto b, auto k) {
     constexpr bool B = decltype(b)::value, K = decltype(k)::value;
     if (a.bf) {

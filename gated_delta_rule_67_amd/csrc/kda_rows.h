@@ -40,7 +40,7 @@ template <typename T> struct RowVec<T, 1> { typedef T type; };
 template <typename T, int VEC> struct Piece {
   typename RowVec<T, VEC>::type raw;
 
-  // ONCE: past the caches, where a call moves more than they hold (kCached).
+  // ONCE: past the caches (kCached).
   template <bool ONCE = false> __device__ __forceinline__ void load(const void* p, int64_t off) {
     const auto* q = reinterpret_cast<const typename RowVec<T, VEC>::type*>(static_cast<const T*>(p) + off);
     if constexpr (ONCE) raw = __builtin_nontemporal_load(q);
@@ -97,10 +97,13 @@ template <int VEC> struct PackedPiece {
 
   template <bool ONCE = false> __device__ __forceinline__ void load(const Source& s, int64_t off) {
     const uint8_t* c = static_cast<const uint8_t*>(s.p) + off;
+    typedef unsigned two __attribute__((ext_vector_type(2)));
     if constexpr (VEC == 8) {
-      const uint2 v = *reinterpret_cast<const uint2*>(c);
-      word[0] = v.x, word[1] = v.y;
-    } else if constexpr (VEC == 4) word[0] = *reinterpret_cast<const unsigned*>(c);
+      const two* q = reinterpret_cast<const two*>(c);
+      const two v = ONCE ? __builtin_nontemporal_load(q) : *q;
+      word[0] = v[0], word[1] = v[1];
+    } else if constexpr (VEC == 4 && ONCE) word[0] = __builtin_nontemporal_load(reinterpret_cast<const unsigned*>(c));
+    else if constexpr (VEC == 4) word[0] = *reinterpret_cast<const unsigned*>(c);
     else if constexpr (VEC == 2) word[0] = *reinterpret_cast<const unsigned short*>(c);
     else word[0] = *c;
     byte = s.scales[off / kScaleBlock];
@@ -134,10 +137,18 @@ template <int VEC> struct PackedPiece {
   }
 };
 
-// Bytes that the last-level cache holds. A call that moves more reads its tensors past the caches: of
-// prenorm over 2048 columns of bf16 with a residual, 24576 rows (403 MB) take 63 us so and 75 through the
-// caches, 32768 rows 82 and 100; 12288 rows (201 MB), whose inputs may still be there, 35 and 32. The norms
-// store through the caches: past them 32768 rows take 96 us instead of 86.
+// Bytes that the last-level cache holds. A call that moves more reads its tensors past the caches, in its form of
+// whole 16-byte pieces (the narrower forms read through them). What that gains depends on where the outputs are.
+// Past the caches and through them, 32768 rows of 2048 channels in bf16, in us:
+//                                            outputs last written long ago    by the call before
+//   in front of a block                             102 and 102                    86 and 102
+//   behind, under a gate                             74 and  77                    68 and  77
+//   in front, backward                              167 and 168                   157 and 168
+//   behind, backward                                148 and 140                   134 and 141
+//   in front, backward, from checkpoints            154 and 154                   147 and 153
+//   behind, backward, from checkpoints              136 and 133                   132 and 133
+// 12288 rows, whose inputs may still be there, in front of a block 42 and 44, 40 and 40. The norms store through
+// the caches; past them, too, the first case takes 96 us in both places.
 constexpr int64_t kCached = (int64_t)256 << 20;
 
 // What a backward pass reads of the forward's inputs: elements, or a checkpoint of them.
