@@ -65,8 +65,7 @@ template <int VEC> struct FwdTile {
 template <typename T, int VEC, bool CK, bool GATE, bool NORM>
 __global__ __launch_bounds__(64 * (FwdTile<VEC>::kWaves + 1)) void fwd_kernel(GlrArgs a, Chain chain) {
   constexpr int NT = FwdTile<VEC>::kTokens, NW = FwdTile<VEC>::kWaves, kFwdTile = NT * NW, C = 64 * VEC;
-  constexpr unsigned kFull = 0xffffffffu >> (32 - NT);
-  typedef Held<T, VEC, FwdTile<VEC>::kTokens, CK> held;
+  typedef Held<T, VEC, NT, CK> held;
   // Of this turn's tile and of the one before: the spans' maps, which the chain wave replaces by the maps
   // from the tile's front to each span's, and whether a sequence begins in them; the state in front of the
   // tile; the products of decays (the last of a span is in registers too).
