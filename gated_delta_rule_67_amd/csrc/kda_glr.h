@@ -129,7 +129,7 @@ __device__ __forceinline__ float input_weight(float a, float g2, float& inv) {
 //
 // One more wave of the workgroup does this (the chain wave), while the others load their next tile: a wave's loads
 // return in order, so a wave with a tile's loads in flight would see an answer only after them. A workgroup a tile
-// and no such wave: forward 186 us, backward 409, at 4 x 8192 x 2048 bf16, where they take 128 and 270.
+// and no such wave: forward 186 us, backward 409, at 4 x 8192 x 2048 bf16, where they take 127 and 265.
 // Groups of 4, 8 and 16 tiles: forward 141, 139 and 140 us, backward 265, 267 and 271, and from checkpoints,
 // 8192 x 2048, 200, 203 and 229 (all before later steps).
 constexpr int kGroup = 8;

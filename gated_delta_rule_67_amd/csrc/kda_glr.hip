@@ -4,17 +4,19 @@
 //   h_t = a_t h_{t-1} + w_t logistic(in_gate_t) x_t,  w_t = sqrt(1 - a_t^2) or 1;   y_t = h_t
 //
 // 38 instructions of the vector ALU an element, six of them transcendental (which take twice the others'
-// time), and 8 bytes in bf16: the vector ALU is busy 64% of the time, HBM and the last-level cache bring 4.2 TB/s, so the gates are
+// time), and 8 bytes in bf16: the vector ALU is busy 65% of the time, memory moves 4.2 TB/s, so the gates are
 // computed once and every tensor moves once. A wave holds a span of tokens for 64 VEC channels: the states
 // from zero in registers, and in LDS the products of decays with which the state in front of the span
 // enters them. That state comes through the waves of the workgroup and the chain of tiles (kda_glr.h); the
 // chain's waiting is covered by the next tile, whose loads are under way and whose states from zero are
 // computed before the outputs of this one (without any waiting the kernel would take 3 us less).
 //
-// Measured: 128 us at 4 x 8192 tokens of 2048 channels, bf16, with both gates (537 MB; loads and stores
-// alone, of the same sizes in the same order, take 100 us), 79 us at 16391 packed tokens of 1030 channels,
-// float32. Tiles loaded one ahead instead of two: 139 us. y is stored through the caches: the layer's next
-// operator reads it.
+// Measured, calls back to back: 127 us at 4 x 8192 tokens of 2048 channels, bf16, with both gates (537 MB; loads and
+// stores alone, of the same sizes in the same order, take 100 us; with block_states 126 to 129). Traced, kernels
+// apart, 139 and 5.4 for the one that readies the chain. 115 us at 4 x 8192 x 1024, 79 us at 16391 packed tokens of
+// 1030 channels, float32: there rows are 4120 bytes apart, a wave's 256 bytes mostly straddle a third line, and 281 MB
+// are read for 203; the vector ALU is busy 35%. Tiles loaded one ahead instead of two, at an earlier step: 139 us
+// instead of 136 at the first size. y is stored through the caches: the layer's next operator reads it.
 #include <type_traits>
 
 #include "kda_glr.h"
@@ -56,7 +58,7 @@ hipError_t launch_ready(const GlrArgs& a, const Chain& c, const float* from, flo
 // first size above, with one tile ahead: 8 tokens x 15 waves 137 us, x 14 148, x 11 150, x 8 158; 16 x 7 153;
 // four channels a lane, 4 x 15, 220. A checkpoint's codes are a byte each: four channels a lane there keep
 // the loads 4 bytes wide (states of 8192 x 2048 for the backward pass, which takes 144 us with them and 147
-// with two channels a lane).
+// with two channels a lane; 20 bytes a lane go to scratch).
 template <int VEC> struct FwdTile {
   static constexpr int kTokens = VEC == 4 ? 4 : 8, kWaves = 15, kTile = kTokens * kWaves;
   static_assert(kGlrBlock % kTokens == 0, "a block's first token begins a span");

@@ -12,11 +12,13 @@
 // are computed once; what the outputs need of them and nothing in between waits in LDS, the rest in
 // registers, of which a span of 8 tokens takes 156 (163 from checkpoints).
 //
-// Measured: 270 us at 4 x 8192 tokens of 2048 channels, bf16, with both gates (940 MB, 3.5 TB/s); without any
-// waiting for the chain 10 us less. Bound by the gates' and gradients' instructions: 4 tokens x 14 waves 310 us,
-// 8 x 7 309, 8 x 11 272. From checkpoints, 8192 x 2048 in nine sequences: 144 us, of them 57 for the states.
-// The gradients are stored past the caches, which hold none of them until they are read: 267 us at the first
-// size (270 through them), 174 at the second (194, before other steps).
+// Measured, calls back to back: 265 us at 4 x 8192 tokens of 2048 channels, bf16, with both gates and kept states
+// (940 MB, 3.5 TB/s), 396 without those and 416 from checkpoints; 212, 312 and 320 at 4 x 8192 x 1024, float32; from
+// checkpoints, 8192 x 2048 in nine sequences, 145 us, of them 52 and 5 for the states. The vector ALU is busy 57%,
+// 75 instructions an element; beside the vector registers 39 to 81 scalar ones spill into lanes of others. At earlier
+// steps, at the first size: without any waiting for the chain 10 us less; 4 tokens x 14 waves 310 us, 8 x 7 309, 8 x 11
+// 272, against 270; the gradients, which the caches would not hold until they are read, stored past them 267 against
+// 270, and from checkpoints 174 against 194.
 #include <type_traits>
 
 #include "kda_glr.h"

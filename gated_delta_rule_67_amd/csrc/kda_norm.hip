@@ -11,8 +11,9 @@
 // moves what it must (8 bytes an element with a residual in bf16) and is bound by HBM. weight and
 // scale are read once a thread: its columns stay the same over the rows that it works on.
 //
-// Measured in bf16: in front, 32768 rows of 2048 with the residual 86 us (537 MB, 6.3 TB/s, a large copy's
-// rate); behind, 524288 rows of 128 under a gate 66 us (403 MB, 6.1 TB/s); one row 3.1 us, 9.7 with its launch.
+// Measured in bf16, back to back: in front, 32768 rows of 2048 with the residual 102 us (537 MB, 5.3 TB/s; 85 where
+// the outputs' memory is still in the last-level cache from the call before); behind, 524288 rows of 128 under a gate
+// 66 us (403 MB, 6.1 TB/s) into memory that calls reuse, 73 otherwise; one row 3.1 us, 9.7 with its launch.
 #include <type_traits>
 
 #include "kda_norm_tile.h"

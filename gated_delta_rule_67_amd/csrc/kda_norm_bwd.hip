@@ -11,9 +11,12 @@
 // that every tensor moves once and HBM bounds the kernel. A thread keeps its columns over all of its
 // rows and adds dweight and dscale up in registers; workgroups leave partial sums, which a second
 // kernel adds in a fixed order.
-// Measured: behind, 524288 rows of 128 in bf16 under a gate 139 us (671 MB, 4.8 TB/s; the gate's activation is
-// computed twice: kept in registers between its uses, 145 us; 1, 2, 3 and 4 rows at a time 149, 148, 168 and
-// 170 us before loads went past the caches); in front, 5003 rows of 1030 in float32 28.5 us (124 MB).
+// Measured, back to back: behind, 524288 rows of 128 in bf16 under a gate 137 us (671 MB, 4.9 TB/s), 132 and 146 with
+// outputs in the last-level cache and not; from checkpoints 131 and 136. In front, 32768 rows of 2048 in bf16 with
+// residual and scale 156 and 165 us (805 MB), from checkpoints 145 and 153; 5003 rows of 1030 in float32 31 us
+// (124 MB; its kernels, traced, 27 and 4.4). Behind, at an earlier step (139 us): the gate's activation kept in
+// registers between its two uses 145 us; 1, 2, 3 and 4 rows at a time, before loads went past the caches, 149, 148,
+// 168 and 170.
 // v (and the gate, and x in front) may be 8-bit checkpoints: the gradients are those at the values
 // that these stand for, and the tensor moves 33 bytes for every 32 elements.
 #include <type_traits>
@@ -190,7 +193,7 @@ __global__ __launch_bounds__(TILE::BLOCK) void bwd_kernel(NormArgs a) {
 
 // Workgroups of a launch at most: three of 256 threads a CU in one round (their partial sums are
 // written and read once more, 8 bytes a column each). 2, 3, 4, 6 and 8 a CU: 28.5, 28.5, 29.7, 33 and
-// 34.6 us for 5003 rows of 1030.
+// 34.6 us for 5003 rows of 1030, on two sets of buffers in turn (31 us on more).
 constexpr int kBwdBlocks = 3 * 256;
 
 inline int bwd_blocks(int64_t rows, int batch) {

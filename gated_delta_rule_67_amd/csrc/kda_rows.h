@@ -141,7 +141,7 @@ template <int VEC> struct PackedPiece {
 // whole 16-byte pieces (the narrower forms read through them). What that gains depends on where the outputs are.
 // Past the caches and through them, 32768 rows of 2048 channels in bf16, in us:
 //                                            outputs last written long ago    by the call before
-//   in front of a block                             102 and 102                    86 and 102
+//   in front of a block                             102 and 102                    85 and 102
 //   behind, under a gate                             74 and  77                    68 and  77
 //   in front, backward                              167 and 168                   157 and 168
 //   behind, backward                                148 and 140                   134 and 141
