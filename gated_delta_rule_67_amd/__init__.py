@@ -1132,7 +1132,8 @@ def kda_glr_fwd(x, gate_x, A_log, dt_bias=None, in_gate=None, initial_state=None
     wider activation allowed; in_gate None: factor 1), or packed [T,D] / [1,T,D] with cu_seqlens int32
     [N+1]; A_log, dt_bias [D] float32; initial_state [N,D] float32. Returns (y like x, final_state [N,D]
     float32 or None); y rows in no packed sequence are zero. output_block_states: also returns the states
-    [ceil(tokens / 64), D] that kda_glr_bwd takes, so that it need not compute them again."""
+    [ceil(tokens / 64), D] that kda_glr_bwd takes, so that it need not compute them again. The decay is the
+    library's gate, not exp(-c softplus(L) sigmoid(r)) of the published layers with this weight."""
     index, code = _gpu(x)
     lead, N, T = _sequences(x, cu_seqlens, 3, index)
     D = x.shape[-1]
@@ -1158,7 +1159,9 @@ def kda_glr_bwd(x, gate_x, A_log, dy, dt_bias=None, in_gate=None, initial_state=
                 cu_seqlens=None, normalise=True, block_states=None):
     """Gradients of <y, dy> + <final_state, dfinal_state> for kda_glr_fwd's inputs. x, gate_x and in_gate
     may be checkpoints (codes, scales), all of them or none. block_states: as kda_glr_fwd returned them for
-    these inputs, or None: they are computed again. Returns (dx, dgate_x, din_gate, dA_log [D], ddt_bias
+    these inputs, or None: they are computed again. Beside checkpoints leave them None, or give those of a
+    forward pass over kda_checkpoint_unpack's values: with the states of the inputs before they were packed the
+    gradients would belong to neither. Returns (dx, dgate_x, din_gate, dA_log [D], ddt_bias
     [D], dinitial_state [N,D]); din_gate, ddt_bias and dinitial_state are None where their inputs are, and
     rows in no packed sequence are zero."""
     index, code = _gpu(dy)

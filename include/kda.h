@@ -692,7 +692,9 @@ int kda_checkpoint_unpack(const void* codes, const void* scales, void* x, int64_
  *
  *     g_t = -exp(A_log) softplus(gate_x_t + dt_bias),   a_t = exp(g_t)
  *     h_t = a_t h_{t-1} + w_t logistic(in_gate_t) x_t,   y_t = h_t
- * with w_t = sqrt(1 - a_t^2) with KDA_GLR_NORMALISE, else 1.
+ * with w_t = sqrt(1 - a_t^2) with KDA_GLR_NORMALISE, else 1. The decay is this library's gate, not the
+ * exp(-c softplus(L) logistic(r)) of the published layers that this weight is known from: their weights do not
+ * run through it.
  *
  *   x, gate_x, in_gate  [T, D]  dtype, *_stride elements between tokens (>= D, <= 2^24); in_gate may be NULL:
  *                               factor 1
@@ -733,8 +735,9 @@ int kda_glr_fwd(const void* x, int64_t x_stride, const void* gate_x, int64_t gat
  * dx, dgate_x and (where in_gate is given) din_gate [T, D] dtype, dA_log and ddt_bias [D] float32 (either
  * may be NULL), dinitial_state [N, D] float32 (may be NULL). Rows in no sequence are treated as y rows are
  * there. block_states: those that the forward call with the same arguments left, or NULL (they are
- * computed once more). x, gate_x and in_gate may be 8-bit checkpoints, as for kda_prenorm_bwd (the
- * block_states are then best left NULL: those of the unrounded inputs belong to other gradients).
+ * computed once more). x, gate_x and in_gate may be 8-bit checkpoints, as for kda_prenorm_bwd; block_states are
+ * then NULL, or those of a forward call on kda_checkpoint_unpack's values (with those of the unrounded inputs the
+ * gradients would belong to neither).
  * The sums over tokens are taken in a fixed order. workspace: kda_glr_bwd_workspace_size() bytes
  * (kept_states: whether block_states are given), otherwise as kda_glr_fwd.
  */

@@ -73,3 +73,20 @@ def test_no_wait_gives_up(lengths, D, dtype, packed):
                                        int(dt is torch.bfloat16), p(ws), size, s) == 0
                 assert int(ws[1]) == clear
     assert bool(torch.isfinite(dA).all())
+
+
+def test_states_beside_checkpoints():
+    """Block states of a forward pass over the values that checkpoints stand for give the gradients of a call that
+    computes them again, up to their rounding on the way (the same values in float32)."""
+    d = _make([300, 70], 96, torch.float32, 9, rate=-4.0)
+    kept = [kda.kda_checkpoint_pack(d[k]) for k in ("x", "gate_x", "in_gate")]
+    x, r, i = (kda.kda_checkpoint_unpack(*t, torch.float32) for t in kept)
+    states = kda.kda_glr_fwd(x, r, d["A_log"], d["dt_bias"], i, d["init"], d["cu"], output_block_states=True)[2]
+    args = (d["A_log"], d["dy"], d["dt_bias"])
+    rest = (d["init"], d["dfinal"], d["cu"])
+    given = kda.kda_glr_bwd(kept[0], kept[1], *args, kept[2], *rest, block_states=states)
+    again = kda.kda_glr_bwd(kept[0], kept[1], *args, kept[2], *rest)
+    plain = kda.kda_glr_bwd(x, r, *args, i, *rest, block_states=states)
+    for a, b, c in zip(given, again, plain):
+        assert torch.equal(a, c)
+        assert float((a - b).abs().max()) <= 400 * 60 * U * float(c.abs().max())
