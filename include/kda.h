@@ -738,6 +738,7 @@ int kda_glr_fwd(const void* x, int64_t x_stride, const void* gate_x, int64_t gat
  * computed once more). x, gate_x and in_gate may be 8-bit checkpoints, as for kda_prenorm_bwd; block_states are
  * then NULL, or those of a forward call on kda_checkpoint_unpack's values (with those of the unrounded inputs the
  * gradients would belong to neither).
+ * With KDA_GLR_NORMALISE the gradient of gate_x holds x / w_t, w_t from 2^-63 on, in float32: |x| below 2^64.
  * The sums over tokens are taken in a fixed order. workspace: kda_glr_bwd_workspace_size() bytes
  * (kept_states: whether block_states are given), otherwise as kda_glr_fwd.
  */

@@ -90,3 +90,20 @@ def test_states_beside_checkpoints():
     for a, b, c in zip(given, again, plain):
         assert torch.equal(a, c)
         assert float((a - b).abs().max()) <= 400 * 60 * U * float(c.abs().max())
+
+
+@pytest.mark.parametrize("gate", [-200.0, -87.0, -60.0, -3.0])
+def test_large_inputs_under_small_weights(gate):
+    """|x| up to 2^63.9: finite gradients, 0 from a weight of 0; the gate's is that of the oracle."""
+    x = torch.tensor([[2.0 ** 63.9, -2.0 ** 63.9, 1.0, 0.0]], device="cuda")
+    r, A = torch.full_like(x, gate), torch.tensor([0.3] * 4, device="cuda")
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    dx, dr = kda.kda_glr_bwd(x, r, A, torch.ones_like(x), cu_seqlens=cu)[:2]
+    assert bool(torch.isfinite(dx).all() and torch.isfinite(dr).all())
+    if gate == -200.0:
+        assert not dr.any() and not dx.any()
+    elif gate >= -60.0:
+        z, _, a, w, _ = glr_gates(to64(r), to64(A))
+        ref = np.exp(0.3) * to64(x) * a * a / w / (1 + np.exp(-z))
+        # weight, decay and slope within (17 + 2.3 |z|) u each, twice over, and 40 u
+        close(dr, ref, np.abs(ref) * (3 * (17 + 2.3 * abs(gate)) + 40) * U, "dgate_x")
